@@ -51,7 +51,9 @@ typedef enum {
   PKV_FMT_BF16 = 0, /* native: K and V rows are head_dim bf16 values            */
   PKV_FMT_K4V4 = 1, /* K 4-bit codes (Hadamard basis), V 4-bit codes           */
   PKV_FMT_K8V4 = 2, /* K 8-bit codes (Hadamard basis), V 4-bit codes           */
-  PKV_FMT_K8V8 = 3  /* K 8-bit codes (Hadamard basis), V 8-bit codes           */
+  PKV_FMT_K8V8 = 3, /* K 8-bit codes (Hadamard basis), V 8-bit codes           */
+  PKV_FMT_LATENT = 4 /* one bf16 row a token for every head: a latent vector of
+                      * head_dim values, then a position key of group_size values */
 } pkv_format;
 
 typedef enum {
@@ -69,15 +71,15 @@ enum { PKV_KIND_K = 0, PKV_KIND_V = 1, PKV_KIND_KMETA = 2, PKV_KIND_VMETA = 3 };
 
 typedef struct {
   int32_t n_layers;      /* >= 1                                                */
-  int32_t n_kv_heads;    /* 1..8 (one decode consumer warp per kv head)         */
-  int32_t head_dim;      /* 64, 128 or 256                                      */
+  int32_t n_kv_heads;    /* 1..8 (one decode consumer warp per kv head); latent: 1 */
+  int32_t head_dim;      /* 64, 128 or 256; latent: the latent vector's width, 256 or 512 */
   int32_t block_size;    /* tokens per block; must be 32                        */
   int32_t slab_blocks;   /* blocks per slab (POOL_SLAB_BLOCKS); 1..4096, 32 is the default */
   int32_t group_size;    /* values per affine group (ignored for bf16): 32, or 64 for K4/V4 with
                           * head_dim 128 or 256 (one FP32 scale/offset pair per 64 values: five
                           * bits per value, 3.2x against bf16)
                           *   [mlx-swift-lm #142, Summary: K4/V4 at five bits per value,
-                          *    metadata included] */
+                          *    metadata included]; latent: the position key's width, 64 */
   int32_t format;        /* pkv_format                                          */
   int32_t max_slabs;     /* capacity of the slab pointer table (>= 1)           */
   uint64_t hadamard_seed;/* signs s_i = -1 iff top bit of splitmix64(seed + i)  */
@@ -93,7 +95,7 @@ typedef struct {
 
 typedef struct {
   int32_t n_slabs;            /* slabs per (layer, tensor) currently held          */
-  int32_t n_kinds;            /* 2 (bf16) or 4 (packed: K, V, K meta, V meta)      */
+  int32_t n_kinds;            /* 2 (bf16), 4 (packed: K, V, K meta, V meta) or 1 (latent) */
   int64_t slab_append_events; /* slabs appended since create (never a copy)        */
   int64_t rows_capacity;      /* n_slabs * slab_blocks                             */
   int64_t rows_in_use;        /* rows with a nonzero reference count               */
@@ -107,7 +109,8 @@ typedef struct {
  * receives the pool (owned by the caller until pkv_pool_destroy).  Errors:
  * PKV_ERR_INVALID for an unsupported configuration (n_kv_heads outside 1..8,
  * head_dim not 64/128/256, block_size not 32, group_size not allowed for the
- * format), PKV_ERR_CUDA if the device cannot be used.  Synchronous.
+ * format; latent: n_kv_heads not 1, head_dim not 256/512, group_size not 64),
+ * PKV_ERR_CUDA if the device cannot be used.  Synchronous.
  *   [mlxcel #235, Proposed solution, bullet 1: the single pool tensor of a layer
  *    becomes a vector of fixed-size slabs] */
 pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_allocator* alloc, void* stream,
@@ -167,7 +170,8 @@ pkv_status pkv_copy_on_write_block(pkv_pool* pool, int n, const int32_t* src_row
  * Outputs (device): k_out, v_out [n_kv_heads, ctx_len, row_bytes(kind)];
  * kmeta_out, vmeta_out [n_kv_heads, ctx_len, head_dim/group_size, 2] float32,
  * which must be NULL for bf16 and non-NULL for packed (else PKV_ERR_FORMAT);
- * with ctx_len 0 nothing is written and every output may be NULL.
+ * with ctx_len 0 nothing is written and every output may be NULL.  A latent pool has
+ * one stored tensor: its rows go to k_out and the other outputs must be NULL.
  *   [mlxcel #235, touch point 3] */
 pkv_status pkv_gather_visible(pkv_pool* pool, int layer, const int32_t* bt_row_dev, int ctx_len,
                               void* k_out_dev, void* v_out_dev, void* kmeta_out_dev,
@@ -320,8 +324,8 @@ typedef struct {
 pkv_status pkv_price_request(const pkv_pool* pool, const pkv_request* req, pkv_price* out);
 
 /* Storage identity check: PKV_OK if cfg describes the same stored layout as the
- * pool (format, head_dim, n_kv_heads, block_size, slab_blocks, group_size and,
- * for packed formats, hadamard_seed), else PKV_ERR_FORMAT.  Used to reject an
+ * pool (format, head_dim, n_kv_heads, block_size, slab_blocks and, except for bf16,
+ * group_size and, for packed formats, hadamard_seed), else PKV_ERR_FORMAT.  Used to reject an
  * incompatible storage identity before any allocation or copy.
  *   [mlx-swift-lm #142, Summary: a checkpoint of another storage identity is
  *    refused before anything is allocated] */
@@ -395,9 +399,107 @@ pkv_status pkv_export_blocks(pkv_pool* pool, int n, const int32_t* rows_dev, voi
 pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, int n, const int32_t* rows_dev,
                              const void* in_dev, size_t in_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Latent pools (PKV_FMT_LATENT): attention with keys and values from one latent
+ * vector a token, shared by every query head.  R = head_dim (the latent vector),
+ * P = group_size = 64 (the position key, rotated before it is stored).
+ *
+ * Rows, slabs, copy-on-write, gather, block records and pricing work as for the
+ * other formats; write_block and the decode / prefill calls with per-head K/V
+ * return PKV_ERR_FORMAT on a latent pool, and the calls below do so on any other.
+ * The pages describe no such format: the operators are written from the formulas
+ * given with each call.  They require the pool's device to be the current one
+ * (PKV_ERR_INVALID otherwise).  pkv_price_request prices a latent request's
+ * workspace as pkv_latent_workspace_bytes and its q and output rows as R + P and R
+ * values.
+ * --------------------------------------------------------------------------- */
+
+/* write_latent: token i's row goes to (rows_dev[i], slots_dev[i]) of `layer`:
+ *   c' = c * rsqrt(mean(c^2) + eps) * w   (c' = c, copied bit for bit, if
+ *                                          norm_weight is NULL)
+ *   r' = r with each pair (a, b) turned to (a cos t - b sin t, a sin t + b cos t),
+ * and, with Hq > 0, the P position values of token i's query heads turned by the same
+ * angles into q_out.  Pair j is (2j, 2j + 1) when `interleaved`, else (j, j + P/2);
+ * its angle's cosine and sine are cos_sin[positions_dev[i]][j] and [P/2 + j].
+ *   kv_bf16:       [n_tokens] rows of R + P values (c, then r), kv_stride values apart
+ *   positions_dev: [n_tokens] int32, each in [0, n_positions)
+ *   cos_sin:       [n_positions, P] float32, on the device
+ *   norm_weight:   [R] bf16, or NULL
+ *   q_rope, q_out: bf16, head h of token i at i * token_stride + h * head_stride;
+ *                  q_out may be q_rope with the same strides (in place)
+ * Arithmetic in fp32, one rounding to bf16 per stored value.  Pointers 16-byte
+ * aligned; strides in values, non-negative multiples of 8, kv_stride >= R + P; output
+ * rows of q_out at least P apart; 0 <= Hq <= 1024 (else PKV_ERR_INVALID).  Two tokens
+ * with the same (row, slot) leave either one's values.  A row, slot or position out
+ * of range sets the device error word (bit 1, 4 or 16): the row is then not written
+ * and, for a bad position, neither are the token's q_out rows.  n_tokens 0 returns
+ * PKV_OK.  Asynchronous. */
+pkv_status pkv_write_latent(pkv_pool* pool, int layer, int n_tokens, const int32_t* rows_dev,
+                            const int32_t* slots_dev, const void* kv_bf16, int64_t kv_stride,
+                            const int32_t* positions_dev, const float* cos_sin, int n_positions,
+                            const void* norm_weight, float eps, int interleaved, int Hq, const void* q_rope,
+                            int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t out_token_stride,
+                            int64_t out_head_stride, void* stream);
+
+/* Workspace bytes of pkv_paged_latent_attention for batches of B sequences with n_q
+ * queries of Hq heads each (split-K partials; no initialisation needed).  Host only;
+ * the limits are those of that call. */
+pkv_status pkv_latent_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq, size_t* bytes);
+
+/* Absorbed attention over the latent rows themselves, for decode (n_q = 1) and for
+ * several newest tokens of each sequence (n_q > 1: drafted tokens, short chunks):
+ *   x[t] = scale * (q_latent[b,i,h] . c_t + q_rope[b,i,h] . r_t)
+ *   out[b,i,h] = sum_t softmax(x)[t] c_t      over t in [0, ctx_lens[b] - n_q + i]
+ * The caller has multiplied the heads' queries by the key projection, and multiplies
+ * the output by the value projection.
+ *   q_latent, q_rope: bf16 rows (b, i, h) of R and of P values, row (b n_q + i) Hq + h
+ *                     at that many strides (q_latent_stride >= R, q_rope_stride >= P;
+ *                     multiples of 8)
+ *   block_table_dev:  [B, max_blocks] int32 rows; ctx_lens_dev: [B] int32
+ *   out_bf16:         [B, n_q, Hq, R] bf16, contiguous
+ *   workspace:        256-byte aligned, ws_bytes >= pkv_latent_workspace_bytes
+ * A length of 0 (an unused batch slot) gives zero rows.  A negative length, one
+ * beyond max_blocks * 32 or one in (0, n_q) sets the device error word (bit 2) and
+ * gives zero rows; a block-table row outside the pool sets bit 1 (the sequence's
+ * result is then undefined).  Slots past a sequence's length are never read into the
+ * result, whatever they hold.  max_ctx is accepted for interface stability.
+ * Probabilities enter the second product in bf16; sums and softmax state are fp32.
+ * Deterministic.  Limits: B <= 4096, Hq <= 1024, B * n_q * Hq <= 2^24, scale finite,
+ * pointers 16-byte aligned.  B = 0 returns PKV_OK.  Asynchronous. */
+pkv_status pkv_paged_latent_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_latent,
+                                      int64_t q_latent_stride, const void* q_rope, int64_t q_rope_stride,
+                                      const int32_t* block_table_dev, int max_blocks, const int32_t* ctx_lens_dev,
+                                      int max_ctx, float scale, void* out_bf16, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* Workspace bytes of pkv_latent_prefill_attention: the expanded keys and values of B
+ * contexts of at most max_ctx tokens (0 or above max_blocks * 32: max_blocks * 32).
+ * Host only; the limits are those of that call. */
+pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq, int max_blocks,
+                                              int max_ctx, size_t* bytes);
+
+/* Expanded attention, for prompts and long chunks: every visible latent row becomes
+ * per-head keys and values, then ordinary causal attention runs over them:
+ *   k[t,h] = (w_k[h] c_t, r_t)   v[t,h] = w_v[h] c_t
+ *   out[b,i,h] = sum_t softmax(scale * q[b,i,h] . k[t,h])[t] v[t,h]
+ * over t in [0, ctx_lens[b] - n_q + i], for the n_q newest tokens of each sequence
+ * (already written with pkv_write_latent).
+ *   q_bf16:   [B, n_q, Hq, 128 + P], each head's 128 values and then its rotated P
+ *   w_k, w_v: [Hq, 128, R] bf16;  out_bf16: [B, n_q, Hq, 128]
+ *   max_ctx:  bound on ctx_lens (0: max_blocks * 32); a longer context is an error
+ *   workspace: 256-byte aligned, ws_bytes >= pkv_latent_prefill_workspace_bytes of the
+ *              same arguments, not initialised
+ * Lengths, errors, limits, alignment and B = 0 as for pkv_paged_latent_attention,
+ * and max_blocks <= 2^20.  Expanded keys and values and the probabilities are rounded
+ * to bf16 once; sums and softmax state are fp32.  Deterministic.  Asynchronous. */
+pkv_status pkv_latent_prefill_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_bf16,
+                                        const void* w_k, const void* w_v, const int32_t* block_table_dev,
+                                        int max_blocks, const int32_t* ctx_lens_dev, int max_ctx, float scale,
+                                        void* out_bf16, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read and clear the device error word.  PKV_ERR_DEVICE if it
  * was set (bits: 1 row out of range, 2 context too long, 4 slot out of range,
- * 8 wait limit reached); *word_out (optional) receives the bits.  The kernels record
+ * 8 wait limit reached, 16 rotary position out of range); *word_out (optional) receives the bits.  The kernels record
  * errors on the device instead of returning them, so that a decode step needs no
  * host synchronisation; the caller checks when it chooses.
  *   [mlxcel #2171, Implementation Notes: a decode step adds no host sync] */

@@ -19,7 +19,7 @@ import numpy as np
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpkv.so")
 
-FORMATS = {"bf16": 0, "k4v4": 1, "k8v4": 2, "k8v8": 3}
+FORMATS = {"bf16": 0, "k4v4": 1, "k8v4": 2, "k8v8": 3, "latent": 4}
 FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 KIND_K, KIND_V, KIND_KMETA, KIND_VMETA = 0, 1, 2, 3
 
@@ -27,7 +27,8 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "allocation failed", -3: "CUDA er
           -4: "format mismatch", -5: "out of range", -6: "device error word set"}
 PKV_OK, PKV_ERR_INVALID, PKV_ERR_OOM, PKV_ERR_CUDA, PKV_ERR_FORMAT, PKV_ERR_RANGE, PKV_ERR_DEVICE = \
     0, -1, -2, -3, -4, -5, -6
-ERR_ROW, ERR_CTX, ERR_SLOT, ERR_TIMEOUT = 1, 2, 4, 8
+ERR_ROW, ERR_CTX, ERR_SLOT, ERR_TIMEOUT, ERR_POS = 1, 2, 4, 8, 16
+LATENT_HEAD = 128  # values of a head's expanded key (without its position part) and value
 
 
 class PkvError(RuntimeError):
@@ -107,6 +108,12 @@ SIGNATURES = {
     "pkv_block_record_bytes": ([_P, ctypes.POINTER(_SZ)], _I),
     "pkv_export_blocks": ([_P, _I, _P, _P, _SZ, _P], _I),
     "pkv_import_blocks": ([_P, ctypes.POINTER(PoolConfig), _I, _P, _P, _SZ, _P], _I),
+    "pkv_write_latent": ([_P, _I, _I, _P, _P, _P, _I64, _P, _P, _I, _P, _F, _I, _I, _P, _I64, _I64, _P, _I64, _I64,
+                          _P], _I),
+    "pkv_latent_workspace_bytes": ([_P, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "pkv_paged_latent_attention": ([_P, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
+    "pkv_latent_prefill_workspace_bytes": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "pkv_latent_prefill_attention": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
     "pkv_status_string": ([_I], ctypes.c_char_p),
     "pkv_last_error": ([], ctypes.c_char_p),
 }
@@ -165,6 +172,33 @@ def _dev(t, dtype, name: str, shape=None):
     return t.data_ptr()
 
 
+def _dev_strided(t, dtype, name: str, shape):
+    """Like _dev, for a tensor whose last dimension alone has to be contiguous."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def _row_stride(t, name: str) -> int:
+    """The one distance between consecutive rows (every leading dimension) of `t`."""
+    step, rows = None, 1
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1:
+            if step is None:
+                step = st
+            elif st != step * rows:
+                raise ValueError(f"{name}: its rows must be evenly spaced (strides {tuple(t.stride())})")
+        rows *= n
+    return t.shape[-1] if step is None else step
+
+
 def slab_runs(rows, slab_blocks: int = 32) -> np.ndarray:
     """Start index of each maximal same-slab run of a block-table row list (host)."""
     r = np.ascontiguousarray(rows, np.int32)
@@ -187,8 +221,14 @@ class Pool:
 
     def __init__(self, n_layers: int, n_kv_heads: int, head_dim: int, format="bf16", hadamard_seed: int = 0,
                  slab_blocks: int = 32, max_slabs: int = 1024, allocator: Optional[Allocator] = None,
-                 stream=None, group_size: int = 32):
+                 stream=None, group_size: int = 32, rope_dim: Optional[int] = None):
+        """For format "latent", n_kv_heads is 1, head_dim the latent vector's width and
+        rope_dim (default 64) the position key's; the other formats take no rope_dim."""
         self._lib = lib()
+        if FORMATS.get(format, format) == FORMATS["latent"]:
+            group_size = 64 if rope_dim is None else rope_dim
+        elif rope_dim is not None:
+            raise ValueError("rope_dim belongs to the latent format")
         self.cfg = make_config(n_layers, n_kv_heads, head_dim, format, hadamard_seed, slab_blocks, max_slabs,
                                group_size=group_size)
         self.n_layers, self.n_kv_heads, self.head_dim = n_layers, n_kv_heads, head_dim
@@ -383,6 +423,127 @@ class Pool:
             int(block_table.shape[1]), _dev(ctx_lens, torch.int32, "ctx_lens", (B,)), int(max_ctx), float(scale),
             _dev(out, torch.bfloat16, "out", (B, Hq, D)), _stream(stream)), "paged_decode_attention_noalloc")
         return out
+
+    # -- latent pools ----------------------------------------------------------
+    def _latent(self):
+        if self.format != "latent":
+            raise PkvError(PKV_ERR_FORMAT, f"a {self.format} pool has no latent rows")
+        return self.head_dim, int(self.cfg.group_size)
+
+    def write_latent(self, layer: int, rows, slots, kv, positions, cos_sin, norm_weight=None, eps: float = 1e-6,
+                     interleaved: bool = True, q_rope=None, q_out=None, stream=None):
+        """Store token i's row kv[i] = (latent, position key) at (rows[i], slots[i]): the latent
+        normalised (with norm_weight), the position key turned by the angles of positions[i];
+        q_rope [n, Hq, P] is turned by the same angles into q_out (which may be q_rope; a new
+        tensor by default).  kv may have any row stride, q_rope and q_out any token and head
+        strides, in multiples of 8 values.  Returns q_out (None without q_rope)."""
+        torch = _torch()
+        R, P = self._latent()
+        n = int(rows.numel())
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions, P]")
+        kvp = _dev_strided(kv, torch.bfloat16, "kv", (n, R + P))
+        Hq, q, qs, o, os_ = 0, None, (0, 0), None, (0, 0)
+        if q_rope is not None:
+            if q_rope.dim() != 3:
+                raise ValueError("q_rope must be [n, Hq, P]")
+            Hq = int(q_rope.shape[1])
+            if q_out is None:
+                q_out = torch.empty((n, Hq, P), dtype=torch.bfloat16, device=q_rope.device)
+            q, o = (_dev_strided(t, torch.bfloat16, name, (n, Hq, P)) for t, name in ((q_rope, "q_rope"), (q_out, "q_out")))
+            # a dimension of one entry is never stepped over: its stride says nothing
+            qs, os_ = (((t.stride(0) if n > 1 else 0), (t.stride(1) if Hq > 1 else 0)) for t in (q_rope, q_out))
+        elif q_out is not None:
+            raise ValueError("q_out without q_rope")
+        _check(self._lib.pkv_write_latent(
+            self._h, layer, n, _dev(rows, torch.int32, "rows", (n,)), _dev(slots, torch.int32, "slots", (n,)), kvp,
+            int(kv.stride(0)) if n > 1 else R + P, _dev(positions, torch.int32, "positions", (n,)),
+            _dev(cos_sin, torch.float32, "cos_sin", (cos_sin.shape[0], P)), int(cos_sin.shape[0]),
+            None if norm_weight is None else _dev(norm_weight, torch.bfloat16, "norm_weight", (R,)), float(eps),
+            int(bool(interleaved)), Hq, q, *qs, o, *os_, _stream(stream)), "write_latent")
+        return q_out
+
+    def latent_workspace_bytes(self, B: int, n_q: int, Hq: int) -> int:
+        n = _SZ()
+        _check(self._lib.pkv_latent_workspace_bytes(self._h, B, n_q, Hq, ctypes.byref(n)), "latent_workspace_bytes")
+        return int(n.value)
+
+    def paged_latent_attention(self, layer: int, q_latent, q_rope, block_table, ctx_lens, scale: float,
+                               max_ctx: int = 0, out=None, workspace=None, stream=None):
+        """Absorbed attention over the latent rows: q_latent [B, Hq, R] and q_rope [B, Hq, P], or
+        [B, n_q, Hq, .] for the n_q newest tokens of each sequence, any even row stride (views
+        of one [.., R + P] tensor, for instance).  Returns out, shaped as q_latent."""
+        torch = _torch()
+        R, P = self._latent()
+        if q_latent.dim() not in (3, 4):
+            raise ValueError("q_latent must be [B, Hq, R] or [B, n_q, Hq, R]")
+        lead = tuple(q_latent.shape[:-1])
+        B, Hq, n_q = lead[0], lead[-1], (lead[1] if len(lead) == 3 else 1)
+        ql = _dev_strided(q_latent, torch.bfloat16, "q_latent", lead + (R,))
+        qr = _dev_strided(q_rope, torch.bfloat16, "q_rope", lead + (P,))
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [B, max_blocks]")
+        if out is None:
+            out = torch.empty(lead + (R,), dtype=torch.bfloat16, device=q_latent.device)
+        workspace = self._step_workspace(workspace, self.latent_workspace_bytes(B, n_q, Hq), q_latent.device, stream)
+        _check(self._lib.pkv_paged_latent_attention(
+            self._h, layer, B, n_q, Hq, ql, _row_stride(q_latent, "q_latent"), qr, _row_stride(q_rope, "q_rope"),
+            _dev(block_table, torch.int32, "block_table"), int(block_table.shape[1]),
+            _dev(ctx_lens, torch.int32, "ctx_lens", (B,)), int(max_ctx), float(scale),
+            _dev(out, torch.bfloat16, "out", lead + (R,)), workspace.data_ptr(), int(workspace.numel()),
+            _stream(stream)), "paged_latent_attention")
+        return out
+
+    def latent_prefill_workspace_bytes(self, B: int, n_q: int, Hq: int, max_blocks: int, max_ctx: int = 0) -> int:
+        n = _SZ()
+        _check(self._lib.pkv_latent_prefill_workspace_bytes(self._h, B, n_q, Hq, max_blocks, max_ctx, ctypes.byref(n)),
+               "latent_prefill_workspace_bytes")
+        return int(n.value)
+
+    def latent_prefill_attention(self, layer: int, q, w_k, w_v, block_table, ctx_lens, scale: float, max_ctx: int = 0,
+                                 out=None, workspace=None, stream=None):
+        """Expanded causal attention of the n_q newest tokens of each sequence: q [B, n_q, Hq,
+        128 + P], w_k and w_v [Hq, 128, R]; max_ctx bounds ctx_lens and sizes the workspace.
+        Returns out [B, n_q, Hq, 128]."""
+        torch = _torch()
+        R, P = self._latent()
+        D = LATENT_HEAD
+        if q.dim() != 4:
+            raise ValueError("q must be [B, n_q, Hq, 128 + P]")
+        B, n_q, Hq = (int(x) for x in q.shape[:3])
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [B, max_blocks]")
+        mb = int(block_table.shape[1])
+        if out is None:
+            out = torch.empty((B, n_q, Hq, D), dtype=torch.bfloat16, device=q.device)
+        need = self.latent_prefill_workspace_bytes(B, n_q, Hq, mb, int(max_ctx))
+        workspace = self._step_workspace(workspace, need, q.device, stream)
+        _check(self._lib.pkv_latent_prefill_attention(
+            self._h, layer, B, n_q, Hq, _dev(q, torch.bfloat16, "q", (B, n_q, Hq, D + P)),
+            _dev(w_k, torch.bfloat16, "w_k", (Hq, D, R)), _dev(w_v, torch.bfloat16, "w_v", (Hq, D, R)),
+            _dev(block_table, torch.int32, "block_table"), mb, _dev(ctx_lens, torch.int32, "ctx_lens", (B,)),
+            int(max_ctx), float(scale), _dev(out, torch.bfloat16, "out", (B, n_q, Hq, D)), workspace.data_ptr(),
+            int(workspace.numel()), _stream(stream)), "latent_prefill_attention")
+        return out
+
+    @staticmethod
+    def _step_workspace(workspace, nbytes: int, device, stream):
+        """The caller's workspace, or memory of this call alone: two calls on two streams, or in
+        two captured graphs, share none."""
+        torch = _torch()
+        if workspace is not None:
+            if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8 \
+                    or not workspace.is_contiguous():
+                raise TypeError("workspace must be a contiguous CUDA uint8 tensor")
+            return workspace
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if stream is not None:
+            # made on the current stream, used on another
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+            if s != torch.cuda.current_stream():
+                s.wait_stream(torch.cuda.current_stream())
+                workspace.record_stream(s)
+        return workspace
 
     # -- introspection -------------------------------------------------------
     def stats(self) -> dict:

@@ -22,6 +22,7 @@
 #include <string>
 #include <vector>
 
+#include "latent.cuh"
 #include "pkv_internal.cuh"
 
 using namespace pkv;
@@ -140,11 +141,14 @@ static bool encode_group_maps(const pkv_pool* p, uint8_t* group, std::vector<CUt
                                     : box == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
       // 3-D view [column block][token][W bytes] of the [token][row] tensor: one copy
-      // moves 16 tokens of the whole row and lands as nx boxes of 16 x W bytes.
+      // moves 16 tokens of the whole row and lands as nx boxes of 16 x W bytes.  A
+      // latent pool's kernels take one column block of a 32-token block at a time.
       const cuuint64_t nx = (cuuint64_t)(row / box);
       const cuuint64_t dims[3] = {(cuuint64_t)box, (cuuint64_t)p->cfg.slab_blocks * kBlockTokens, nx};
       const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)box};
-      const cuuint32_t boxd[3] = {(cuuint32_t)box, 16u, (cuuint32_t)nx};
+      const bool latent = p->cfg.format == PKV_FMT_LATENT;
+      const cuuint32_t boxd[3] = {(cuuint32_t)box, latent ? (cuuint32_t)kBlockTokens : 16u,
+                                  latent ? 1u : (cuuint32_t)nx};
       const cuuint32_t estr[3] = {1u, 1u, 1u};
       if (enc(&maps[(size_t)l * K + k], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, group + off, dims, strides, boxd, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -178,14 +182,17 @@ pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_allocator* allo
   *out = nullptr;
   const FormatBits fb = format_bits(cfg->format);
   const int D = cfg->head_dim;
-  if (fb.k == 0 || cfg->n_layers < 1 || cfg->n_kv_heads < 1 || cfg->n_kv_heads > 8 ||
-      !(D == 64 || D == 128 || D == 256) || cfg->block_size != kBlockTokens || cfg->slab_blocks < 1 ||
-      cfg->slab_blocks > 4096 || cfg->max_slabs < 1)
+  const bool latent = cfg->format == PKV_FMT_LATENT;
+  if (latent && (cfg->n_kv_heads != 1 || cfg->group_size != kRope || !(D == 256 || D == 512)))
+    return PKV_ERR_INVALID;
+  if ((!latent && (fb.k == 0 || !(D == 64 || D == 128 || D == 256))) || cfg->n_layers < 1 || cfg->n_kv_heads < 1 ||
+      cfg->n_kv_heads > 8 || cfg->block_size != kBlockTokens || cfg->slab_blocks < 1 || cfg->slab_blocks > 4096 ||
+      cfg->max_slabs < 1)
     return PKV_ERR_INVALID;
   // Groups of 32 for every packed format; groups of 64 (the five-bit K4/V4 layout)
   // for K4/V4 with head_dim >= 128, so a (token, head) metadata row stays a whole
   // number of 16-byte chunks.
-  if (cfg->format != PKV_FMT_BF16 && cfg->group_size != kGroup &&
+  if (!latent && cfg->format != PKV_FMT_BF16 && cfg->group_size != kGroup &&
       !(cfg->group_size == kGroupWide && cfg->format == PKV_FMT_K4V4 && D >= 128))
     return PKV_ERR_INVALID;
   if (alloc && (!alloc->alloc || !alloc->release)) return PKV_ERR_INVALID;
@@ -212,9 +219,9 @@ pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_allocator* allo
   if (e != cudaSuccess) return fail(cuda_fail(e, "cudaDeviceGetAttribute(smem)"));
   p->smem_optin = (size_t)optin;
 
-  p->n_kinds = (cfg->format == PKV_FMT_BF16) ? 2 : 4;
-  p->row_bytes[PKV_KIND_K] = (int64_t)D * fb.k / 8;
-  p->row_bytes[PKV_KIND_V] = (int64_t)D * fb.v / 8;
+  p->n_kinds = latent ? 1 : (cfg->format == PKV_FMT_BF16) ? 2 : 4;
+  p->row_bytes[PKV_KIND_K] = latent ? (int64_t)(D + kRope) * 2 : (int64_t)D * fb.k / 8;
+  p->row_bytes[PKV_KIND_V] = latent ? 0 : (int64_t)D * fb.v / 8;
   if (p->n_kinds == 4) {
     p->row_bytes[PKV_KIND_KMETA] = (int64_t)(D / cfg->group_size) * 2 * sizeof(float);
     p->row_bytes[PKV_KIND_VMETA] = p->row_bytes[PKV_KIND_KMETA];
@@ -411,6 +418,7 @@ int pkv_slab_runs(const int32_t* rows, int n, int slab_blocks, int32_t* run_star
 pkv_status pkv_write_block(pkv_pool* p, int layer, int n, const int32_t* rows, const int32_t* slots,
                            const void* k, const void* v, void* stream) {
   if (!p || n < 0 || layer < 0 || layer >= p->cfg.n_layers) return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   if (n == 0) return PKV_OK;
   if (!rows || !slots || !k || !v) return PKV_ERR_INVALID;
   if (((uintptr_t)k & 15u) != 0 || ((uintptr_t)v & 15u) != 0) return PKV_ERR_INVALID;
@@ -496,8 +504,9 @@ pkv_status pkv_gather_visible(pkv_pool* p, int layer, const int32_t* bt_row, int
   if (!p || layer < 0 || layer >= p->cfg.n_layers || ctx < 0) return PKV_ERR_INVALID;
   if (ctx == 0) return PKV_OK;  // nothing visible; output pointers may be NULL
   const bool packed = p->n_kinds == 4;
-  if (packed != (kmeta_out != nullptr) || packed != (vmeta_out != nullptr)) return PKV_ERR_FORMAT;
-  if (!bt_row || !k_out || !v_out) return PKV_ERR_INVALID;
+  const bool latent = p->n_kinds == 1;  // one stored tensor
+  if (packed != (kmeta_out != nullptr) || packed != (vmeta_out != nullptr) || (latent && v_out)) return PKV_ERR_FORMAT;
+  if (!bt_row || !k_out || (!latent && !v_out)) return PKV_ERR_INVALID;
   for (void* o : {k_out, v_out, kmeta_out, vmeta_out})
     if (((uintptr_t)o & 15u) != 0) return PKV_ERR_INVALID;
   cudaStream_t s = (cudaStream_t)stream;
@@ -520,6 +529,7 @@ static size_t workspace_bytes(const pkv_pool* p, int B, int Hq) {
 pkv_status pkv_decode_workspace_bytes(const pkv_pool* p, int B, int Hq, int max_ctx, size_t* bytes) {
   (void)max_ctx;
   if (!p || !bytes || B < 0 || Hq < 1) return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   *bytes = workspace_bytes(p, B, Hq);
   return PKV_OK;
 }
@@ -535,6 +545,7 @@ static pkv_status decode_impl(pkv_pool* p, int layer, int B, int Hq, const void*
                               void* stream, int kv_reuse, int nq) {
   if (!p || layer < 0 || layer >= p->cfg.n_layers || B < 0 || Hq < 1 || max_blocks < 0)
     return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   if (B == 0) return PKV_OK;
   const int hkv = p->cfg.n_kv_heads;
   if (Hq % hkv) return PKV_ERR_INVALID;
@@ -635,6 +646,7 @@ static void prefill_layout(const pkv_pool* p, int B, int n_q, int Hq, int max_bl
 pkv_status pkv_prefill_workspace_bytes(const pkv_pool* p, int B, int n_q, int Hq, int max_blocks, size_t* bytes) {
   if (!p || !bytes || B < 0 || n_q < 1 || Hq < 1 || max_blocks < 0 || (int64_t)B * n_q > 4096)
     return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   size_t a, b, c;
   prefill_layout(p, B, n_q, Hq, max_blocks, &a, &b, &c, bytes);
   return PKV_OK;
@@ -647,6 +659,7 @@ pkv_status pkv_paged_prefill_attention(pkv_pool* p, int layer, int B, int n_q, i
   if (!p || layer < 0 || layer >= p->cfg.n_layers || B < 0 || n_q < 1 || Hq < 1 || max_blocks < 0 ||
       (int64_t)B * n_q > 4096)
     return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   if (B == 0) return PKV_OK;
   if (Hq % p->cfg.n_kv_heads) return PKV_ERR_INVALID;
   const int G = Hq / p->cfg.n_kv_heads;
@@ -684,6 +697,174 @@ pkv_status pkv_paged_prefill_attention(pkv_pool* p, int layer, int B, int n_q, i
                      ws_bytes - dec_off, stream, 1, nq);
 }
 
+// ---------------------------------------------------------------------------
+// Latent pools
+// ---------------------------------------------------------------------------
+
+// What every latent entry point checks first: a latent pool, the layer, and the
+// pool's device as the current one (the kernels launch there).
+static pkv_status latent_check(const pkv_pool* p, int layer) {
+  if (!p || layer < 0 || layer >= p->cfg.n_layers) return PKV_ERR_INVALID;
+  if (p->cfg.format != PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  int dev = -1;
+  PKV_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev != p->device) return PKV_ERR_INVALID;
+  return PKV_OK;
+}
+
+static bool misaligned(const void* ptr, uintptr_t a) { return ((uintptr_t)ptr & (a - 1)) != 0; }
+
+pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, const int32_t* slots, const void* kv,
+                            int64_t kv_stride, const int32_t* positions, const float* cos_sin, int n_positions,
+                            const void* norm_weight, float eps, int interleaved, int Hq, const void* q_rope,
+                            int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t out_token_stride,
+                            int64_t out_head_stride, void* stream) {
+  pkv_status st = latent_check(p, layer);
+  if (st != PKV_OK) return st;
+  const int R = p->cfg.head_dim;
+  if (n < 0 || Hq < 0 || Hq > kLatentMaxHeads || n_positions < 0) return PKV_ERR_INVALID;
+  if (n == 0) return PKV_OK;
+  if (!rows || !slots || !kv || !positions || !cos_sin) return PKV_ERR_INVALID;
+  if (misaligned(kv, 16) || misaligned(cos_sin, 16) || misaligned(norm_weight, 16) || misaligned(q_rope, 16) ||
+      misaligned(q_out, 16))
+    return PKV_ERR_INVALID;
+  if (kv_stride < R + kRope || kv_stride % 8) return PKV_ERR_INVALID;
+  if (norm_weight && !(std::isfinite(eps) && eps >= 0.f)) return PKV_ERR_INVALID;
+  if (Hq > 0) {
+    if (!q_rope || !q_out) return PKV_ERR_INVALID;
+    for (int64_t x : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
+      if (x < 0 || x % 8) return PKV_ERR_INVALID;
+    // output rows must not overlap one another
+    if ((Hq > 1 && out_head_stride < kRope) || (n > 1 && out_token_stride < kRope)) return PKV_ERR_INVALID;
+  }
+  LatentWriteArgs a;
+  a.lv = layer_view(p, layer);
+  a.R = R;
+  a.n = n;
+  a.rows = rows;
+  a.slots = slots;
+  a.kv = (const uint16_t*)kv;
+  a.kv_stride = kv_stride;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.n_pos = n_positions;
+  a.weight = (const uint16_t*)norm_weight;
+  a.eps = eps;
+  a.interleaved = interleaved != 0;
+  a.Hq = Hq;
+  a.q = (const uint16_t*)q_rope;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.qo = (uint16_t*)q_out;
+  a.o_tok = out_token_stride;
+  a.o_head = out_head_stride;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_latent_write(a), "write_latent launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
+static bool latent_sizes_ok(int B, int n_q, int Hq) {
+  return B >= 0 && B <= kLatentMaxBatch && n_q >= 1 && Hq >= 1 && Hq <= kLatentMaxHeads &&
+         (int64_t)B * n_q * Hq <= kLatentMaxRows;
+}
+
+pkv_status pkv_latent_workspace_bytes(const pkv_pool* p, int B, int n_q, int Hq, size_t* bytes) {
+  if (!p || !bytes || !latent_sizes_ok(B, n_q, Hq)) return PKV_ERR_INVALID;
+  if (p->cfg.format != PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  *bytes = latent_attn_workspace(p->cfg.head_dim, B, n_q, Hq, decode_grid(p));
+  return PKV_OK;
+}
+
+pkv_status pkv_paged_latent_attention(pkv_pool* p, int layer, int B, int n_q, int Hq, const void* q_latent,
+                                      int64_t q_latent_stride, const void* q_rope, int64_t q_rope_stride,
+                                      const int32_t* bt, int max_blocks, const int32_t* ctx, int max_ctx, float scale,
+                                      void* out, void* ws, size_t ws_bytes, void* stream) {
+  (void)max_ctx;
+  pkv_status st = latent_check(p, layer);
+  if (st != PKV_OK) return st;
+  const int R = p->cfg.head_dim;
+  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || !std::isfinite(scale)) return PKV_ERR_INVALID;
+  if (B == 0) return PKV_OK;
+  if (!q_latent || !q_rope || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
+  if (q_latent_stride < R || q_latent_stride % 8 || q_rope_stride < kRope || q_rope_stride % 8) return PKV_ERR_INVALID;
+  if (misaligned(q_latent, 16) || misaligned(q_rope, 16) || misaligned(out, 16) || misaligned(ws, 256))
+    return PKV_ERR_INVALID;
+  LatentAttnArgs a;
+  a.ctas = decode_grid(p);
+  if (ws_bytes < latent_attn_workspace(R, B, n_q, Hq, a.ctas)) return PKV_ERR_INVALID;
+  a.lv = layer_view(p, layer);
+  a.R = R;
+  a.B = B;
+  a.n_q = n_q;
+  a.Hq = Hq;
+  a.max_blocks = max_blocks;
+  a.ql = (const uint16_t*)q_latent;
+  a.ql_stride = q_latent_stride;
+  a.qr = (const uint16_t*)q_rope;
+  a.qr_stride = q_rope_stride;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.out = (uint16_t*)out;
+  a.ws = ws;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_latent_attn(a), "paged_latent_attention launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
+// The bound on context lengths that the expanded form's workspace is sized by.
+static int latent_prefill_ctx(int max_blocks, int max_ctx) {
+  const int64_t all = (int64_t)max_blocks * kBlockTokens;
+  return (int)(max_ctx > 0 && max_ctx < all ? max_ctx : all);
+}
+
+pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* p, int B, int n_q, int Hq, int max_blocks, int max_ctx,
+                                              size_t* bytes) {
+  if (!p || !bytes || !latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || max_ctx < 0)
+    return PKV_ERR_INVALID;
+  if (p->cfg.format != PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  *bytes = latent_prefill_workspace(B, Hq, latent_prefill_ctx(max_blocks, max_ctx));
+  return PKV_OK;
+}
+
+pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, int Hq, const void* q, const void* w_k,
+                                        const void* w_v, const int32_t* bt, int max_blocks, const int32_t* ctx,
+                                        int max_ctx, float scale, void* out, void* ws, size_t ws_bytes, void* stream) {
+  pkv_status st = latent_check(p, layer);
+  if (st != PKV_OK) return st;
+  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || max_ctx < 0 ||
+      !std::isfinite(scale))
+    return PKV_ERR_INVALID;
+  if (B == 0) return PKV_OK;
+  if (!q || !w_k || !w_v || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
+  if (misaligned(q, 16) || misaligned(w_k, 16) || misaligned(w_v, 16) || misaligned(out, 16) || misaligned(ws, 256))
+    return PKV_ERR_INVALID;
+  LatentPrefillArgs a;
+  a.max_ctx = latent_prefill_ctx(max_blocks, max_ctx);
+  if (ws_bytes < latent_prefill_workspace(B, Hq, a.max_ctx)) return PKV_ERR_INVALID;
+  a.lv = layer_view(p, layer);
+  a.R = p->cfg.head_dim;
+  a.B = B;
+  a.n_q = n_q;
+  a.Hq = Hq;
+  a.max_blocks = max_blocks;
+  a.q = (const uint16_t*)q;
+  a.wk = (const uint16_t*)w_k;
+  a.wv = (const uint16_t*)w_v;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.out = (uint16_t*)out;
+  a.ws = ws;
+  a.ctas = p->n_sm;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_latent_prefill(a), "latent_prefill_attention launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
 pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price* out) {
   if (!p || !r || !out || r->new_blocks < 0 || r->B < 1 || r->Hq < 1 || r->n_q < 1 || r->max_blocks < 0)
     return PKV_ERR_INVALID;
@@ -700,9 +881,12 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
   out->free_rows = free_rows;
   out->storage_bytes = (uint64_t)slabs * (uint64_t)p->group_bytes;
   out->page_bytes = (uint64_t)r->new_blocks * (uint64_t)block_bytes * (uint64_t)p->cfg.n_layers;
-  out->fixed_bytes = (uint64_t)r->max_blocks * 4u + 4u + 2ull * (uint64_t)r->n_q * (uint64_t)r->Hq *
-                                                          (uint64_t)p->cfg.head_dim * 2u;
-  if (r->n_q == 1) {
+  const bool latent = p->cfg.format == PKV_FMT_LATENT;
+  const uint64_t q_out = 2ull * (uint64_t)p->cfg.head_dim + (latent ? kRope : 0);  // values of a q and an output row
+  out->fixed_bytes = (uint64_t)r->max_blocks * 4u + 4u + (uint64_t)r->n_q * (uint64_t)r->Hq * q_out * 2u;
+  if (latent) {
+    out->workspace_bytes = latent_attn_workspace(p->cfg.head_dim, r->B, r->n_q, r->Hq, decode_grid(p));
+  } else if (r->n_q == 1) {
     out->workspace_bytes = workspace_bytes(p, r->B, r->Hq);
   } else {
     size_t a, b, c, t;
@@ -739,8 +923,8 @@ pkv_status pkv_pool_check_identity(const pkv_pool* p, const pkv_pool_config* c) 
   const pkv_pool_config& a = p->cfg;
   bool same = a.format == c->format && a.head_dim == c->head_dim && a.n_kv_heads == c->n_kv_heads &&
               a.block_size == c->block_size && a.slab_blocks == c->slab_blocks;
-  if (a.format != PKV_FMT_BF16)
-    same = same && a.group_size == c->group_size && a.hadamard_seed == c->hadamard_seed;
+  if (a.format != PKV_FMT_BF16) same = same && a.group_size == c->group_size;
+  if (a.format != PKV_FMT_BF16 && a.format != PKV_FMT_LATENT) same = same && a.hadamard_seed == c->hadamard_seed;
   return same ? PKV_OK : PKV_ERR_FORMAT;
 }
 
