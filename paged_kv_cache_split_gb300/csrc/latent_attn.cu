@@ -1,74 +1,743 @@
-// latent_attn.cu — absorbed attention over a latent pool.
+// latent_attn.cu — absorbed attention over a latent pool, on the tensor cores.
+//
+//   x[t, n] = scale (ql[n] . c_t + qr[n] . r_t)        n: a row (query, head) of a sequence
+//   o[n]    = sum_t exp2(x[t, n] - m[n]) c_t / sum_t exp2(x[t, n] - m[n])
+//
+// Every token's row of R + 64 values is read once and used twice, as a key by all rows
+// and as a value (its first R).  With H rows a token costs 2 H (2R + 64) operations and
+// 2 (R + 64) bytes: at H = 128 both sides of the roofline take about as long, below that
+// HBM bounds.
+//
+// Layout.  Both products have the tokens, or the latent's dims, as the MMA's M and the
+// rows as its N, so the head count sets N (16, 32 or 64 rows a tile; more rows take more
+// tiles) and small head counts waste nothing:
+//   S^T [64 tokens x N] = K [64 x (R + 64)] Q^T      K as it lies in shared memory
+//   O^T [R x N]        += V^T [R x 64] P^T [64 x N]  the same bytes, read MN-major
+// O^T stays in tensor memory (R / 128 blocks of N columns), S^T is double-buffered there.
+//
+// A CTA runs one warp that issues copies, one that issues MMAs and four for the softmax.
+// Cache rows arrive by TMA in boxes of 32 tokens x 64 values into a ring of 16 KB slots
+// (64 tokens x 128 latent values) and one of 8 KB slots (64 tokens' position keys); the
+// next tile's S^T product runs while the softmax works on this one, and a slot is refilled
+// as soon as its block of O^T has been added to.  The softmax reference m moves only when
+// a logit passes it by more than 2^8 (all rescaling of O^T is skipped otherwise): p is
+// then at most 2^8 and loses nothing in bf16, and the sums are FP32.
+//
+// Tiles of every sequence are laid end to end and split evenly over groups of CTAs (one
+// CTA per row tile in a group).  A sequence inside one CTA's share is written directly; a
+// split one leaves FP32 records that a second kernel merges in order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "latent.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+constexpr int kTile = 64;             // tokens a tile
+constexpr int kSoftmaxThreads = 128;  // warps 0..3
+constexpr int kThreads = 192;         // + warp 4: copies, warp 5: MMAs
+constexpr int kChunkBytes = kTile * 128;      // 64 tokens x 64 values: one swizzled box column
+constexpr int kPairBytes = 2 * kChunkBytes;   // 64 tokens x 128 latent values
+constexpr int kBlockBytes = kBlockTokens * 128;  // what one copy moves: 32 tokens x 64 values
+constexpr float kSlack = 8.0f;        // log2 of how far a logit may pass the reference
+constexpr float kNoMax = -1e30f;      // the reference before any visible token
+constexpr int kSmemLimit = 232448;    // 227 KB opt-in shared memory per block
+constexpr int kSmall = 3072;          // alignment (1024), barriers and per-row values
 
-// One warp per query row (b, i, h): lane l holds dims l, l + 32, ... of q and of the
-// output; a token costs one dot product, five shuffles and an online-softmax step.
-template <int R>
-__global__ void __launch_bounds__(256) latent_attn_simple_kernel(const LatentAttnArgs a) {
-  constexpr int E = R / 32, EP = kRope / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (row >= (int64_t)a.B * a.n_q * a.Hq) return;
-  const int b = (int)(row / ((int64_t)a.n_q * a.Hq));
-  const int i = (int)(row / a.Hq % a.n_q);
+// Cost of a sequence's start in quarter tiles, in the split over the CTAs: its queries are
+// loaded and its output or record written.
+constexpr int kSegCost = 8;
+constexpr int kCost = 4;
+
+// Ring sizes: the next tile's S^T product needs its whole tile while this tile's latent
+// slots are still held, so two tiles at least; what is left of shared memory goes to more.
+template <int R, int N>
+struct Plan {
+  static constexpr int kPairs = R / 128;  // latent slots a tile
+  static constexpr int kQBytes = N * (R + kRope) * 2;
+  static constexpr int kPBytes = N * 128;
+  static constexpr int kRoom = kSmemLimit - kSmall - kQBytes - kPBytes;
+  static constexpr int kTileBytes = kPairs * kPairBytes + kChunkBytes;
+  static constexpr int kRopeSlots =
+      kRoom / kTileBytes + (kRoom % kTileBytes >= kPairBytes + kChunkBytes ? 1 : 0);
+  static constexpr int kPairSlots = (kRoom - kRopeSlots * kChunkBytes) / kPairBytes;
+  static constexpr int kSmem = kSmall + kQBytes + kPBytes + kPairSlots * kPairBytes + kRopeSlots * kChunkBytes;
+  static constexpr int kTmemUsed = (2 + kPairs) * N;  // two S^T buffers, O^T
+  static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kPairSlots >= 2 * kPairs && kRopeSlots >= 2, "two tiles have to fit");
+  static_assert(kSmem <= kSmemLimit && kTmemUsed <= 512, "shared memory or TMEM");
+};
+
+struct Params {
+  LatentAttnArgs a;
+  int rows;     // n_q * Hq: rows of a sequence
+  int n_rt;     // row tiles of a sequence
+  int groups;   // CTAs along the token axis (each with n_rt row tiles)
+  int2* meta;   // [B][n_rt]: first record slot of a split sequence (-1: written directly), last group
+  float2* ml;   // [2 * grid][N]: reference and sum of a record's rows
+  float* acc;   // [2 * grid][N][R]
+};
+
+// Tokens that the last (most) of tile rt's rows sees, 0 for an unused or bad sequence.
+template <int N>
+__device__ __forceinline__ int32_t visible(const Params& P, int b, int rt, int32_t* len) {
   bool bad;
-  const int32_t L = latent_ctx(a.ctx[b], (int64_t)a.max_blocks * kBlockTokens, a.n_q, &bad);
-  if (bad && lane == 0) atomicOr(a.lv.err, ERR_CTX);
-  const int32_t vis = L == 0 ? 0 : L - a.n_q + i + 1;
-  float q[E + EP], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = bf(a.ql[row * a.ql_stride + lane + 32 * e]), acc[e] = 0.f;
-#pragma unroll
-  for (int e = 0; e < EP; ++e) q[E + e] = bf(a.qr[row * a.qr_stride + lane + 32 * e]);
-  float m = -INFINITY, l = 0.f;
-  for (int32_t t = 0; t < vis; ++t) {
-    const int32_t r = a.bt[(int64_t)b * a.max_blocks + t / kBlockTokens];
-    if (!latent_row_ok(a.lv, r)) {
-      if (lane == 0) atomicOr(a.lv.err, ERR_ROW);
-      continue;
+  const int32_t L =
+      latent_ctx(__ldg(P.a.ctx + b), (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
+  *len = L;
+  if (L == 0) return 0;
+  const int last = min(P.rows, (rt + 1) * N) - 1;
+  return L - P.a.n_q + last / P.a.Hq + 1;
+}
+
+// A CTA's share of the tiles.  Tile k of sequence b, the u-th of all, sits at position
+// kCost u + kSegCost (b + 1); group g holds the positions [g V, (g + 1) V).  V is at least
+// kCost, so the groups that hold a sequence's tiles are consecutive.
+struct Segment {
+  int b, len, vis;   // sequence, its length, tokens the last row sees
+  int k0, k1, n;     // this CTA's tiles of it, and all of them
+};
+
+struct Walk {
+  int b;
+  int64_t up;      // tiles before sequence b
+  int64_t lo, hi;  // positions of this CTA
+
+  template <int N>
+  __device__ __forceinline__ bool next(const Params& P, int rt, Segment& s) {
+    while (b < P.a.B) {
+      const int64_t base = kCost * up + (int64_t)kSegCost * (b + 1);
+      if (base >= hi) return false;
+      s.b = b;
+      s.vis = visible<N>(P, b, rt, &s.len);
+      s.n = (s.vis + kTile - 1) / kTile;
+      const int64_t f = base >= lo ? 0 : (lo - base + kCost - 1) / kCost;
+      const int64_t e = (hi - base + kCost - 1) / kCost;
+      s.k0 = (int)(f < s.n ? f : s.n);
+      s.k1 = (int)(e < s.n ? e : s.n);
+      up += s.n;
+      ++b;
+      if (s.k1 > s.k0) return true;
     }
-    const uint16_t* kv = reinterpret_cast<const uint16_t*>(latent_row(a.lv, r, t % kBlockTokens));
-    float c[E], s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = bf(kv[lane + 32 * e]), s += q[e] * c[e];
-#pragma unroll
-    for (int e = 0; e < EP; ++e) s += q[E + e] * bf(kv[R + lane + 32 * e]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float k = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * k + p;
-    m = mn;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * k + p * c[e];
+    return false;
   }
-  const float inv = vis > 0 ? 1.f / l : 0.f;
+};
+
+// One warp: the CTA's positions and the sequence its walk starts at.
+template <int N>
+__device__ __forceinline__ Walk start_walk(const Params& P, int rt, int group) {
+  const int lane = threadIdx.x & 31;
+  int32_t len;
+  int64_t total = 0;
+  for (int base = 0; base < P.a.B; base += 32) {
+    const int b = base + lane;
+    total += b < P.a.B ? (visible<N>(P, b, rt, &len) + kTile - 1) / kTile : 0;
+  }
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[row * R + lane + 32 * e] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  Walk w;
+  const int64_t v = (kCost * total + (int64_t)kSegCost * P.a.B + P.groups - 1) / P.groups;
+  const int64_t V = v > kCost ? v : kCost;
+  w.lo = group * V;
+  w.hi = w.lo + V;
+  w.b = P.a.B;
+  w.up = total;
+  int64_t carry = 0;
+  for (int base = 0; base < P.a.B; base += 32) {
+    const int b = base + lane;
+    const int64_t n = b < P.a.B ? (visible<N>(P, b, rt, &len) + kTile - 1) / kTile : 0;
+    int64_t inc = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += y;
+    }
+    // the first sequence whose last tile reaches the CTA's first position
+    const unsigned hit = __ballot_sync(
+        0xffffffffu, b < P.a.B && kCost * (carry + inc - 1) + (int64_t)kSegCost * (b + 1) >= w.lo);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      w.b = base + l;
+      w.up = carry + __shfl_sync(0xffffffffu, inc - n, l);
+      break;
+    }
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return w;
+}
+
+// Shared-memory state besides the operands.
+template <int R, int N>
+struct Small {
+  using L = Plan<R, N>;
+  uint64_t pair_full[L::kPairSlots], pair_empty[L::kPairSlots];
+  uint64_t rope_full[L::kRopeSlots], rope_empty[L::kRopeSlots];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, drain;
+  Walk walk;
+  uint32_t tmem;
+  int dead;          // a wait gave up: every role runs on without waiting or issuing
+  int vis[N];        // tokens each row sees
+  float fac[N];      // per row: rescale factor, or 1 / sum
+  float part[4][N];  // per warp: maxima, or sums
+};
+
+// Waits are bounded.  The first one to give up sets the error word and `dead`; after that
+// no wait blocks and nothing more is issued, so every thread still meets every barrier.
+__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
+  if (mbar_try_wait(bar, parity) || *dead) return;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      if (*dead) return;
+      if (global_timer_ns() - t0 > 1000000000ull) {
+        atomicOr(err, ERR_TIMEOUT);
+        *dead = 1;
+        return;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+__device__ __forceinline__ bool softmax_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+template <int R, int N>
+__global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ Params P) {
+  using L = Plan<R, N>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* pairs = smem;
+  uint8_t* ropes = pairs + L::kPairSlots * kPairBytes;
+  uint8_t* qs = ropes + L::kRopeSlots * kChunkBytes;
+  uint8_t* ps = qs + L::kQBytes;
+  Small<R, N>& sm = *reinterpret_cast<Small<R, N>*>(ps + L::kPBytes);
+  static_assert(sizeof(Small<R, N>) <= kSmall - 1024, "small state");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = blockIdx.x % P.n_rt, group = blockIdx.x / P.n_rt;
+  volatile int* dead = &sm.dead;
+  int32_t* err = P.a.lv.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kPairSlots; ++i) mbar_init(&sm.pair_full[i], 1), mbar_init(&sm.pair_empty[i], 1);
+    for (int i = 0; i < L::kRopeSlots; ++i) mbar_init(&sm.rope_full[i], 1), mbar_init(&sm.rope_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1), mbar_init(&sm.s_free[i], kSoftmaxThreads);
+    mbar_init(&sm.p_full, kSoftmaxThreads);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.q_full, kSoftmaxThreads);
+    mbar_init(&sm.drain, 1);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tc_alloc(&sm.tmem, L::kTmem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 0) {
+    const Walk w = start_walk<N>(P, rt, group);
+    if (lane == 0) sm.walk = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
+  Walk walk = sm.walk;
+  Segment seg;
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    const int tid = threadIdx.x;
+    const int c2 = 2 * (lane & 3), tq = lane >> 2;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    float m[N / 4], l[N / 4];
+    int it = 0;
+    while (walk.next<N>(P, rt, seg)) {
+      const int row0 = rt * N, nrow = min(N, P.rows - row0);
+      // The queries of the tile, in chunks of 64 values, swizzled as the copies are.
+      constexpr int CH = (R + kRope) / 8;
+      const int64_t qrow = (int64_t)seg.b * P.rows + row0;
+      for (int i = tid; i < N * CH; i += kSoftmaxThreads) {
+        const int r = i / CH, ch = i - r * CH;
+        const bool ok = r < nrow;
+        const uint16_t* src = !ok            ? P.a.ql
+                              : ch < R / 8   ? P.a.ql + (qrow + r) * P.a.ql_stride + ch * 8
+                                             : P.a.qr + (qrow + r) * P.a.qr_stride + (ch - R / 8) * 8;
+        cp_async16(smem_u32(qs) + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, ok);
+      }
+      if (tid < N) {
+        const int r = min(row0 + tid, P.rows - 1);
+        sm.vis[tid] = seg.len - P.a.n_q + r / P.a.Hq + 1;
+      }
+      const int vis_first = seg.len - P.a.n_q + row0 / P.a.Hq + 1;
+      cp_async_wait_all();
+      fence_async_shared();
+      mbar_arrive(&sm.q_full);
+      softmax_any(false);  // sm.vis is ready
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) m[k] = kNoMax, l[k] = 0.f;
+
+      for (int u = seg.k0; u < seg.k1; ++u, ++it) {
+        const int buf = it & 1;
+        wait_or_die(&sm.s_full[buf], (it >> 1) & 1, dead, err);
+        tc_fence_after();
+        float x[N / 2];
+        {
+          uint32_t r[N / 2];
+          tc_ld_frag16<N>(tm_s + buf * N + lanes, r);
+          tc_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&sm.s_free[buf]);
+#pragma unroll
+          for (int k = 0; k < N / 2; ++k) x[k] = __uint_as_float(r[k]) * P.a.scale_log2;
+        }
+        if ((u + 1) * kTile > vis_first) {
+          const int t0 = u * kTile + 16 * warp + tq;
+#pragma unroll
+          for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int v = sm.vis[8 * j + c2 + e];
+              if (t0 >= v) x[4 * j + e] = -INFINITY;
+              if (t0 + 8 >= v) x[4 * j + 2 + e] = -INFINITY;
+            }
+        }
+        float over = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            over = fmaxf(over, fmaxf(x[4 * j + e], x[4 * j + 2 + e]) - m[2 * j + e]);
+        const bool raise = softmax_any(over > kSlack);
+        if (it > 0) {
+          wait_or_die(&sm.pv_done, (it - 1) & 1, dead, err);
+          tc_fence_after();
+        }
+        if (raise) {
+          float cm[N / 4];
+#pragma unroll
+          for (int k = 0; k < N / 4; ++k) {
+            cm[k] = fmaxf(x[4 * (k >> 1) + (k & 1)], x[4 * (k >> 1) + 2 + (k & 1)]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) cm[k] = fmaxf(cm[k], __shfl_xor_sync(0xffffffffu, cm[k], off));
+            if (lane < 4) sm.part[warp][8 * (k >> 1) + c2 + (k & 1)] = cm[k];
+          }
+          softmax_any(false);
+#pragma unroll
+          for (int k = 0; k < N / 4; ++k) {
+            const int col = 8 * (k >> 1) + c2 + (k & 1);
+            const float mn = fmaxf(fmaxf(fmaxf(sm.part[0][col], sm.part[1][col]), fmaxf(sm.part[2][col], sm.part[3][col])), m[k]);
+            const float f = ex2(m[k] - mn);
+            m[k] = mn;
+            l[k] *= f;
+            if (warp == 0 && lane < 4) sm.fac[col] = f;
+          }
+          softmax_any(false);
+          if (u > seg.k0) {
+#pragma unroll 1
+            for (int mb = 0; mb < L::kPairs; ++mb)
+#pragma unroll 1
+              for (int q = 0; q < N; q += 16) {
+                uint32_t o[16];
+                const uint32_t at = tm_o + mb * N + q + lanes;
+                tc_ld_rows<16>(at, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sm.fac[q + i]);
+                tc_st_rows<16>(at, o);
+              }
+            tc_wait_st();
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * j + e;
+            x[4 * j + e] = ex2(x[4 * j + e] - m[k]);
+            x[4 * j + 2 + e] = ex2(x[4 * j + 2 + e] - m[k]);
+            l[k] += x[4 * j + e] + x[4 * j + 2 + e];
+          }
+        // P [N rows][64 tokens]: fragments (8 tokens x 8 rows) stored transposed.
+        const int i8 = lane & 7, quad = lane >> 3;
+#pragma unroll
+        for (int j = 0; j < N / 8; j += 2) {
+          const int r = 8 * (j + (quad >> 1)) + i8, chunk = 2 * warp + (quad & 1);
+          const uint32_t dst = smem_u32(ps) + r * 128 + ((chunk ^ (r & 7)) << 4);
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                       "r"(bf2(x[4 * j], x[4 * j + 1])), "r"(bf2(x[4 * j + 2], x[4 * j + 3])),
+                       "r"(bf2(x[4 * j + 4], x[4 * j + 5])), "r"(bf2(x[4 * j + 6], x[4 * j + 7]))
+                       : "memory");
+        }
+        // Slots past the last visible token hold anything (0 x NaN is NaN): their values
+        // become zero; their keys only reached logits that were masked.
+        const int valid = seg.vis - u * kTile;
+        if (valid < kTile) {
+          const int per = (kTile - valid) * 8;  // 16-byte pieces of a chunk
+          for (int i = tid; i < per * 2 * L::kPairs; i += kSoftmaxThreads) {
+            const int ch = i / per, w = i - ch * per;
+            const int slot = (int)(((unsigned)it * L::kPairs + (ch >> 1)) % L::kPairSlots);
+            *reinterpret_cast<uint4*>(pairs + slot * kPairBytes + (ch & 1) * kChunkBytes + valid * 128 + w * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_shared();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full);
+      }
+      // Output of the segment: O^T / sum, or a record (reference, sum, O^T) to be merged.
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+        if (lane < 4) sm.part[warp][8 * (k >> 1) + c2 + (k & 1)] = l[k];
+        if (warp == 0 && lane < 4) sm.fac[8 * (k >> 1) + c2 + (k & 1)] = m[k];
+      }
+      softmax_any(false);
+      const bool whole = seg.k0 == 0 && seg.k1 == seg.n;
+      // record slot: the CTA's first or its last segment (any between is whole)
+      const bool first_seg = seg.k0 > 0 || it == seg.k1 - seg.k0;
+      const size_t slot = 2 * (size_t)blockIdx.x + (first_seg ? 0 : 1);
+      if (tid == 0) {
+        int2* meta = P.meta + (size_t)seg.b * P.n_rt + rt;
+        if (seg.k0 == 0) meta->x = whole ? -1 : (int)slot;
+        if (seg.k1 == seg.n) meta->y = group;
+      }
+      if (tid < N) {
+        const float s = sm.part[0][tid] + sm.part[1][tid] + sm.part[2][tid] + sm.part[3][tid];
+        if (whole)
+          sm.fac[tid] = 1.f / s;
+        else
+          P.ml[slot * N + tid] = make_float2(sm.fac[tid], s);
+      }
+      softmax_any(false);
+      wait_or_die(&sm.pv_done, (it - 1) & 1, dead, err);
+      tc_fence_after();
+#pragma unroll 1
+      for (int mb = 0; mb < L::kPairs; ++mb)
+#pragma unroll 1
+        for (int q = 0; q < nrow; q += 16) {
+          uint32_t o[16];
+          tc_ld_rows<16>(tm_o + mb * N + q + lanes, o);
+          tc_wait_ld();
+          const int d = mb * 128 + tid;
+          if (whole) {
+            uint16_t* out = P.a.out + (qrow + q) * R + d;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (q + i < nrow)
+                out[(int64_t)i * R] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(o[i]) * sm.fac[q + i]));
+          } else {
+            float* out = P.acc + (slot * N + q) * R + d;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (q + i < nrow) out[i * R] = __uint_as_float(o[i]);
+          }
+        }
+      tc_fence_before();
+      softmax_any(false);  // sm.fac, sm.part and sm.vis are free again
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------------ copies
+    const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    uint32_t np = 0, nr = 0;  // slots used so far
+    while (walk.next<N>(P, rt, seg)) {
+      const int nblk = (seg.vis + kBlockTokens - 1) / kBlockTokens;
+      for (int ub = seg.k0; ub < seg.k1; ub += 16) {
+        // lane l looks up block 2 ub + l of the sequence and issues its copies
+        const int j = 2 * ub + lane;
+        const uint8_t* map = nullptr;
+        int y0 = 0;
+        if (j < nblk && j < 2 * seg.k1) {
+          const int32_t row = P.a.bt[(int64_t)seg.b * P.a.max_blocks + j];
+          if (latent_row_ok(P.a.lv, row)) {
+            const int32_t slab = row / P.a.lv.slab_blocks;
+            y0 = (row - slab * P.a.lv.slab_blocks) * kBlockTokens;
+            map = P.a.lv.tab.base[(size_t)slab * P.a.lv.tab.stride] + P.a.lv.map_delta;
+            tensormap_acquire(map);
+          } else {
+            atomicOr(err, ERR_ROW);
+          }
+        }
+        const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
+        const int ue = min(ub + 16, seg.k1);
+        for (int u = ub; u < ue; ++u) {
+          const int i = u - ub;
+          const bool mine = (lane >> 1) == i && map;
+          const int blocks = __popc((have >> (2 * i)) & 3u);
+          const int half = (lane & 1) * kBlockBytes;
+          {
+            const uint32_t slot = nr % L::kRopeSlots, round = nr / L::kRopeSlots;
+            if (round > 0) wait_or_die(&sm.rope_empty[slot], (round - 1) & 1, dead, err);
+            if (__any_sync(0xffffffffu, *dead)) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[slot], blocks * kBlockBytes);
+            __syncwarp();
+            if (mine) tma_load_3d(ropes + slot * kChunkBytes + half, map, 0, y0, R / 64, &sm.rope_full[slot], policy);
+            ++nr;
+          }
+          bool stop = false;
+          for (int p = 0; p < L::kPairs; ++p) {
+            const uint32_t slot = np % L::kPairSlots, round = np / L::kPairSlots;
+            if (round > 0) wait_or_die(&sm.pair_empty[slot], (round - 1) & 1, dead, err);
+            stop = __any_sync(0xffffffffu, *dead);
+            if (stop) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.pair_full[slot], 2 * blocks * kBlockBytes);
+            __syncwarp();
+            if (mine) {
+              uint8_t* dst = pairs + slot * kPairBytes + half;
+              tma_load_3d(dst, map, 0, y0, 2 * p, &sm.pair_full[slot], policy);
+              tma_load_3d(dst + kChunkBytes, map, 0, y0, 2 * p + 1, &sm.pair_full[slot], policy);
+            }
+            ++np;
+          }
+          if (stop) break;
+        }
+      }
+    }
+    // no copy may be in flight when the CTA ends
+    for (uint32_t i = np > L::kPairSlots ? np - L::kPairSlots : 0; i < np; ++i)
+      mbar_wait_bounded(&sm.pair_full[i % L::kPairSlots], (i / L::kPairSlots) & 1, err);
+    for (uint32_t i = nr > L::kRopeSlots ? nr - L::kRopeSlots : 0; i < nr; ++i)
+      mbar_wait_bounded(&sm.rope_full[i % L::kRopeSlots], (i / L::kRopeSlots) & 1, err);
+  } else if (lane == 0) {
+    // -------------------------------------------------------------------- MMAs
+    constexpr uint32_t id_s = tc_idesc(64, N, false, false);
+    constexpr uint32_t id_o = tc_idesc(128, N, true, false);
+    const uint64_t d_rope = tc_desc(smem_u32(ropes), 16, 1024), d_pair = tc_desc(smem_u32(pairs), 16, 1024);
+    const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_p = tc_desc(smem_u32(ps), 16, 1024);
+    const uint64_t d_v = tc_desc(smem_u32(pairs), kChunkBytes, 1024);
+    int it = 0, n_seg = 0;
+    bool pending = false, pending_first = false;
+    // O^T (+)= V^T P^T of tile i
+    auto add_values = [&](int i, bool first) {
+      wait_or_die(&sm.p_full, i & 1, dead, err);
+      if (*dead) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int mb = 0; mb < L::kPairs; ++mb) {
+        const uint32_t slot = ((uint32_t)i * L::kPairs + mb) % L::kPairSlots;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma(tm_o + mb * N, d_v + ((slot * kPairBytes + k * 2048) >> 4), d_p + ((k * 32) >> 4), id_o,
+                 !(first && k == 0));
+        tc_commit(&sm.pair_empty[slot]);
+      }
+      tc_commit(&sm.pv_done);
+    };
+    while (walk.next<N>(P, rt, seg)) {
+      for (int u = seg.k0; u < seg.k1; ++u, ++it) {
+        const bool first = u == seg.k0;
+        if (first) {
+          if (pending) add_values(it - 1, pending_first);
+          pending = false;
+          wait_or_die(&sm.q_full, n_seg & 1, dead, err);
+          ++n_seg;
+        }
+        const int buf = it & 1;
+        if (it >= 2) wait_or_die(&sm.s_free[buf], ((it >> 1) - 1) & 1, dead, err);
+        const uint32_t rslot = (uint32_t)it % L::kRopeSlots, rround = (uint32_t)it / L::kRopeSlots;
+        wait_or_die(&sm.rope_full[rslot], rround & 1, dead, err);
+        if (!*dead) {
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tm_s + buf * N, d_rope + ((rslot * kChunkBytes + k * 32) >> 4),
+                   d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
+          tc_commit(&sm.rope_empty[rslot]);
+        }
+#pragma unroll 1
+        for (int p = 0; p < L::kPairs; ++p) {
+          const uint32_t idx = (uint32_t)it * L::kPairs + p, slot = idx % L::kPairSlots;
+          wait_or_die(&sm.pair_full[slot], (idx / L::kPairSlots) & 1, dead, err);
+          if (*dead) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma(tm_s + buf * N, d_pair + ((slot * kPairBytes + (k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
+                   d_q + (((2 * p + (k >> 2)) * N * 128 + (k & 3) * 32) >> 4), id_s, true);
+        }
+        if (!*dead) tc_commit(&sm.s_full[buf]);
+        if (pending) add_values(it - 1, pending_first);
+        pending = true;
+        pending_first = first;
+      }
+    }
+    if (pending) add_values(it - 1, pending_first);
+    tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
+    mbar_wait_bounded(&sm.drain, 0, err);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tc_dealloc(tmem, L::kTmem);
+}
+
+// Merge of the records of split sequences: one CTA per row, its warps taking the records
+// in turn, then the warps' sums in order.  Also the zero rows of unused or bad sequences.
+template <int R, int N>
+__global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_constant__ Params P) {
+  constexpr int V = R / 128;  // float4 per lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t row = blockIdx.x;
+  const int b = (int)(row / P.rows), r = (int)(row % P.rows);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool bad;
+  const int32_t L = latent_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
+  uint16_t* out = P.a.out + row * R;
+  if (L == 0) {
+    if (bad && r == 0 && threadIdx.x == 0) atomicOr(P.a.lv.err, ERR_CTX);
+    for (int i = threadIdx.x; i < R / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int rt = r / N, rr = r % N;
+  const int2 meta = P.meta[(size_t)b * P.n_rt + rt];
+  if (meta.x < 0) return;
+  // records: the first in slot meta.x, then slot 0 of every later group's CTA
+  const int g0 = (meta.x >> 1) / P.n_rt, n = meta.y - g0 + 1;
+  auto slot_of = [&](int i) -> size_t {
+    return i == 0 ? (size_t)meta.x : 2 * ((size_t)(g0 + i) * P.n_rt + rt);
+  };
+  float M = kNoMax;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, P.ml[slot_of(i) * N + rr].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float s = 0.f;
+  float4 acc[V] = {};
+  constexpr int U = 4;  // records in flight
+  for (int i0 = warp; i0 < n; i0 += 4 * U) {
+    float4 v[U][V];
+    float w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + 4 * k;
+      w[k] = 0.f;
+      if (i < n) {
+        const size_t at = slot_of(i) * N + rr;
+        const float2 ml = P.ml[at];
+        w[k] = ex2(ml.x - M);
+        s += w[k] * ml.y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = reinterpret_cast<const float4*>(P.acc + at * R)[lane + 32 * e];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i0 + 4 * k < n) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          acc[e].x += w[k] * v[k][e].x;
+          acc[e].y += w[k] * v[k][e].y;
+          acc[e].z += w[k] * v[k][e].z;
+          acc[e].w += w[k] * v[k][e].w;
+        }
+      }
+  }
+  __shared__ float4 sh[4][32 * V];
+  __shared__ float shs[4];
+#pragma unroll
+  for (int e = 0; e < V; ++e) sh[warp][lane + 32 * e] = acc[e];
+  if (lane == 0) shs[warp] = s;
+  __syncthreads();
+  if (threadIdx.x < 32 * V) {
+    const float inv = 1.f / (shs[0] + shs[1] + shs[2] + shs[3]);
+    const float4 a = sh[0][threadIdx.x], c = sh[1][threadIdx.x], d = sh[2][threadIdx.x], e = sh[3][threadIdx.x];
+    const uint2 o = make_uint2(bf2((a.x + c.x + d.x + e.x) * inv, (a.y + c.y + d.y + e.y) * inv),
+                               bf2((a.z + c.z + d.z + e.z) * inv, (a.w + c.w + d.w + e.w) * inv));
+    reinterpret_cast<uint2*>(out)[threadIdx.x] = o;
+  }
+}
+
+// Rows a tile: the smallest of 16, 32 and 64 that holds all of a sequence's.
+struct Geometry {
+  int rows, N, n_rt, groups;
+  size_t meta, ml, total;  // workspace offsets
+};
+
+Geometry geometry(int R, int B, int n_q, int Hq, int ctas) {
+  Geometry g;
+  g.rows = n_q * Hq;
+  g.N = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : 64;
+  g.n_rt = (g.rows + g.N - 1) / g.N;
+  g.groups = ctas / g.n_rt > 1 ? ctas / g.n_rt : 1;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t slots = 2 * (size_t)g.groups * g.n_rt;
+  g.meta = up(sizeof(int2) * (size_t)B * g.n_rt);
+  g.ml = g.meta + up(sizeof(float2) * slots * g.N);
+  g.total = g.ml + sizeof(float) * slots * g.N * R;
+  return g;
+}
+
+template <typename K>
+cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, const Params& P) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = P.a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P);
+}
+
+template <int R, int N>
+cudaError_t launch_rn(const Params& P) {
+  static_assert(sizeof(Params) <= 4096, "kernel parameters");
+  cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<R, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Plan<R, N>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch(latent_attn_kernel<R, N>, (unsigned)(P.groups * P.n_rt), kThreads, Plan<R, N>::kSmem, P);
+  if (e != cudaSuccess) return e;
+  return launch(latent_combine_kernel<R, N>, (unsigned)((int64_t)P.a.B * P.rows), 128, 0, P);
 }
 
 }  // namespace
 
-size_t latent_attn_workspace(int R, int B, int n_q, int Hq, int ctas) { return 256; }
+size_t latent_attn_workspace(int R, int B, int n_q, int Hq, int ctas) {
+  return geometry(R, B, n_q, Hq, ctas).total;
+}
 
 cudaError_t launch_latent_attn(const LatentAttnArgs& a) {
-  const int64_t rows = (int64_t)a.B * a.n_q * a.Hq;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
-  if (a.R == 512)
-    latent_attn_simple_kernel<512><<<grid, 256, 0, a.stream>>>(a);
-  else
-    latent_attn_simple_kernel<256><<<grid, 256, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  const Geometry g = geometry(a.R, a.B, a.n_q, a.Hq, a.ctas);
+  Params P;
+  P.a = a;
+  P.rows = g.rows;
+  P.n_rt = g.n_rt;
+  P.groups = g.groups;
+  P.meta = reinterpret_cast<int2*>(a.ws);
+  P.ml = reinterpret_cast<float2*>((uint8_t*)a.ws + g.meta);
+  P.acc = reinterpret_cast<float*>((uint8_t*)a.ws + g.ml);
+  if (a.R == 512) {
+    if (g.N == 16) return launch_rn<512, 16>(P);
+    if (g.N == 32) return launch_rn<512, 32>(P);
+    return launch_rn<512, 64>(P);
+  }
+  if (g.N == 16) return launch_rn<256, 16>(P);
+  if (g.N == 32) return launch_rn<256, 32>(P);
+  return launch_rn<256, 64>(P);
 }
 
 }  // namespace pkv
