@@ -5,6 +5,8 @@
 // vector c (R values) followed by a position key r (kRope values), in bf16.
 #pragma once
 
+#include <cuda.h>
+
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -78,6 +80,10 @@ struct LatentPrefillArgs {
   cudaStream_t stream;
 };
 size_t latent_prefill_workspace(int B, int Hq, int max_ctx);
+// A bf16 tensor map of `rank` dimensions (dims[0] contiguous, strides in bytes from the
+// second on), read in boxes with the 128-byte swizzle; false if the driver refuses it.
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a);
 
 // Address of one token's row, and whether a block-table entry names a pool row.

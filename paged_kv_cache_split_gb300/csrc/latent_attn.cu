@@ -183,34 +183,6 @@ struct Small {
   float part[4][N];  // per warp: maxima, or sums
 };
 
-// Waits are bounded.  The first one to give up sets the error word and `dead`; after that
-// no wait blocks and nothing more is issued, so every thread still meets every barrier.
-__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
-  if (mbar_try_wait(bar, parity) || *dead) return;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if ((it & 63u) == 0) {
-      if (*dead) return;
-      if (global_timer_ns() - t0 > 1000000000ull) {
-        atomicOr(err, ERR_TIMEOUT);
-        *dead = 1;
-        return;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-
 __device__ __forceinline__ bool softmax_any(bool p) {
   uint32_t r;
   asm volatile(

@@ -1,104 +1,568 @@
-// latent_prefill.cu — expanded attention over a latent pool.
+// latent_prefill.cu — expanded attention over a latent pool, on the tensor cores: an
+// expansion of the latent rows to per-head keys and values, then causal attention.
 //
-// The latent rows of every sequence are expanded to per-head keys and values in the
-// workspace ([B, Hq, max_ctx, kLatentHead] each, bf16), then ordinary causal attention
-// runs over (k, r) and v.
+//   k[t, h] = (Wk[h] c_t, r_t),  v[t, h] = Wv[h] c_t
+//   o[i, h] = sum_t exp2(x - m) v[t, h] / sum_t exp2(x - m),  x = scale q[i, h] . k[t, h]
+//
+// Both kernels are bound by the tensor cores: the expansion takes 512 R operations per
+// token and head, the attention 640 per (query, key, head).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "latent.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int DH = kLatentHead;
+constexpr int kTile = 128;               // tokens (keys) a tile, queries a tile
+constexpr int kSlot = kTile * 128;       // 128 rows x 64 values: one swizzled box column
+constexpr int kBlockBytes = kBlockTokens * 128;
+constexpr int kSmall = 3072;             // alignment (1024) and barriers
+constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
+constexpr float kNoMax = -1e30f;
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+struct Params {
+  LatentPrefillArgs a;
+  int T;                // tokens per (sequence, head) in the workspace: max_ctx rounded up to a tile
+  int heads_per_cta;    // expansion
+  int pairs;            // query tile pairs a sequence (attention)
+  float scale;          // |scale| log2(e)
+  int negative;         // scale < 0
+  uint16_t* k;          // [B, Hq, T, DH]
+  uint16_t* v;
+  CUtensorMap wk_map, wv_map, q_map, k_map, v_map;
+};
 
-// One thread per expanded value.
-__global__ void __launch_bounds__(256) latent_expand_simple_kernel(const LatentPrefillArgs a, uint16_t* ko, uint16_t* vo) {
-  const int d = threadIdx.x & 127, kind = threadIdx.x >> 7;
-  const int h = blockIdx.y, b = blockIdx.z;
+__device__ __forceinline__ int32_t context(const Params& P, int b, bool* bad) {
+  const int64_t all = (int64_t)P.a.max_blocks * kBlockTokens;
+  return latent_ctx(__ldg(P.a.ctx + b), all < P.a.max_ctx ? all : (int64_t)P.a.max_ctx, P.a.n_q, bad);
+}
+
+// Block j of sequence b: its tensor map (null outside the pool) and first row in it.
+__device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int j, int* y0) {
+  const int32_t row = P.a.bt[(int64_t)b * P.a.max_blocks + j];
+  if (!latent_row_ok(P.a.lv, row)) {
+    atomicOr(P.a.lv.err, ERR_ROW);
+    return nullptr;
+  }
+  const int32_t slab = row / P.a.lv.slab_blocks;
+  *y0 = (row - slab * P.a.lv.slab_blocks) * kBlockTokens;
+  const uint8_t* map = P.a.lv.tab.base[(size_t)slab * P.a.lv.tab.stride] + P.a.lv.map_delta;
+  tensormap_acquire(map);
+  return map;
+}
+
+// ---------------------------------------------------------------------------
+// Expansion: [128 tokens x R] x [R x 256] per head (128 key values, 128 value values).
+// The tokens' latents stay in shared memory while the CTA goes over its heads, so only
+// the weights stream (from L2, through a ring of 64-wide k-chunks); two accumulators of
+// 256 columns let the epilogue of one head run under the products of the next.
+// ---------------------------------------------------------------------------
+constexpr int kExpandThreads = 192;  // warps 0..3 epilogue, 4 copies, 5 MMAs
+constexpr int kWStages = 3;
+constexpr int kWStage = 2 * kSlot;
+
+template <int R>
+struct ExpandSmall {
+  uint64_t a_full[R / 64], w_full[kWStages], w_empty[kWStages], d_full[2], d_free[2], drain;
+  uint32_t tmem;
+  int dead;
+};
+
+template <int R>
+__global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* as = smem;
+  uint8_t* ws = as + (R / 64) * kSlot;
+  ExpandSmall<R>& sm = *reinterpret_cast<ExpandSmall<R>*>(ws + kWStages * kWStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* dead = &sm.dead;
+  int32_t* err = P.a.lv.err;
+  const int tile = blockIdx.x, b = blockIdx.z;
+  const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(P.a.Hq, h0 + P.heads_per_cta);
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   bool bad;
-  const int64_t lim = min((int64_t)a.max_blocks * kBlockTokens, (int64_t)a.max_ctx);
-  const int32_t L = latent_ctx(a.ctx[b], lim, a.n_q, &bad);
-  if (bad && threadIdx.x == 0) atomicOr(a.lv.err, ERR_CTX);
-  const uint16_t* w = (kind ? a.wv : a.wk) + ((int64_t)h * DH + d) * a.R;
-  uint16_t* o = kind ? vo : ko;
-  for (int t = blockIdx.x; t < L; t += gridDim.x) {
-    const int32_t r = a.bt[(int64_t)b * a.max_blocks + t / kBlockTokens];
-    float s = 0.f;
-    if (latent_row_ok(a.lv, r)) {
-      const uint16_t* c = reinterpret_cast<const uint16_t*>(latent_row(a.lv, r, t % kBlockTokens));
-      for (int e = 0; e < a.R; ++e) s += bf(c[e]) * bf(w[e]);
-    } else if (d == 0) {
-      atomicOr(a.lv.err, ERR_ROW);
+  const int32_t L = context(P, b, &bad);
+  if (tile * kTile >= L) return;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R / 64; ++i) mbar_init(&sm.a_full[i], 1);
+    for (int i = 0; i < kWStages; ++i) mbar_init(&sm.w_full[i], 1), mbar_init(&sm.w_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_free[i], 128);
+    mbar_init(&sm.drain, 1);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) tc_alloc(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  constexpr int C = R / 64;  // k-chunks
+
+  if (warp < 4) {
+    const int t = tile * kTile + threadIdx.x;
+    const int partner = t ^ 1;
+    for (int h = h0, n = 0; h < h1; ++h, ++n) {
+      wait_or_die(&sm.d_full[n & 1], (n >> 1) & 1, dead, err);
+      tc_fence_after();
+      const int64_t base = ((int64_t)b * P.a.Hq + h) * P.T;
+      // Pairs of lanes exchange 16-byte pieces so that each store of the pair fills a
+      // 32-byte sector of one row.
+      const bool odd = lane & 1;
+#pragma unroll 1
+      for (int q = 0; q < 8; ++q) {
+        uint32_t r[32];
+        tc_ld_rows<32>(tmem + (n & 1) * 256 + q * 32 + ((uint32_t)(warp * 32) << 16), r);
+        tc_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = t < L ? bf2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
+        uint16_t* dst = (q < 4 ? P.k : P.v) + (q & 3) * 32;
+        uint4* own = reinterpret_cast<uint4*>(dst + (base + t) * DH);
+        uint4* other = reinterpret_cast<uint4*>(dst + (base + partner) * DH);
+        uint4* even_row = odd ? other : own;
+        uint4* odd_row = odd ? own : other;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t got[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            got[i] = __shfl_xor_sync(0xffffffffu, odd ? w[8 * p + i] : w[8 * p + 4 + i], 1);
+          const uint4 g = make_uint4(got[0], got[1], got[2], got[3]);
+          const uint4 lo = make_uint4(w[8 * p], w[8 * p + 1], w[8 * p + 2], w[8 * p + 3]);
+          const uint4 hi = make_uint4(w[8 * p + 4], w[8 * p + 5], w[8 * p + 6], w[8 * p + 7]);
+          even_row[2 * p + odd] = odd ? g : lo;
+          odd_row[2 * p + odd] = odd ? hi : g;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.d_free[n & 1]);
     }
-    o[(((int64_t)b * a.Hq + h) * a.max_ctx + t) * DH + d] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+  } else if (warp == 4) {
+    // lane l < 4 copies block l of the tile
+    const uint64_t keep = l2_policy_evict_normal();
+    const int j = tile * (kTile / kBlockTokens) + lane;
+    int y0 = 0;
+    const uint8_t* map = lane < 4 && j * kBlockTokens < L ? block_map(P, b, j, &y0) : nullptr;
+    const int blocks = __popc(__ballot_sync(0xffffffffu, map != nullptr));
+    uint32_t nw = 0, na = 0;
+    for (int h = h0; h < h1; ++h)
+      for (int c = 0; c < C; ++c) {
+        if (h == h0) {
+          na = c + 1;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.a_full[c], blocks * kBlockBytes);
+          __syncwarp();
+          if (map) tma_load_3d(as + c * kSlot + lane * kBlockBytes, map, 0, y0, c, &sm.a_full[c], keep);
+        }
+        const uint32_t s = nw % kWStages, round = nw / kWStages;
+        if (round > 0) wait_or_die(&sm.w_empty[s], (round - 1) & 1, dead, err);
+        if (__any_sync(0xffffffffu, *dead)) {
+          h = h1;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.w_full[s], kWStage);
+          tma_load_2d(ws + s * kWStage, &P.wk_map, c * 64, h * DH, &sm.w_full[s], keep);
+          tma_load_2d(ws + s * kWStage + kSlot, &P.wv_map, c * 64, h * DH, &sm.w_full[s], keep);
+        }
+        ++nw;
+      }
+    for (uint32_t i = nw > kWStages ? nw - kWStages : 0; i < nw; ++i)
+      mbar_wait_bounded(&sm.w_full[i % kWStages], (i / kWStages) & 1, err);
+    for (uint32_t c = 0; c < na; ++c) mbar_wait_bounded(&sm.a_full[c], 0, err);
+  } else if (lane == 0) {
+    constexpr uint32_t id = tc_idesc(128, 256, false, false);
+    const uint64_t d_a = tc_desc(smem_u32(as), 16, 1024), d_w = tc_desc(smem_u32(ws), 16, 1024);
+    uint32_t nw = 0;
+    for (int h = h0, n = 0; h < h1; ++h, ++n) {
+      if (n >= 2) wait_or_die(&sm.d_free[n & 1], ((n >> 1) - 1) & 1, dead, err);
+#pragma unroll 1
+      for (int c = 0; c < C; ++c, ++nw) {
+        if (n == 0) wait_or_die(&sm.a_full[c], 0, dead, err);
+        const uint32_t s = nw % kWStages;
+        wait_or_die(&sm.w_full[s], (nw / kWStages) & 1, dead, err);
+        if (*dead) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma(tmem + (n & 1) * 256, d_a + ((c * kSlot + k * 32) >> 4), d_w + ((s * kWStage + k * 32) >> 4), id,
+                 c > 0 || k > 0);
+        tc_commit(&sm.w_empty[s]);
+      }
+      if (!*dead) tc_commit(&sm.d_full[n & 1]);
+    }
+    tc_commit(&sm.drain);
+    mbar_wait_bounded(&sm.drain, 0, err);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tc_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Attention: a CTA takes two tiles of 128 queries of one head.  S = Q K^T (12 k-steps)
+// and O += P V (8 k-steps) of the two tiles alternate on the tensor cores, so that one
+// tile's softmax runs under the other's products.  A thread owns a query: its row of S
+// comes from tensor memory into registers, P goes back over it in bf16 and is the next
+// product's A operand there.  The reference m moves only when a logit passes it by more
+// than 2^8, which is when the row's O is rescaled.  Keys and values arrive in 16 KB
+// slots (K: two of 64 dims and one of the position keys, straight from the pool's blocks;
+// V: two of 64 dims), eight in the ring.
+// ---------------------------------------------------------------------------
+// Warps 0..3 and 4..7: softmax of a tile each; 8: copies; 9: MMAs; 10, 11 fill the third
+// warpgroup, which gives registers to the other two: 2 x 200 + 104 = 3 x 168, the launch
+// allocation (the launcher checks that the kernel was built with 168).
+constexpr int kAttnThreads = 384;
+constexpr int kAttnRegs = 168;
+constexpr int kSlots = 8;
+constexpr int kQTile = 3 * kSlot;
+
+struct AttnSmall {
+  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], o_full[2], drain, done;
+  uint32_t tmem;
+  int dead;
+};
+
+__global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* qs = smem;
+  uint8_t* ring = qs + 2 * kQTile;
+  AttnSmall& sm = *reinterpret_cast<AttnSmall*>(ring + kSlots * kSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* dead = &sm.dead;
+  int32_t* err = P.a.lv.err;
+  // the last queries see most: their tiles go first
+  const int bh = P.a.B * P.a.Hq;
+  const int pair = P.pairs - 1 - (int)(blockIdx.x / bh), rest = (int)(blockIdx.x % bh);
+  const int b = rest / P.a.Hq, h = rest % P.a.Hq;
+  const int R = P.a.R, n_q = P.a.n_q;
+  const int i0 = pair * 2 * kTile;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.o_full[i], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.done, 256);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  bool bad;
+  const int32_t L = context(P, b, &bad);
+  if (L == 0) {
+    if (bad && blockIdx.x / bh == 0 && h == 0 && threadIdx.x == 0) atomicOr(err, ERR_CTX);
+    const int n = min(2 * kTile, n_q - i0);
+    for (int i = threadIdx.x; i < n * (DH / 8); i += kAttnThreads)
+      reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i0 + i / (DH / 8)) * P.a.Hq + h) * DH)[i % (DH / 8)] =
+          make_uint4(0, 0, 0, 0);
+    return;
+  }
+  if (warp == 9) tc_alloc(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;  // S of the two tiles, then O of the two
+  const int off = L - n_q;        // query i sees off + i + 1 tokens
+  // key tiles of each query tile
+  int nt[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(n_q, i0 + (t + 1) * kTile) - 1;
+    nt[t] = last < i0 + t * kTile ? 0 : (off + last + 1 + kTile - 1) / kTile;
+  }
+  const int nmax = max(nt[0], nt[1]);
+
+  // The warpgroups' paths do not rejoin: each ends in a return.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + t * kTile + lanes, tm_o = tmem + 2 * kTile + t * kTile + lanes;
+    const int i = i0 + t * kTile + (warp & 3) * 32 + lane;
+    const int vis = off + i + 1;
+    const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
+    float m = kNoMax, l = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < nt[t]; ++j) {
+      wait_or_die(&sm.s_full[t], j & 1, dead, err);
+      tc_fence_after();
+      float x[128];
+      {
+        uint32_t r[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tc_ld_rows<32>(tm_s + 32 * q, r[q]);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
+      }
+      if (P.negative) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = -x[c];
+      }
+      if ((j + 1) * kTile > vis_first) {
+        const int n = vis - j * kTile;  // this query sees the tile's first n keys
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= n) x[c] = -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale;
+      if (__any_sync(0xffffffffu, top > m + kSlack)) {
+        const float mn = fmaxf(m, top);
+        const float f = ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+          // the products of the tile before are complete: this S was issued after them
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tc_ld_rows<32>(tm_o + 32 * q, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tc_st_rows<32>(tm_o + 32 * q, o);
+          }
+        }
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float e0 = ex2(fmaf(x[32 * q + 2 * c], P.scale, -m));
+          const float e1 = ex2(fmaf(x[32 * q + 2 * c + 1], P.scale, -m));
+          sum[2 * (c & 1)] += e0;
+          sum[2 * (c & 1) + 1] += e1;
+          w[c] = bf2(e0, e1);
+        }
+        tc_st_rows<16>(tm_s + 16 * q, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sm.p_full[t]);
+    }
+    if (nt[t] > 0) {
+      wait_or_die(&sm.o_full[t], 0, dead, err);
+      tc_fence_after();
+      const float inv = 1.f / l;
+      uint4* out = reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i) * P.a.Hq + h) * DH);
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[32];
+        tc_ld_rows<32>(tm_o + 32 * q, o);
+        tc_wait_ld();
+        if (i < n_q) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = bf2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+            out[4 * q + c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(&sm.done);
+    return;
+  }
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp == 8) {
+    // ------------------------------------------------------------------ copies
+    const uint64_t keep = l2_policy_evict_normal();
+    if (lane == 0) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (nt[t] > 0) {
+          mbar_arrive_expect_tx(&sm.q_full[t], kQTile);
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d(qs + t * kQTile + c * kSlot, &P.q_map, c * 64, h, b * n_q + i0 + t * kTile, &sm.q_full[t], keep);
+        }
+    }
+    const int row0 = (b * P.a.Hq + h) * P.T;
+    uint32_t n = 0;
+    bool stop = false;
+    for (int jb = 0; jb < nmax && !stop; jb += 8) {
+      // lane l looks up block 4 jb + l and copies its position keys
+      const int blk = 4 * jb + lane;
+      int y0 = 0;
+      const uint8_t* map = blk < 4 * nmax && blk * kBlockTokens < L ? block_map(P, b, blk, &y0) : nullptr;
+      const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
+      for (int j = jb; j < min(jb + 8, nmax) && !stop; ++j)
+        for (int c = 0; c < 5; ++c) {
+          const uint32_t s = n % kSlots, round = n / kSlots;
+          if (round > 0) wait_or_die(&sm.empty[s], (round - 1) & 1, dead, err);
+          stop = __any_sync(0xffffffffu, *dead);
+          if (stop) break;
+          uint8_t* dst = ring + s * kSlot;
+          if (c == 2) {
+            const int i = j - jb;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], __popc((have >> (4 * i)) & 15u) * kBlockBytes);
+            __syncwarp();
+            if ((lane >> 2) == i && map) tma_load_3d(dst + (lane & 3) * kBlockBytes, map, 0, y0, R / 64, &sm.full[s], keep);
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.full[s], kSlot);
+            if (c < 2)
+              tma_load_2d(dst, &P.k_map, c * 64, row0 + j * kTile, &sm.full[s], keep);
+            else
+              tma_load_2d(dst, &P.v_map, (c - 3) * 64, row0 + j * kTile, &sm.full[s], keep);
+          }
+          ++n;
+        }
+    }
+    for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
+      mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1, err);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (nt[t] > 0) mbar_wait_bounded(&sm.q_full[t], 0, err);
+  } else if (warp == 9) {
+    // -------------------------------------------------------------------- MMAs
+    if (lane == 0) {
+    constexpr uint32_t id_s = tc_idesc(128, 128, false, false);
+    constexpr uint32_t id_o = tc_idesc(128, 64, false, true);
+    const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ring), 16, 1024);
+    const uint64_t d_v = d_k;  // one 64-wide column of rows: the same strides, read MN-major
+#pragma unroll 1
+    for (int j = 0; j <= nmax; ++j) {
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (j > 0 && j - 1 < nt[t]) {
+          // O_t += P_t(j-1) V(j-1): 64 value columns from each slot
+          wait_or_die(&sm.p_full[t], (j - 1) & 1, dead, err);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t n = 5 * (uint32_t)(j - 1) + 3 + c;
+            wait_or_die(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
+            if (!*dead) {
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc_mma_ts(tmem + 2 * kTile + t * kTile + 64 * c, tmem + t * kTile + 8 * k,
+                          d_v + (((n % kSlots) * kSlot + k * 2048) >> 4), id_o, j > 1 || k > 0);
+            }
+          }
+          if (!*dead && j == nt[t]) tc_commit(&sm.o_full[t]);
+        }
+        if (t == 1 && j > 0 && !*dead)
+          for (int c = 3; c < 5; ++c) tc_commit(&sm.empty[(5 * (uint32_t)(j - 1) + c) % kSlots]);
+        if (j < nt[t]) {
+          if (j == 0) wait_or_die(&sm.q_full[t], 0, dead, err);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint32_t n = 5 * (uint32_t)j + c;
+            wait_or_die(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
+            if (!*dead) {
+              tc_fence_after();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc_mma(tmem + t * kTile, d_q + ((t * kQTile + c * kSlot + k * 32) >> 4),
+                       d_k + (((n % kSlots) * kSlot + k * 32) >> 4), id_s, c > 0 || k > 0);
+            }
+          }
+          if (!*dead) tc_commit(&sm.s_full[t]);
+        }
+      }
+      if (j < nmax && !*dead)
+        for (int c = 0; c < 3; ++c) tc_commit(&sm.empty[(5 * (uint32_t)j + c) % kSlots]);
+    }
+    tc_commit(&sm.drain);
+    mbar_wait_bounded(&sm.drain, 0, err);
+    }
+    __syncwarp();
+    mbar_wait_bounded(&sm.done, 0, err);  // the softmax warps have read their last column
+    tc_fence_after();
+    __syncwarp();
+    tc_dealloc(tmem, 512);
   }
 }
 
-// One warp per query row (b, i, h).
-__global__ void __launch_bounds__(256) latent_prefill_simple_kernel(const LatentPrefillArgs a, const uint16_t* ki,
-                                                                    const uint16_t* vi) {
-  constexpr int E = DH / 32, EP = kRope / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (row >= (int64_t)a.B * a.n_q * a.Hq) return;
-  const int b = (int)(row / ((int64_t)a.n_q * a.Hq));
-  const int i = (int)(row / a.Hq % a.n_q), h = (int)(row % a.Hq);
-  bool bad;
-  const int64_t lim = min((int64_t)a.max_blocks * kBlockTokens, (int64_t)a.max_ctx);
-  const int32_t L = latent_ctx(a.ctx[b], lim, a.n_q, &bad);
-  const int32_t vis = L == 0 ? 0 : L - a.n_q + i + 1;
-  float q[E + EP], acc[E];
-#pragma unroll
-  for (int e = 0; e < E + EP; ++e) q[e] = bf(a.q[row * (DH + kRope) + lane + 32 * e]);
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  const int64_t base = ((int64_t)b * a.Hq + h) * a.max_ctx;
-  for (int32_t t = 0; t < vis; ++t) {
-    const int32_t r = a.bt[(int64_t)b * a.max_blocks + t / kBlockTokens];
-    if (!latent_row_ok(a.lv, r)) continue;
-    const uint16_t* rp = reinterpret_cast<const uint16_t*>(latent_row(a.lv, r, t % kBlockTokens)) + a.R;
-    const uint16_t* kp = ki + (base + t) * DH;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * bf(kp[lane + 32 * e]);
-#pragma unroll
-    for (int e = 0; e < EP; ++e) s += q[E + e] * bf(rp[lane + 32 * e]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float k = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * k + p;
-    m = mn;
-    const uint16_t* vp = vi + (base + t) * DH;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * k + p * bf(vp[lane + 32 * e]);
-  }
-  const float inv = vis > 0 ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[row * DH + lane + 32 * e] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
+int tile_up(int x) { return (x + kTile - 1) / kTile * kTile; }
+
+template <typename K>
+cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const Params& P) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = P.a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, P);
 }
 
 }  // namespace
 
 size_t latent_prefill_workspace(int B, int Hq, int max_ctx) {
-  return 256 + (size_t)2 * B * Hq * (size_t)max_ctx * DH * sizeof(uint16_t);
+  return 256 + (size_t)2 * B * Hq * (size_t)tile_up(max_ctx) * DH * sizeof(uint16_t);
 }
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
-  uint16_t* k = (uint16_t*)a.ws;
-  uint16_t* v = k + (size_t)a.B * a.Hq * a.max_ctx * DH;
-  dim3 grid((unsigned)max(1, min(a.max_ctx, 4096)), (unsigned)a.Hq, (unsigned)a.B);
-  latent_expand_simple_kernel<<<grid, 256, 0, a.stream>>>(a, k, v);
-  const int64_t rows = (int64_t)a.B * a.n_q * a.Hq;
-  latent_prefill_simple_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, a.stream>>>(a, k, v);
-  return cudaGetLastError();
+  Params P;
+  P.a = a;
+  P.T = tile_up(a.max_ctx);
+  P.k = (uint16_t*)a.ws;
+  P.v = P.k + (size_t)a.B * a.Hq * P.T * DH;
+  // -inf (a hidden key) times 0 would be NaN: a scale of 0 becomes a tiny one
+  P.scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
+  P.negative = a.scale_log2 < 0.f;
+  P.pairs = (a.n_q + 2 * kTile - 1) / (2 * kTile);
+  const int tiles = P.T / kTile;
+  if (tiles > 0) {
+    const uint64_t wd[2] = {(uint64_t)a.R, (uint64_t)a.Hq * DH}, wst[1] = {(uint64_t)a.R * 2};
+    const uint64_t kd[2] = {DH, (uint64_t)a.B * a.Hq * P.T}, kst[1] = {DH * 2};
+    const uint64_t qd[3] = {DH + kRope, (uint64_t)a.Hq, (uint64_t)a.B * a.n_q};
+    const uint64_t qst[2] = {(DH + kRope) * 2, (uint64_t)a.Hq * (DH + kRope) * 2};
+    const uint32_t box[2] = {64, kTile}, qbox[3] = {64, 1, kTile};
+    if (!encode_bf16_map(&P.wk_map, a.wk, 2, wd, wst, box) || !encode_bf16_map(&P.wv_map, a.wv, 2, wd, wst, box) ||
+        !encode_bf16_map(&P.k_map, P.k, 2, kd, kst, box) || !encode_bf16_map(&P.v_map, P.v, 2, kd, kst, box) ||
+        !encode_bf16_map(&P.q_map, a.q, 3, qd, qst, qbox))
+      return cudaErrorInvalidValue;
+    // few token tiles: a CTA takes fewer heads, so that two rounds of CTAs fill the GPU
+    const int64_t work = (int64_t)tiles * a.B * a.Hq;
+    const int64_t per = work / (2 * (int64_t)a.ctas);
+    P.heads_per_cta = (int)(per < 1 ? 1 : per > a.Hq ? a.Hq : per);
+    const dim3 grid((unsigned)tiles, (unsigned)((a.Hq + P.heads_per_cta - 1) / P.heads_per_cta), (unsigned)a.B);
+    const size_t smem = kSmall + (size_t)(a.R / 64) * kSlot + kWStages * kWStage;
+    const cudaError_t e = a.R == 512 ? launch(latent_expand_kernel<512>, grid, kExpandThreads, smem, P)
+                                     : launch(latent_expand_kernel<256>, grid, kExpandThreads, smem, P);
+    if (e != cudaSuccess) return e;
+  }
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, latent_prefill_kernel) == cudaSuccess ? fa.numRegs : -1;
+  }();
+  if (regs != kAttnRegs) return cudaErrorInvalidDeviceFunction;
+  return launch(latent_prefill_kernel, dim3((unsigned)((int64_t)P.pairs * a.B * a.Hq)), kAttnThreads,
+                kSmall + 2 * kQTile + kSlots * kSlot, P);
 }
 
 }  // namespace pkv

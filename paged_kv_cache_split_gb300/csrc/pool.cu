@@ -122,6 +122,20 @@ static EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
+bool pkv::encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                          const uint32_t* box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3];
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i];
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Tensor maps of one slab group: for every layer and stored tensor, the slab
 // [slab_blocks * 32 tokens][Hkv * row] bytes viewed in 3-D as [column block][token]
 // [W bytes] (W = box_bytes), read in boxes of 16 tokens x the whole row, which land
@@ -820,11 +834,17 @@ static int latent_prefill_ctx(int max_blocks, int max_ctx) {
   return (int)(max_ctx > 0 && max_ctx < all ? max_ctx : all);
 }
 
+// The expanded rows (per sequence and head) are numbered in 32 bits.
+static bool latent_prefill_fits(int B, int Hq, int max_ctx) {
+  return (int64_t)B * Hq * ((int64_t)max_ctx + 128) < (int64_t)1 << 31;
+}
+
 pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* p, int B, int n_q, int Hq, int max_blocks, int max_ctx,
                                               size_t* bytes) {
   if (!p || !bytes || !latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || max_ctx < 0)
     return PKV_ERR_INVALID;
   if (p->cfg.format != PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  if (!latent_prefill_fits(B, Hq, latent_prefill_ctx(max_blocks, max_ctx))) return PKV_ERR_INVALID;
   *bytes = latent_prefill_workspace(B, Hq, latent_prefill_ctx(max_blocks, max_ctx));
   return PKV_OK;
 }
@@ -843,6 +863,7 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
     return PKV_ERR_INVALID;
   LatentPrefillArgs a;
   a.max_ctx = latent_prefill_ctx(max_blocks, max_ctx);
+  if (!latent_prefill_fits(B, Hq, a.max_ctx)) return PKV_ERR_INVALID;
   if (ws_bytes < latent_prefill_workspace(B, Hq, a.max_ctx)) return PKV_ERR_INVALID;
   a.lv = layer_view(p, layer);
   a.R = p->cfg.head_dim;

@@ -3,6 +3,8 @@
 // with FP32 accumulators in tensor memory (TMEM), commits, and TMEM loads and stores.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -124,6 +126,35 @@ __device__ __forceinline__ void tc_ld_frag16(uint32_t addr, uint32_t (&r)[N / 2]
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : PKV_R8(r, 0), PKV_R8(r, 8), PKV_R8(r, 16), PKV_R8(r, 24)
         : "r"(addr));
+}
+
+// Waits are bounded.  The first one to give up sets the error word and `dead`; after that
+// no wait blocks and nothing more is issued, so every thread still meets every barrier.
+__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
+  if (mbar_try_wait(bar, parity) || *dead) return;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      if (*dead) return;
+      if (global_timer_ns() - t0 > 1000000000ull) {
+        atomicOr(err, ERR_TIMEOUT);
+        *dead = 1;
+        return;
+      }
+    }
+  }
+}
+
+// 2^x with the hardware approximation (relative error below 2^-22; tiny results flush to 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, bool valid) {
