@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   Small<R, N>& sm = *reinterpret_cast<Small<R, N>*>(ps + L::kPBytes);
   static_assert(sizeof(Small<R, N>) <= kSmall - 1024, "small state");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int rt = blockIdx.x % P.n_rt, group = blockIdx.x / P.n_rt;
   volatile int* dead = &sm.dead;
   int32_t* err = P.a.lv.err;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
   Walk walk = sm.walk;
   Segment seg;
@@ -431,15 +431,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   } else if (warp == 4) {
     // ------------------------------------------------------------------ copies
     const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-    uint32_t np = 0, nr = 0;  // slots used so far
-    while (walk.next<N>(P, rt, seg)) {
+    uint32_t ps_ = 0, pround = 0, rs_ = 0, rround = 0;  // next slot and round of each ring
+    uint32_t np = 0, nr = 0;                            // slots filled so far
+    bool alive = true;
+    while (alive && walk.next<N>(P, rt, seg)) {
       const int nblk = (seg.vis + kBlockTokens - 1) / kBlockTokens;
-      for (int ub = seg.k0; ub < seg.k1; ub += 16) {
-        // lane l looks up block 2 ub + l of the sequence and issues its copies
+      const int k0 = uniform(seg.k0), k1 = uniform(seg.k1);
+      for (int ub = k0; alive && ub < k1; ub += 16) {
+        // lane l looks up block 2 ub + l of the sequence
         const int j = 2 * ub + lane;
         const uint8_t* map = nullptr;
         int y0 = 0;
-        if (j < nblk && j < 2 * seg.k1) {
+        if (j < nblk && j < 2 * k1) {
           const int32_t row = P.a.bt[(int64_t)seg.b * P.a.max_blocks + j];
           if (latent_row_ok(P.a.lv, row)) {
             const int32_t slab = row / P.a.lv.slab_blocks;
@@ -450,38 +453,42 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             atomicOr(err, ERR_ROW);
           }
         }
-        const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
-        const int ue = min(ub + 16, seg.k1);
+        const int ue = min(ub + 16, k1);
         for (int u = ub; u < ue; ++u) {
-          const int i = u - ub;
-          const bool mine = (lane >> 1) == i && map;
-          const int blocks = __popc((have >> (2 * i)) & 3u);
-          const int half = (lane & 1) * kBlockBytes;
-          {
-            const uint32_t slot = nr % L::kRopeSlots, round = nr / L::kRopeSlots;
-            if (round > 0) wait_or_die(&sm.rope_empty[slot], (round - 1) & 1, dead, err);
-            if (__any_sync(0xffffffffu, *dead)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.rope_full[slot], blocks * kBlockBytes);
-            __syncwarp();
-            if (mine) tma_load_3d(ropes + slot * kChunkBytes + half, map, 0, y0, R / 64, &sm.rope_full[slot], policy);
-            ++nr;
+          const int i = 2 * (u - ub);
+          const uint8_t *m0 = lane_ptr(map, i), *m1 = lane_ptr(map, i + 1);
+          const int ya = __shfl_sync(0xffffffffu, y0, i), yb = __shfl_sync(0xffffffffu, y0, i + 1);
+          const uint32_t bytes = ((m0 != nullptr) + (m1 != nullptr)) * kBlockBytes;
+          if (rround > 0) alive = warp_wait(&sm.rope_empty[rs_], (rround - 1) & 1, dead, err);
+          if (!alive) break;
+          if (elect_one()) {
+            uint8_t* dst = ropes + rs_ * kChunkBytes;
+            mbar_arrive_expect_tx(&sm.rope_full[rs_], bytes);
+            if (m0) tma_load_3d(dst, m0, 0, ya, R / 64, &sm.rope_full[rs_], policy);
+            if (m1) tma_load_3d(dst + kBlockBytes, m1, 0, yb, R / 64, &sm.rope_full[rs_], policy);
           }
-          bool stop = false;
+          ++nr;
+          if (++rs_ == L::kRopeSlots) rs_ = 0, ++rround;
+#pragma unroll 1
           for (int p = 0; p < L::kPairs; ++p) {
-            const uint32_t slot = np % L::kPairSlots, round = np / L::kPairSlots;
-            if (round > 0) wait_or_die(&sm.pair_empty[slot], (round - 1) & 1, dead, err);
-            stop = __any_sync(0xffffffffu, *dead);
-            if (stop) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.pair_full[slot], 2 * blocks * kBlockBytes);
-            __syncwarp();
-            if (mine) {
-              uint8_t* dst = pairs + slot * kPairBytes + half;
-              tma_load_3d(dst, map, 0, y0, 2 * p, &sm.pair_full[slot], policy);
-              tma_load_3d(dst + kChunkBytes, map, 0, y0, 2 * p + 1, &sm.pair_full[slot], policy);
+            if (pround > 0) alive = warp_wait(&sm.pair_empty[ps_], (pround - 1) & 1, dead, err);
+            if (!alive) break;
+            if (elect_one()) {
+              uint8_t* dst = pairs + ps_ * kPairBytes;
+              mbar_arrive_expect_tx(&sm.pair_full[ps_], 2 * bytes);
+              if (m0) {
+                tma_load_3d(dst, m0, 0, ya, 2 * p, &sm.pair_full[ps_], policy);
+                tma_load_3d(dst + kChunkBytes, m0, 0, ya, 2 * p + 1, &sm.pair_full[ps_], policy);
+              }
+              if (m1) {
+                tma_load_3d(dst + kBlockBytes, m1, 0, yb, 2 * p, &sm.pair_full[ps_], policy);
+                tma_load_3d(dst + kChunkBytes + kBlockBytes, m1, 0, yb, 2 * p + 1, &sm.pair_full[ps_], policy);
+              }
             }
             ++np;
+            if (++ps_ == L::kPairSlots) ps_ = 0, ++pround;
           }
-          if (stop) break;
+          if (!alive) break;
         }
       }
     }
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       mbar_wait_bounded(&sm.pair_full[i % L::kPairSlots], (i / L::kPairSlots) & 1, err);
     for (uint32_t i = nr > L::kRopeSlots ? nr - L::kRopeSlots : 0; i < nr; ++i)
       mbar_wait_bounded(&sm.rope_full[i % L::kRopeSlots], (i / L::kRopeSlots) & 1, err);
-  } else if (lane == 0) {
+  } else {
     // -------------------------------------------------------------------- MMAs
     constexpr uint32_t id_s = tc_idesc(64, N, false, false);
     constexpr uint32_t id_o = tc_idesc(128, N, true, false);
@@ -498,63 +505,72 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_p = tc_desc(smem_u32(ps), 16, 1024);
     const uint64_t d_v = tc_desc(smem_u32(pairs), kChunkBytes, 1024);
     int it = 0, n_seg = 0;
-    bool pending = false, pending_first = false;
+    uint32_t ks = 0, kround = 0, vs = 0, rs_ = 0, rround = 0;  // slots of the next K, V and position keys
+    bool alive = true, pending = false, pending_first = false;
     // O^T (+)= V^T P^T of tile i
     auto add_values = [&](int i, bool first) {
-      wait_or_die(&sm.p_full, i & 1, dead, err);
-      if (*dead) return;
+      alive = alive && warp_wait(&sm.p_full, i & 1, dead, err);
+      if (!alive) return;
       tc_fence_after();
 #pragma unroll 1
       for (int mb = 0; mb < L::kPairs; ++mb) {
-        const uint32_t slot = ((uint32_t)i * L::kPairs + mb) % L::kPairSlots;
+        if (elect_one()) {
+          const uint64_t a = d_v + ((vs * kPairBytes) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma(tm_o + mb * N, d_v + ((slot * kPairBytes + k * 2048) >> 4), d_p + ((k * 32) >> 4), id_o,
-                 !(first && k == 0));
-        tc_commit(&sm.pair_empty[slot]);
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tm_o + mb * N, a + (k * 2048 >> 4), d_p + (k * 32 >> 4), id_o, !(first && k == 0));
+          tc_commit(&sm.pair_empty[vs]);
+          if (mb == L::kPairs - 1) tc_commit(&sm.pv_done);
+        }
+        if (++vs == L::kPairSlots) vs = 0;
       }
-      tc_commit(&sm.pv_done);
     };
-    while (walk.next<N>(P, rt, seg)) {
-      for (int u = seg.k0; u < seg.k1; ++u, ++it) {
-        const bool first = u == seg.k0;
+    while (alive && walk.next<N>(P, rt, seg)) {
+      const int k0 = uniform(seg.k0), k1 = uniform(seg.k1);
+      for (int u = k0; alive && u < k1; ++u, ++it) {
+        const bool first = u == k0;
         if (first) {
           if (pending) add_values(it - 1, pending_first);
           pending = false;
-          wait_or_die(&sm.q_full, n_seg & 1, dead, err);
+          alive = alive && warp_wait(&sm.q_full, n_seg & 1, dead, err);
           ++n_seg;
         }
         const int buf = it & 1;
-        if (it >= 2) wait_or_die(&sm.s_free[buf], ((it >> 1) - 1) & 1, dead, err);
-        const uint32_t rslot = (uint32_t)it % L::kRopeSlots, rround = (uint32_t)it / L::kRopeSlots;
-        wait_or_die(&sm.rope_full[rslot], rround & 1, dead, err);
-        if (!*dead) {
-          tc_fence_after();
+        if (it >= 2) alive = alive && warp_wait(&sm.s_free[buf], ((it >> 1) - 1) & 1, dead, err);
+        alive = alive && warp_wait(&sm.rope_full[rs_], rround & 1, dead, err);
+        if (!alive) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = d_rope + ((rs_ * kChunkBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma(tm_s + buf * N, d_rope + ((rslot * kChunkBytes + k * 32) >> 4),
-                   d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
-          tc_commit(&sm.rope_empty[rslot]);
+            tc_mma(tm_s + buf * N, a + (k * 32 >> 4), d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
+          tc_commit(&sm.rope_empty[rs_]);
         }
+        if (++rs_ == L::kRopeSlots) rs_ = 0, ++rround;
 #pragma unroll 1
         for (int p = 0; p < L::kPairs; ++p) {
-          const uint32_t idx = (uint32_t)it * L::kPairs + p, slot = idx % L::kPairSlots;
-          wait_or_die(&sm.pair_full[slot], (idx / L::kPairSlots) & 1, dead, err);
-          if (*dead) break;
+          alive = alive && warp_wait(&sm.pair_full[ks], kround & 1, dead, err);
+          if (!alive) break;
           tc_fence_after();
+          if (elect_one()) {
+            const uint64_t a = d_pair + ((ks * kPairBytes) >> 4), q = d_q + ((2 * p * N * 128) >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma(tm_s + buf * N, d_pair + ((slot * kPairBytes + (k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
-                   d_q + (((2 * p + (k >> 2)) * N * 128 + (k & 3) * 32) >> 4), id_s, true);
+            for (int k = 0; k < 8; ++k)
+              tc_mma(tm_s + buf * N, a + (((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
+                     q + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), id_s, true);
+            if (p == L::kPairs - 1) tc_commit(&sm.s_full[buf]);
+          }
+          if (++ks == L::kPairSlots) ks = 0, ++kround;
         }
-        if (!*dead) tc_commit(&sm.s_full[buf]);
         if (pending) add_values(it - 1, pending_first);
         pending = true;
         pending_first = first;
       }
     }
-    if (pending) add_values(it - 1, pending_first);
-    tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
+    if (pending && alive) add_values(it - 1, pending_first);
+    __syncwarp();
+    if (elect_one()) tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
     mbar_wait_bounded(&sm.drain, 0, err);
   }
   __syncwarp();

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   uint8_t* as = smem;
   uint8_t* ws = as + (R / 64) * kSlot;
   ExpandSmall<R>& sm = *reinterpret_cast<ExpandSmall<R>*>(ws + kWStages * kWStage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* dead = &sm.dead;
   int32_t* err = P.a.lv.err;
   const int tile = blockIdx.x, b = blockIdx.z;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = uniform(sm.tmem);
   constexpr int C = R / 64;  // k-chunks
 
   if (warp < 4) {
@@ -148,59 +148,67 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
       mbar_arrive(&sm.d_free[n & 1]);
     }
   } else if (warp == 4) {
-    // lane l < 4 copies block l of the tile
+    // lane l < 4 looks up block l of the tile
     const uint64_t keep = l2_policy_evict_normal();
     const int j = tile * (kTile / kBlockTokens) + lane;
     int y0 = 0;
     const uint8_t* map = lane < 4 && j * kBlockTokens < L ? block_map(P, b, j, &y0) : nullptr;
-    const int blocks = __popc(__ballot_sync(0xffffffffu, map != nullptr));
-    uint32_t nw = 0, na = 0;
-    for (int h = h0; h < h1; ++h)
+    const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, map != nullptr));
+    uint32_t nw = 0, na = 0, s = 0, round = 0;
+    bool alive = true;
+    for (int h = h0; alive && h < h1; ++h)
+#pragma unroll 1
       for (int c = 0; c < C; ++c) {
         if (h == h0) {
-          na = c + 1;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.a_full[c], blocks * kBlockBytes);
-          __syncwarp();
-          if (map) tma_load_3d(as + c * kSlot + lane * kBlockBytes, map, 0, y0, c, &sm.a_full[c], keep);
+          if (elect_one()) mbar_arrive_expect_tx(&sm.a_full[c], blocks * kBlockBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint8_t* mk = lane_ptr(map, k);
+            const int yk = __shfl_sync(0xffffffffu, y0, k);
+            if (mk && elect_one())
+              tma_load_3d(as + c * kSlot + k * kBlockBytes, mk, 0, yk, c, &sm.a_full[c], keep);
+          }
+          ++na;
         }
-        const uint32_t s = nw % kWStages, round = nw / kWStages;
-        if (round > 0) wait_or_die(&sm.w_empty[s], (round - 1) & 1, dead, err);
-        if (__any_sync(0xffffffffu, *dead)) {
-          h = h1;
-          break;
-        }
-        if (lane == 0) {
+        if (round > 0) alive = warp_wait(&sm.w_empty[s], (round - 1) & 1, dead, err);
+        if (!alive) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&sm.w_full[s], kWStage);
           tma_load_2d(ws + s * kWStage, &P.wk_map, c * 64, h * DH, &sm.w_full[s], keep);
           tma_load_2d(ws + s * kWStage + kSlot, &P.wv_map, c * 64, h * DH, &sm.w_full[s], keep);
         }
         ++nw;
+        if (++s == kWStages) s = 0, ++round;
       }
     for (uint32_t i = nw > kWStages ? nw - kWStages : 0; i < nw; ++i)
       mbar_wait_bounded(&sm.w_full[i % kWStages], (i / kWStages) & 1, err);
     for (uint32_t c = 0; c < na; ++c) mbar_wait_bounded(&sm.a_full[c], 0, err);
-  } else if (lane == 0) {
+  } else {
     constexpr uint32_t id = tc_idesc(128, 256, false, false);
     const uint64_t d_a = tc_desc(smem_u32(as), 16, 1024), d_w = tc_desc(smem_u32(ws), 16, 1024);
-    uint32_t nw = 0;
-    for (int h = h0, n = 0; h < h1; ++h, ++n) {
-      if (n >= 2) wait_or_die(&sm.d_free[n & 1], ((n >> 1) - 1) & 1, dead, err);
+    uint32_t s = 0, round = 0;
+    bool alive = true;
+    for (int h = h0, n = 0; alive && h < h1; ++h, ++n) {
+      if (n >= 2) alive = warp_wait(&sm.d_free[n & 1], ((n >> 1) - 1) & 1, dead, err);
 #pragma unroll 1
-      for (int c = 0; c < C; ++c, ++nw) {
-        if (n == 0) wait_or_die(&sm.a_full[c], 0, dead, err);
-        const uint32_t s = nw % kWStages;
-        wait_or_die(&sm.w_full[s], (nw / kWStages) & 1, dead, err);
-        if (*dead) break;
+      for (int c = 0; c < C; ++c) {
+        if (n == 0) alive = alive && warp_wait(&sm.a_full[c], 0, dead, err);
+        alive = alive && warp_wait(&sm.w_full[s], round & 1, dead, err);
+        if (!alive) break;
         tc_fence_after();
+        if (elect_one()) {
+          const uint64_t da = d_a + ((c * kSlot) >> 4), dw = d_w + ((s * kWStage) >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma(tmem + (n & 1) * 256, d_a + ((c * kSlot + k * 32) >> 4), d_w + ((s * kWStage + k * 32) >> 4), id,
-                 c > 0 || k > 0);
-        tc_commit(&sm.w_empty[s]);
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tmem + (n & 1) * 256, da + (k * 32 >> 4), dw + (k * 32 >> 4), id, c > 0 || k > 0);
+          tc_commit(&sm.w_empty[s]);
+          if (c == C - 1) tc_commit(&sm.d_full[n & 1]);
+        }
+        if (++s == kWStages) s = 0, ++round;
       }
-      if (!*dead) tc_commit(&sm.d_full[n & 1]);
     }
-    tc_commit(&sm.drain);
+    __syncwarp();
+    if (elect_one()) tc_commit(&sm.drain);
     mbar_wait_bounded(&sm.drain, 0, err);
   }
   __syncwarp();
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   uint8_t* qs = smem;
   uint8_t* ring = qs + 2 * kQTile;
   AttnSmall& sm = *reinterpret_cast<AttnSmall*>(ring + kSlots * kSlot);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* dead = &sm.dead;
   int32_t* err = P.a.lv.err;
   // the last queries see most: their tiles go first
@@ -279,22 +287,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;  // S of the two tiles, then O of the two
+  const uint32_t tmem = uniform(sm.tmem);  // S of the two tiles, then O of the two
   const int off = L - n_q;        // query i sees off + i + 1 tokens
   // key tiles of each query tile
-  int nt[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  auto key_tiles = [&](int t) {
     const int last = min(n_q, i0 + (t + 1) * kTile) - 1;
-    nt[t] = last < i0 + t * kTile ? 0 : (off + last + 1 + kTile - 1) / kTile;
-  }
-  const int nmax = max(nt[0], nt[1]);
+    return last < i0 + t * kTile ? 0 : uniform((off + last + 1 + kTile - 1) / kTile);
+  };
+  const int nt0 = key_tiles(0), nt1 = key_tiles(1), nmax = max(nt0, nt1);
 
   // The warpgroups' paths do not rejoin: each ends in a return.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------------------------------------------------------- softmax
-    const int t = warp >> 2;
+    const int t = warp >> 2, ntt = t ? nt1 : nt0;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + t * kTile + lanes, tm_o = tmem + 2 * kTile + t * kTile + lanes;
     const int i = i0 + t * kTile + (warp & 3) * 32 + lane;
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
     float m = kNoMax, l = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < nt[t]; ++j) {
+    for (int j = 0; j < ntt; ++j) {
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
       tc_fence_after();
       float x[128];
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       tc_fence_before();
       mbar_arrive(&sm.p_full[t]);
     }
-    if (nt[t] > 0) {
+    if (ntt > 0) {
       wait_or_die(&sm.o_full[t], 0, dead, err);
       tc_fence_after();
       const float inv = 1.f / l;
@@ -395,10 +401,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   if (warp == 8) {
     // ------------------------------------------------------------------ copies
     const uint64_t keep = l2_policy_evict_normal();
-    if (lane == 0) {
+    if (elect_one()) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        if (nt[t] > 0) {
+        if ((t ? nt1 : nt0) > 0) {
           mbar_arrive_expect_tx(&sm.q_full[t], kQTile);
           for (int c = 0; c < 3; ++c)
             tma_load_3d(qs + t * kQTile + c * kSlot, &P.q_map, c * 64, h, b * n_q + i0 + t * kTile, &sm.q_full[t], keep);
@@ -406,26 +412,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     }
     const int row0 = (b * P.a.Hq + h) * P.T;
     uint32_t n = 0;
-    bool stop = false;
-    for (int jb = 0; jb < nmax && !stop; jb += 8) {
-      // lane l looks up block 4 jb + l and copies its position keys
+    bool alive = true;
+    for (int jb = 0; alive && jb < nmax; jb += 8) {
+      // lane l looks up block 4 jb + l
       const int blk = 4 * jb + lane;
       int y0 = 0;
       const uint8_t* map = blk < 4 * nmax && blk * kBlockTokens < L ? block_map(P, b, blk, &y0) : nullptr;
       const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
-      for (int j = jb; j < min(jb + 8, nmax) && !stop; ++j)
+      const int je = min(jb + 8, nmax);
+#pragma unroll 1
+      for (int j = jb; alive && j < je; ++j)
+#pragma unroll
         for (int c = 0; c < 5; ++c) {
           const uint32_t s = n % kSlots, round = n / kSlots;
-          if (round > 0) wait_or_die(&sm.empty[s], (round - 1) & 1, dead, err);
-          stop = __any_sync(0xffffffffu, *dead);
-          if (stop) break;
+          alive = alive && (round == 0 || warp_wait(&sm.empty[s], (round - 1) & 1, dead, err));
+          if (!alive) break;
           uint8_t* dst = ring + s * kSlot;
           if (c == 2) {
-            const int i = j - jb;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], __popc((have >> (4 * i)) & 15u) * kBlockBytes);
-            __syncwarp();
-            if ((lane >> 2) == i && map) tma_load_3d(dst + (lane & 3) * kBlockBytes, map, 0, y0, R / 64, &sm.full[s], keep);
-          } else if (lane == 0) {
+            const int i = 4 * (j - jb);
+            if (elect_one()) mbar_arrive_expect_tx(&sm.full[s], __popc((have >> i) & 15u) * kBlockBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint8_t* mk = lane_ptr(map, i + k);
+              const int yk = __shfl_sync(0xffffffffu, y0, i + k);
+              if (mk && elect_one()) tma_load_3d(dst + k * kBlockBytes, mk, 0, yk, R / 64, &sm.full[s], keep);
+            }
+          } else if (elect_one()) {
             mbar_arrive_expect_tx(&sm.full[s], kSlot);
             if (c < 2)
               tma_load_2d(dst, &P.k_map, c * 64, row0 + j * kTile, &sm.full[s], keep);
@@ -437,62 +449,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     }
     for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
       mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1, err);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      if (nt[t] > 0) mbar_wait_bounded(&sm.q_full[t], 0, err);
+    if (nt0 > 0) mbar_wait_bounded(&sm.q_full[0], 0, err);
+    if (nt1 > 0) mbar_wait_bounded(&sm.q_full[1], 0, err);
   } else if (warp == 9) {
     // -------------------------------------------------------------------- MMAs
-    if (lane == 0) {
     constexpr uint32_t id_s = tc_idesc(128, 128, false, false);
     constexpr uint32_t id_o = tc_idesc(128, 64, false, true);
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ring), 16, 1024);
     const uint64_t d_v = d_k;  // one 64-wide column of rows: the same strides, read MN-major
-#pragma unroll 1
-    for (int j = 0; j <= nmax; ++j) {
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        if (j > 0 && j - 1 < nt[t]) {
-          // O_t += P_t(j-1) V(j-1): 64 value columns from each slot
-          wait_or_die(&sm.p_full[t], (j - 1) & 1, dead, err);
+    bool alive = true;
+    auto slot_full = [&](uint32_t n) {
+      alive = alive && warp_wait(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
+      return alive;
+    };
+    // O_t += P_t(j) V(j), 64 value columns from each slot
+    auto add_values = [&](int t, int j, int ntt) {
+      alive = alive && warp_wait(&sm.p_full[t], j & 1, dead, err);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t n = 5 * (uint32_t)(j - 1) + 3 + c;
-            wait_or_die(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
-            if (!*dead) {
-              tc_fence_after();
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t n = 5 * (uint32_t)j + 3 + c;
+        if (!slot_full(n)) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t v = d_v + (((n % kSlots) * kSlot) >> 4);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc_mma_ts(tmem + 2 * kTile + t * kTile + 64 * c, tmem + t * kTile + 8 * k,
-                          d_v + (((n % kSlots) * kSlot + k * 2048) >> 4), id_o, j > 1 || k > 0);
-            }
-          }
-          if (!*dead && j == nt[t]) tc_commit(&sm.o_full[t]);
-        }
-        if (t == 1 && j > 0 && !*dead)
-          for (int c = 3; c < 5; ++c) tc_commit(&sm.empty[(5 * (uint32_t)(j - 1) + c) % kSlots]);
-        if (j < nt[t]) {
-          if (j == 0) wait_or_die(&sm.q_full[t], 0, dead, err);
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint32_t n = 5 * (uint32_t)j + c;
-            wait_or_die(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
-            if (!*dead) {
-              tc_fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tc_mma(tmem + t * kTile, d_q + ((t * kQTile + c * kSlot + k * 32) >> 4),
-                       d_k + (((n % kSlots) * kSlot + k * 32) >> 4), id_s, c > 0 || k > 0);
-            }
-          }
-          if (!*dead) tc_commit(&sm.s_full[t]);
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + 2 * kTile + t * kTile + 64 * c, tmem + t * kTile + 8 * k, v + (k * 2048 >> 4), id_o,
+                      j > 0 || k > 0);
+          if (c == 1 && j == ntt - 1) tc_commit(&sm.o_full[t]);
         }
       }
-      if (j < nmax && !*dead)
+    };
+    // S_t = Q_t K(j)^T
+    auto logits = [&](int t, int j) {
+      if (j == 0) alive = alive && warp_wait(&sm.q_full[t], 0, dead, err);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t n = 5 * (uint32_t)j + c;
+        if (!slot_full(n)) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t q = d_q + ((t * kQTile + c * kSlot) >> 4), k0 = d_k + (((n % kSlots) * kSlot) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tmem + t * kTile, q + (k * 32 >> 4), k0 + (k * 32 >> 4), id_s, c > 0 || k > 0);
+          if (c == 2) tc_commit(&sm.s_full[t]);
+        }
+      }
+    };
+#pragma unroll 1
+    for (int j = 0; alive && j <= nmax; ++j) {
+      if (j > 0 && j - 1 < nt0) add_values(0, j - 1, nt0);
+      if (j < nt0) logits(0, j);
+      if (j > 0 && j - 1 < nt1) add_values(1, j - 1, nt1);
+      if (j > 0 && alive && elect_one())
+        for (int c = 3; c < 5; ++c) tc_commit(&sm.empty[(5 * (uint32_t)(j - 1) + c) % kSlots]);
+      if (j < nt1) logits(1, j);
+      if (j < nmax && alive && elect_one())
         for (int c = 0; c < 3; ++c) tc_commit(&sm.empty[(5 * (uint32_t)j + c) % kSlots]);
     }
-    tc_commit(&sm.drain);
+    __syncwarp();
+    if (elect_one()) tc_commit(&sm.drain);
     mbar_wait_bounded(&sm.drain, 0, err);
-    }
     __syncwarp();
     mbar_wait_bounded(&sm.done, 0, err);  // the softmax warps have read their last column
     tc_fence_after();

@@ -145,6 +145,41 @@ __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, vola
   }
 }
 
+// The same for a whole converged warp, with warp-uniform control flow: the instructions
+// that issue MMAs and copies take their operands from uniform registers, and a loop the
+// compiler cannot prove uniform moves every operand there one by one (measured: 90 cycles
+// per MMA issued by one diverged thread).  False when the wait gave up or the CTA is dead.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 63u) == 0) {
+      if (__any_sync(0xffffffffu, *dead)) return false;
+      if (__any_sync(0xffffffffu, global_timer_ns() - t0 > 1000000000ull)) {
+        atomicOr(err, ERR_TIMEOUT);
+        *dead = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+
+// A value every lane holds, known to the compiler as warp-uniform.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ const uint8_t* lane_ptr(const uint8_t* p, int lane) {
+  return reinterpret_cast<const uint8_t*>(
+      (uintptr_t)__shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)p, lane));
+}
+
 // 2^x with the hardware approximation (relative error below 2^-22; tiny results flush to 0).
 __device__ __forceinline__ float ex2(float x) {
   float y;
