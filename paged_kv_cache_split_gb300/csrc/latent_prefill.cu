@@ -28,7 +28,6 @@ constexpr float kNoMax = -1e30f;
 struct Params {
   LatentPrefillArgs a;
   int T;                // tokens per (sequence, head) in the workspace: max_ctx rounded up to a tile
-  int heads_per_cta;    // expansion
   int pairs;            // query tile pairs a sequence (attention)
   float scale;          // |scale| log2(e)
   int negative;         // scale < 0
@@ -58,17 +57,56 @@ __device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int 
 
 // ---------------------------------------------------------------------------
 // Expansion: [128 tokens x R] x [R x 256] per head (128 key values, 128 value values).
-// The tokens' latents stay in shared memory while the CTA goes over its heads, so only
-// the weights stream (from L2, through a ring of 64-wide k-chunks); two accumulators of
-// 256 columns let the epilogue of one head run under the products of the next.
+// The items (token tile, head) of all sequences, heads fastest, are split evenly over the
+// CTAs.  A tile's latents stay in shared memory over its heads, so only the weights stream
+// (from L2, through a ring of 64-wide k-chunks); two accumulators of 256 columns let the
+// epilogue of one item run under the products of the next.
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 192;  // warps 0..3 epilogue, 4 copies, 5 MMAs
 constexpr int kWStages = 3;
 constexpr int kWStage = 2 * kSlot;
 
+// The items of one CTA, in order.  Every role walks them by itself.
+struct Items {
+  int64_t item, end, base;  // next item; last + 1; tiles before sequence b
+  int b, len, tile, h;
+  __device__ __forceinline__ void start(const Params& P) {
+    const int lane = threadIdx.x & 31;
+    bool bad;
+    int64_t n = 0;
+    for (int i = lane; i < P.a.B; i += 32) n += (context(P, i, &bad) + kTile - 1) / kTile;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+    n *= P.a.Hq;
+    item = n * blockIdx.x / gridDim.x;
+    end = n * (blockIdx.x + 1) / gridDim.x;
+    base = 0;
+    b = 0;
+  }
+  // Whole warp.  new_tile: the tile differs from the item's before.
+  __device__ __forceinline__ bool next(const Params& P, bool first, bool* new_tile) {
+    if (item >= end) return false;
+    h = uniform((int)(item % P.a.Hq));
+    *new_tile = first || h == 0;
+    if (*new_tile) {
+      const int64_t t = item / P.a.Hq;
+      for (;; ++b) {
+        bool bad;
+        len = uniform(context(P, b, &bad));
+        const int n = (len + kTile - 1) / kTile;
+        if (t < base + n) break;
+        base += n;
+      }
+      tile = uniform((int)(t - base));
+    }
+    ++item;
+    return true;
+  }
+};
+
 template <int R>
 struct ExpandSmall {
-  uint64_t a_full[R / 64], w_full[kWStages], w_empty[kWStages], d_full[2], d_free[2], drain;
+  uint64_t a_full[R / 64], a_empty[R / 64], w_full[kWStages], w_empty[kWStages], d_full[2], d_free[2], drain;
   uint32_t tmem;
   int dead;
 };
@@ -83,17 +121,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* dead = &sm.dead;
   int32_t* err = P.a.lv.err;
-  const int tile = blockIdx.x, b = blockIdx.z;
-  const int h0 = blockIdx.y * P.heads_per_cta, h1 = min(P.a.Hq, h0 + P.heads_per_cta);
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  bool bad;
-  const int32_t L = context(P, b, &bad);
-  if (tile * kTile >= L) return;
+  constexpr int C = R / 64;  // k-chunks
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R / 64; ++i) mbar_init(&sm.a_full[i], 1);
+    for (int i = 0; i < C; ++i) mbar_init(&sm.a_full[i], 1), mbar_init(&sm.a_empty[i], 1);
     for (int i = 0; i < kWStages; ++i) mbar_init(&sm.w_full[i], 1), mbar_init(&sm.w_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_free[i], 128);
     mbar_init(&sm.drain, 1);
@@ -101,21 +132,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
     fence_mbar_init();
   }
   if (warp == 5) tc_alloc(&sm.tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem);
-  constexpr int C = R / 64;  // k-chunks
+  Items it;
+  it.start(P);
+  bool new_tile;
 
   if (warp < 4) {
-    const int t = tile * kTile + threadIdx.x;
-    const int partner = t ^ 1;
-    for (int h = h0, n = 0; h < h1; ++h, ++n) {
+    for (int n = 0; it.next(P, n == 0, &new_tile); ++n) {
+      const int t = it.tile * kTile + threadIdx.x, L = it.len;
+      const int partner = t ^ 1;
       wait_or_die(&sm.d_full[n & 1], (n >> 1) & 1, dead, err);
       tc_fence_after();
-      const int64_t base = ((int64_t)b * P.a.Hq + h) * P.T;
+      const int64_t base = ((int64_t)it.b * P.a.Hq + it.h) * P.T;
       // Pairs of lanes exchange 16-byte pieces so that each store of the pair fills a
-      // 32-byte sector of one row.
+      // 32-byte sector of one row.  Rows past the context become zero: their values meet
+      // probabilities of zero in the attention, which a NaN would survive.
       const bool odd = lane & 1;
 #pragma unroll 1
       for (int q = 0; q < 8; ++q) {
@@ -148,19 +184,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
       mbar_arrive(&sm.d_free[n & 1]);
     }
   } else if (warp == 4) {
-    // lane l < 4 looks up block l of the tile
     const uint64_t keep = l2_policy_evict_normal();
-    const int j = tile * (kTile / kBlockTokens) + lane;
+    uint32_t nw = 0, na = 0, s = 0, round = 0, tiles = 0;
+    const uint8_t* map = nullptr;
     int y0 = 0;
-    const uint8_t* map = lane < 4 && j * kBlockTokens < L ? block_map(P, b, j, &y0) : nullptr;
-    const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, map != nullptr));
-    uint32_t nw = 0, na = 0, s = 0, round = 0;
+    uint32_t bytes = 0;
     bool alive = true;
-    for (int h = h0; alive && h < h1; ++h)
+    for (int n = 0; alive && it.next(P, n == 0, &new_tile); ++n) {
+      if (new_tile) {
+        // lane l < 4 looks up block l of the tile
+        const int j = it.tile * (kTile / kBlockTokens) + lane;
+        map = lane < 4 && j * kBlockTokens < it.len ? block_map(P, it.b, j, &y0) : nullptr;
+        bytes = __popc(__ballot_sync(0xffffffffu, map != nullptr)) * kBlockBytes;
+        ++tiles;
+      }
 #pragma unroll 1
       for (int c = 0; c < C; ++c) {
-        if (h == h0) {
-          if (elect_one()) mbar_arrive_expect_tx(&sm.a_full[c], blocks * kBlockBytes);
+        if (new_tile) {
+          if (tiles > 1) alive = warp_wait(&sm.a_empty[c], tiles & 1, dead, err);
+          if (!alive) break;
+          if (elect_one()) mbar_arrive_expect_tx(&sm.a_full[c], bytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint8_t* mk = lane_ptr(map, k);
@@ -174,25 +217,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
         if (!alive) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&sm.w_full[s], kWStage);
-          tma_load_2d(ws + s * kWStage, &P.wk_map, c * 64, h * DH, &sm.w_full[s], keep);
-          tma_load_2d(ws + s * kWStage + kSlot, &P.wv_map, c * 64, h * DH, &sm.w_full[s], keep);
+          tma_load_2d(ws + s * kWStage, &P.wk_map, c * 64, it.h * DH, &sm.w_full[s], keep);
+          tma_load_2d(ws + s * kWStage + kSlot, &P.wv_map, c * 64, it.h * DH, &sm.w_full[s], keep);
         }
         ++nw;
         if (++s == kWStages) s = 0, ++round;
       }
+    }
+    // no copy may be in flight when the CTA ends
     for (uint32_t i = nw > kWStages ? nw - kWStages : 0; i < nw; ++i)
       mbar_wait_bounded(&sm.w_full[i % kWStages], (i / kWStages) & 1, err);
-    for (uint32_t c = 0; c < na; ++c) mbar_wait_bounded(&sm.a_full[c], 0, err);
+    for (uint32_t i = na > C ? na - C : 0; i < na; ++i) mbar_wait_bounded(&sm.a_full[i % C], (i / C) & 1, err);
   } else {
     constexpr uint32_t id = tc_idesc(128, 256, false, false);
     const uint64_t d_a = tc_desc(smem_u32(as), 16, 1024), d_w = tc_desc(smem_u32(ws), 16, 1024);
-    uint32_t s = 0, round = 0;
+    uint32_t s = 0, round = 0, tiles = 0;
     bool alive = true;
-    for (int h = h0, n = 0; alive && h < h1; ++h, ++n) {
+    for (int n = 0; alive && it.next(P, n == 0, &new_tile); ++n) {
+      if (new_tile) ++tiles;
+      const bool last_of_tile = it.h == P.a.Hq - 1 || it.item == it.end;
       if (n >= 2) alive = warp_wait(&sm.d_free[n & 1], ((n >> 1) - 1) & 1, dead, err);
 #pragma unroll 1
       for (int c = 0; c < C; ++c) {
-        if (n == 0) alive = alive && warp_wait(&sm.a_full[c], 0, dead, err);
+        if (new_tile) alive = alive && warp_wait(&sm.a_full[c], (tiles - 1) & 1, dead, err);
         alive = alive && warp_wait(&sm.w_full[s], round & 1, dead, err);
         if (!alive) break;
         tc_fence_after();
@@ -202,6 +249,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
           for (int k = 0; k < 4; ++k)
             tc_mma(tmem + (n & 1) * 256, da + (k * 32 >> 4), dw + (k * 32 >> 4), id, c > 0 || k > 0);
           tc_commit(&sm.w_empty[s]);
+          if (last_of_tile) tc_commit(&sm.a_empty[c]);
           if (c == C - 1) tc_commit(&sm.d_full[n & 1]);
         }
         if (++s == kWStages) s = 0, ++round;
@@ -226,7 +274,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
 // product's A operand there.  The reference m moves only when a logit passes it by more
 // than 2^8, which is when the row's O is rescaled.  Keys and values arrive in 16 KB
 // slots (K: two of 64 dims and one of the position keys, straight from the pool's blocks;
-// V: two of 64 dims), eight in the ring.
+// V: two of 64 keys, so that one MMA covers all 128 value columns), eight in the ring.
 // ---------------------------------------------------------------------------
 // Warps 0..3 and 4..7: softmax of a tile each; 8: copies; 9: MMAs; 10, 11 fill the third
 // warpgroup, which gives registers to the other two: 2 x 200 + 104 = 3 x 168, the launch
@@ -442,7 +490,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
             if (c < 2)
               tma_load_2d(dst, &P.k_map, c * 64, row0 + j * kTile, &sm.full[s], keep);
             else
-              tma_load_2d(dst, &P.v_map, (c - 3) * 64, row0 + j * kTile, &sm.full[s], keep);
+              for (int k = 0; k < 2; ++k)
+                tma_load_2d(dst + k * (kSlot / 2), &P.v_map, k * 64, row0 + j * kTile + (c - 3) * 64, &sm.full[s], keep);
           }
           ++n;
         }
@@ -454,15 +503,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   } else if (warp == 9) {
     // -------------------------------------------------------------------- MMAs
     constexpr uint32_t id_s = tc_idesc(128, 128, false, false);
-    constexpr uint32_t id_o = tc_idesc(128, 64, false, true);
+    constexpr uint32_t id_o = tc_idesc(128, 128, false, true);
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ring), 16, 1024);
-    const uint64_t d_v = d_k;  // one 64-wide column of rows: the same strides, read MN-major
+    const uint64_t d_v = tc_desc(smem_u32(ring), kSlot / 2, 1024);  // [2 x 64 values][64 keys], MN-major
     bool alive = true;
     auto slot_full = [&](uint32_t n) {
       alive = alive && warp_wait(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
       return alive;
     };
-    // O_t += P_t(j) V(j), 64 value columns from each slot
+    // O_t += P_t(j) V(j), 64 keys from each slot
     auto add_values = [&](int t, int j, int ntt) {
       alive = alive && warp_wait(&sm.p_full[t], j & 1, dead, err);
 #pragma unroll
@@ -473,9 +522,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         if (elect_one()) {
           const uint64_t v = d_v + (((n % kSlots) * kSlot) >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + 2 * kTile + t * kTile + 64 * c, tmem + t * kTile + 8 * k, v + (k * 2048 >> 4), id_o,
-                      j > 0 || k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + 32 * c + 8 * k, v + (k * 2048 >> 4), id_o,
+                      j > 0 || c > 0 || k > 0);
           if (c == 1 && j == ntt - 1) tc_commit(&sm.o_full[t]);
         }
       }
@@ -559,16 +608,13 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
     const uint64_t kd[2] = {DH, (uint64_t)a.B * a.Hq * P.T}, kst[1] = {DH * 2};
     const uint64_t qd[3] = {DH + kRope, (uint64_t)a.Hq, (uint64_t)a.B * a.n_q};
     const uint64_t qst[2] = {(DH + kRope) * 2, (uint64_t)a.Hq * (DH + kRope) * 2};
-    const uint32_t box[2] = {64, kTile}, qbox[3] = {64, 1, kTile};
+    const uint32_t box[2] = {64, kTile}, vbox[2] = {64, kTile / 2}, qbox[3] = {64, 1, kTile};
     if (!encode_bf16_map(&P.wk_map, a.wk, 2, wd, wst, box) || !encode_bf16_map(&P.wv_map, a.wv, 2, wd, wst, box) ||
-        !encode_bf16_map(&P.k_map, P.k, 2, kd, kst, box) || !encode_bf16_map(&P.v_map, P.v, 2, kd, kst, box) ||
+        !encode_bf16_map(&P.k_map, P.k, 2, kd, kst, box) || !encode_bf16_map(&P.v_map, P.v, 2, kd, kst, vbox) ||
         !encode_bf16_map(&P.q_map, a.q, 3, qd, qst, qbox))
       return cudaErrorInvalidValue;
-    // few token tiles: a CTA takes fewer heads, so that two rounds of CTAs fill the GPU
-    const int64_t work = (int64_t)tiles * a.B * a.Hq;
-    const int64_t per = work / (2 * (int64_t)a.ctas);
-    P.heads_per_cta = (int)(per < 1 ? 1 : per > a.Hq ? a.Hq : per);
-    const dim3 grid((unsigned)tiles, (unsigned)((a.Hq + P.heads_per_cta - 1) / P.heads_per_cta), (unsigned)a.B);
+    const int64_t items = (int64_t)tiles * a.B * a.Hq;  // at most
+    const dim3 grid((unsigned)(items < a.ctas ? items : a.ctas));
     const size_t smem = kSmall + (size_t)(a.R / 64) * kSlot + kWStages * kWStage;
     const cudaError_t e = a.R == 512 ? launch(latent_expand_kernel<512>, grid, kExpandThreads, smem, P)
                                      : launch(latent_expand_kernel<256>, grid, kExpandThreads, smem, P);

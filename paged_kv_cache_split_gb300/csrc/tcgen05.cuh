@@ -130,19 +130,22 @@ __device__ __forceinline__ void tc_ld_frag16(uint32_t addr, uint32_t (&r)[N / 2]
 
 // Waits are bounded.  The first one to give up sets the error word and `dead`; after that
 // no wait blocks and nothing more is issued, so every thread still meets every barrier.
+// Called by whole warps, which leave it converged.
 __device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int* dead, int32_t* err) {
-  if (mbar_try_wait(bar, parity) || *dead) return;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if ((it & 63u) == 0) {
-      if (*dead) return;
-      if (global_timer_ns() - t0 > 1000000000ull) {
-        atomicOr(err, ERR_TIMEOUT);
-        *dead = 1;
-        return;
+  if (!mbar_try_wait(bar, parity)) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+      if ((it & 63u) == 0) {
+        if (*dead) break;
+        if (global_timer_ns() - t0 > 1000000000ull) {
+          atomicOr(err, ERR_TIMEOUT);
+          *dead = 1;
+          break;
+        }
       }
     }
   }
+  __syncwarp();
 }
 
 // The same for a whole converged warp, with warp-uniform control flow: the instructions
