@@ -284,8 +284,39 @@ constexpr int kAttnRegs = 168;
 constexpr int kSlots = 8;
 constexpr int kQTile = 3 * kSlot;
 
+// Two FP32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 struct AttnSmall {
-  uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], o_full[2], drain, done;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by parity of the key tile
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain, done;
   uint32_t tmem;
   int dead;
 };
@@ -307,11 +338,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   const int i0 = pair * 2 * kTile;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&sm.full[i], 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
+      for (uint64_t* bar : {&sm.k_full[i], &sm.k_empty[i], &sm.v_full[i], &sm.v_empty[i]}) mbar_init(bar, 1);
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.p_full[i][0], 128);
+      mbar_init(&sm.p_full[i][1], 128);
       mbar_init(&sm.o_full[i], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -354,7 +386,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int i = i0 + t * kTile + (warp & 3) * 32 + lane;
     const int vis = off + i + 1;
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
-    float m = kNoMax, l = 0.f;
+    float m = kNoMax;
+    uint64_t l = 0;  // two partial sums
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
@@ -380,13 +413,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.scale;
+      for (int c = 4; c + 1 < 124; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale;
       if (__any_sync(0xffffffffu, top > m + kSlack)) {
         const float mn = fmaxf(m, top);
         const float f = ex2(m - mn);
         m = mn;
-        l *= f;
+        l = mul2(l, pair2(f, f));
         if (j > 0) {
           // the products of the tile before are complete: this S was issued after them
 #pragma unroll 1
@@ -400,29 +437,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
           }
         }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t sc = pair2(P.scale, P.scale), mm = pair2(-m, -m);
+      uint64_t sum = l, sum1 = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float e0 = ex2(fmaf(x[32 * q + 2 * c], P.scale, -m));
-          const float e1 = ex2(fmaf(x[32 * q + 2 * c + 1], P.scale, -m));
-          sum[2 * (c & 1)] += e0;
-          sum[2 * (c & 1) + 1] += e1;
+          float e0, e1;
+          split2(fma2(pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]), sc, mm), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          uint64_t& s = c & 1 ? sum1 : sum;
+          s = add2(s, pair2(e0, e1));
           w[c] = bf2(e0, e1);
         }
         tc_st_rows<16>(tm_s + 16 * q, w);
+        if (q & 1) {
+          // the product over these 64 keys may start
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(&sm.p_full[t][q >> 1]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sm.p_full[t]);
+      l = add2(sum, sum1);
     }
     if (ntt > 0) {
       wait_or_die(&sm.o_full[t], 0, dead, err);
       tc_fence_after();
-      const float inv = 1.f / l;
+      float l0, l1;
+      split2(l, l0, l1);
+      const float inv = 1.f / (l0 + l1);
       uint4* out = reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i) * P.a.Hq + h) * DH);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -458,8 +503,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
             tma_load_3d(qs + t * kQTile + c * kSlot, &P.q_map, c * 64, h, b * n_q + i0 + t * kTile, &sm.q_full[t], keep);
         }
     }
+    // Key tile j takes the ring's next five slots: K 0..2, V 3..4.  Eight slots before, slot
+    // 0 held the last of K(j - 2), 1 and 2 V(j - 2), 3 and 4 the first of K(j - 1).
     const int row0 = (b * P.a.Hq + h) * P.T;
-    uint32_t n = 0;
+    int nk = 0, nv = 0;  // tiles whose copies were started
     bool alive = true;
     for (int jb = 0; alive && jb < nmax; jb += 8) {
       // lane l looks up block 4 jb + l
@@ -469,35 +516,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
       const int je = min(jb + 8, nmax);
 #pragma unroll 1
-      for (int j = jb; alive && j < je; ++j)
-#pragma unroll
-        for (int c = 0; c < 5; ++c) {
-          const uint32_t s = n % kSlots, round = n / kSlots;
-          alive = alive && (round == 0 || warp_wait(&sm.empty[s], (round - 1) & 1, dead, err));
-          if (!alive) break;
-          uint8_t* dst = ring + s * kSlot;
-          if (c == 2) {
-            const int i = 4 * (j - jb);
-            if (elect_one()) mbar_arrive_expect_tx(&sm.full[s], __popc((have >> i) & 15u) * kBlockBytes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint8_t* mk = lane_ptr(map, i + k);
-              const int yk = __shfl_sync(0xffffffffu, y0, i + k);
-              if (mk && elect_one()) tma_load_3d(dst + k * kBlockBytes, mk, 0, yk, R / 64, &sm.full[s], keep);
-            }
-          } else if (elect_one()) {
-            mbar_arrive_expect_tx(&sm.full[s], kSlot);
-            if (c < 2)
-              tma_load_2d(dst, &P.k_map, c * 64, row0 + j * kTile, &sm.full[s], keep);
-            else
-              for (int k = 0; k < 2; ++k)
-                tma_load_2d(dst + k * (kSlot / 2), &P.v_map, k * 64, row0 + j * kTile + (c - 3) * 64, &sm.full[s], keep);
-          }
-          ++n;
+      for (int j = jb; j < je; ++j) {
+        const int i = 4 * (j - jb), par = j & 1, rd = (j >> 1) & 1;
+        auto slot = [&](int c) { return ring + ((5 * (uint32_t)j + c) % kSlots) * kSlot; };
+        if (j >= 2) alive = warp_wait(&sm.k_empty[par], rd ^ 1, dead, err);
+        if (!alive) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.k_full[par], 2 * kSlot + __popc((have >> i) & 15u) * kBlockBytes);
+          tma_load_2d(slot(0), &P.k_map, 0, row0 + j * kTile, &sm.k_full[par], keep);
         }
+        ++nk;
+        if (j >= 2) alive = warp_wait(&sm.v_empty[par], rd ^ 1, dead, err);
+        if (!alive) break;
+        if (elect_one()) tma_load_2d(slot(1), &P.k_map, 64, row0 + j * kTile, &sm.k_full[par], keep);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint8_t* mk = lane_ptr(map, i + k);
+          const int yk = __shfl_sync(0xffffffffu, y0, i + k);
+          if (mk && elect_one()) tma_load_3d(slot(2) + k * kBlockBytes, mk, 0, yk, R / 64, &sm.k_full[par], keep);
+        }
+        if (j >= 1) alive = warp_wait(&sm.k_empty[par ^ 1], ((j - 1) >> 1) & 1, dead, err);
+        if (!alive) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.v_full[par], 2 * kSlot);
+          for (int c = 0; c < 2; ++c)
+            for (int k = 0; k < 2; ++k)
+              tma_load_2d(slot(3 + c) + k * (kSlot / 2), &P.v_map, k * 64, row0 + j * kTile + c * 64, &sm.v_full[par], keep);
+        }
+        ++nv;
+      }
     }
-    for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i)
-      mbar_wait_bounded(&sm.full[i % kSlots], (i / kSlots) & 1, err);
+    // No copy may be in flight when the CTA ends.  (A role that gave up between the copies of
+    // one K tile leaves its barrier short of bytes: that wait runs into its limit.)
+    for (int j = max(0, nk - 2); j < nk; ++j) mbar_wait_bounded(&sm.k_full[j & 1], (j >> 1) & 1, err);
+    for (int j = max(0, nv - 2); j < nv; ++j) mbar_wait_bounded(&sm.v_full[j & 1], (j >> 1) & 1, err);
     if (nt0 > 0) mbar_wait_bounded(&sm.q_full[0], 0, err);
     if (nt1 > 0) mbar_wait_bounded(&sm.q_full[1], 0, err);
   } else if (warp == 9) {
@@ -507,20 +559,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ring), 16, 1024);
     const uint64_t d_v = tc_desc(smem_u32(ring), kSlot / 2, 1024);  // [2 x 64 values][64 keys], MN-major
     bool alive = true;
-    auto slot_full = [&](uint32_t n) {
-      alive = alive && warp_wait(&sm.full[n % kSlots], (n / kSlots) & 1, dead, err);
-      return alive;
-    };
-    // O_t += P_t(j) V(j), 64 keys from each slot
+    auto ready = [&](uint64_t* bar, int parity) { alive = alive && warp_wait(bar, parity, dead, err); };
+    // O_t += P_t(j) V(j), 64 keys at a time: the first half starts under the softmax of the second
     auto add_values = [&](int t, int j, int ntt) {
-      alive = alive && warp_wait(&sm.p_full[t], j & 1, dead, err);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const uint32_t n = 5 * (uint32_t)j + 3 + c;
-        if (!slot_full(n)) return;
+        ready(&sm.p_full[t][c], j & 1);
+        if (!alive) return;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t v = d_v + (((n % kSlots) * kSlot) >> 4);
+          const uint64_t v = d_v + ((((5 * (uint32_t)j + 3 + c) % kSlots) * kSlot) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma_ts(tmem + 2 * kTile + t * kTile, tmem + t * kTile + 32 * c + 8 * k, v + (k * 2048 >> 4), id_o,
@@ -531,31 +579,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     };
     // S_t = Q_t K(j)^T
     auto logits = [&](int t, int j) {
-      if (j == 0) alive = alive && warp_wait(&sm.q_full[t], 0, dead, err);
+      if (j == 0) ready(&sm.q_full[t], 0);
+      if (!alive) return;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const uint32_t n = 5 * (uint32_t)j + c;
-        if (!slot_full(n)) return;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t q = d_q + ((t * kQTile + c * kSlot) >> 4), k0 = d_k + (((n % kSlots) * kSlot) >> 4);
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t q = d_q + ((t * kQTile + c * kSlot) >> 4);
+          const uint64_t k0 = d_k + ((((5 * (uint32_t)j + c) % kSlots) * kSlot) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma(tmem + t * kTile, q + (k * 32 >> 4), k0 + (k * 32 >> 4), id_s, c > 0 || k > 0);
-          if (c == 2) tc_commit(&sm.s_full[t]);
         }
+        tc_commit(&sm.s_full[t]);
       }
     };
 #pragma unroll 1
     for (int j = 0; alive && j <= nmax; ++j) {
+      const int par = j & 1;
+      if (j > 0) ready(&sm.v_full[par ^ 1], ((j - 1) >> 1) & 1);
       if (j > 0 && j - 1 < nt0) add_values(0, j - 1, nt0);
+      if (j < nmax) ready(&sm.k_full[par], (j >> 1) & 1);
       if (j < nt0) logits(0, j);
       if (j > 0 && j - 1 < nt1) add_values(1, j - 1, nt1);
-      if (j > 0 && alive && elect_one())
-        for (int c = 3; c < 5; ++c) tc_commit(&sm.empty[(5 * (uint32_t)(j - 1) + c) % kSlots]);
+      if (j > 0 && alive && elect_one()) tc_commit(&sm.v_empty[par ^ 1]);
       if (j < nt1) logits(1, j);
-      if (j < nmax && alive && elect_one())
-        for (int c = 0; c < 3; ++c) tc_commit(&sm.empty[(5 * (uint32_t)j + c) % kSlots]);
+      if (j < nmax && alive && elect_one()) tc_commit(&sm.k_empty[par]);
     }
     __syncwarp();
     if (elect_one()) tc_commit(&sm.drain);
