@@ -147,20 +147,37 @@ def _check(status: int, what: str):
         raise PkvError(status, what, detail)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_raw_stream = None  # (device -> handle of its current stream, current device), once CUDA runs
 
 
 def _stream(stream=None) -> int:
-    torch = _torch()
+    global _raw_stream
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            torch = _torch()
+            handle = torch.cuda.current_stream().cuda_stream  # initialises CUDA, or raises
+            _raw_stream = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+            return handle
+        return _raw_stream[0](_raw_stream[1]())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dev(t, dtype, name: str, shape=None):
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -175,6 +192,8 @@ def _dev(t, dtype, name: str, shape=None):
 def _dev_strided(t, dtype, name: str, shape):
     """Like _dev, for a tensor whose last dimension alone has to be contiguous."""
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.stride(-1) == 1:
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -189,7 +208,7 @@ def _dev_strided(t, dtype, name: str, shape):
 def _row_stride(t, name: str) -> int:
     """The one distance between consecutive rows (every leading dimension) of `t`."""
     step, rows = None, 1
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(t.shape[-2::-1], t.stride()[-2::-1]):
         if n != 1:
             if step is None:
                 step = st
@@ -241,6 +260,7 @@ class Pool:
         _check(st, "pool_create")
         self._h = h
         self._ws = {}
+        self._ws_bytes = {}  # latent_workspace_bytes by (B, n_q, Hq)
         s = self.stats()
         self.row_bytes = s["row_bytes"][: s["n_kinds"]]
 
@@ -362,6 +382,7 @@ class Pool:
     def decode_set_ctas(self, n_ctas: int):
         _check(self._lib.pkv_decode_set_ctas(self._h, n_ctas), "decode_set_ctas")
         self._ws = {}
+        self._ws_bytes = {}
 
     def paged_decode_attention(self, layer: int, q, block_table, ctx_lens, scale: float, max_ctx: int = 0,
                                out=None, workspace=None, stream=None):
@@ -485,13 +506,18 @@ class Pool:
             raise ValueError("block_table must be [B, max_blocks]")
         if out is None:
             out = torch.empty(lead + (R,), dtype=torch.bfloat16, device=q_latent.device)
-        workspace = self._step_workspace(workspace, self.latent_workspace_bytes(B, n_q, Hq), q_latent.device, stream)
+        if workspace is None:
+            key = (B, n_q, Hq)
+            need = self._ws_bytes.get(key)
+            if need is None:
+                need = self._ws_bytes[key] = self.latent_workspace_bytes(B, n_q, Hq)
+            workspace = self._own_workspace(need, q_latent.device, stream)
         _check(self._lib.pkv_paged_latent_attention(
             self._h, layer, B, n_q, Hq, ql, _row_stride(q_latent, "q_latent"), qr, _row_stride(q_rope, "q_rope"),
             _dev(block_table, torch.int32, "block_table"), int(block_table.shape[1]),
             _dev(ctx_lens, torch.int32, "ctx_lens", (B,)), int(max_ctx), float(scale),
-            _dev(out, torch.bfloat16, "out", lead + (R,)), workspace.data_ptr(), int(workspace.numel()),
-            _stream(stream)), "paged_latent_attention")
+            _dev(out, torch.bfloat16, "out", lead + (R,)), _dev(workspace, torch.uint8, "workspace"),
+            workspace.numel(), _stream(stream)), "paged_latent_attention")
         return out
 
     def latent_prefill_workspace_bytes(self, B: int, n_q: int, Hq: int, max_blocks: int, max_ctx: int = 0) -> int:
@@ -516,26 +542,22 @@ class Pool:
         mb = int(block_table.shape[1])
         if out is None:
             out = torch.empty((B, n_q, Hq, D), dtype=torch.bfloat16, device=q.device)
-        need = self.latent_prefill_workspace_bytes(B, n_q, Hq, mb, int(max_ctx))
-        workspace = self._step_workspace(workspace, need, q.device, stream)
+        if workspace is None:
+            need = self.latent_prefill_workspace_bytes(B, n_q, Hq, mb, int(max_ctx))
+            workspace = self._own_workspace(need, q.device, stream)
         _check(self._lib.pkv_latent_prefill_attention(
             self._h, layer, B, n_q, Hq, _dev(q, torch.bfloat16, "q", (B, n_q, Hq, D + P)),
             _dev(w_k, torch.bfloat16, "w_k", (Hq, D, R)), _dev(w_v, torch.bfloat16, "w_v", (Hq, D, R)),
             _dev(block_table, torch.int32, "block_table"), mb, _dev(ctx_lens, torch.int32, "ctx_lens", (B,)),
-            int(max_ctx), float(scale), _dev(out, torch.bfloat16, "out", (B, n_q, Hq, D)), workspace.data_ptr(),
-            int(workspace.numel()), _stream(stream)), "latent_prefill_attention")
+            int(max_ctx), float(scale), _dev(out, torch.bfloat16, "out", (B, n_q, Hq, D)),
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "latent_prefill_attention")
         return out
 
     @staticmethod
-    def _step_workspace(workspace, nbytes: int, device, stream):
-        """The caller's workspace, or memory of this call alone: two calls on two streams, or in
-        two captured graphs, share none."""
+    def _own_workspace(nbytes: int, device, stream):
+        """Memory of one call alone: two calls on two streams, or in two captured graphs, share
+        none."""
         torch = _torch()
-        if workspace is not None:
-            if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or workspace.dtype != torch.uint8 \
-                    or not workspace.is_contiguous():
-                raise TypeError("workspace must be a contiguous CUDA uint8 tensor")
-            return workspace
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         if stream is not None:
             # made on the current stream, used on another

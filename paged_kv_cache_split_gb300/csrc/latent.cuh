@@ -59,6 +59,7 @@ struct LatentAttnArgs {
   uint16_t* out;             // [B, n_q, Hq, R]
   void* ws;
   int ctas;                  // CTAs a launch may use at once (one per SM)
+  int device;                // the pool's, current at the call
   cudaStream_t stream;
 };
 size_t latent_attn_workspace(int R, int B, int n_q, int Hq, int ctas);
@@ -77,6 +78,7 @@ struct LatentPrefillArgs {
   uint16_t* out;             // [B, n_q, Hq, kLatentHead]
   void* ws;
   int ctas;
+  int device;
   cudaStream_t stream;
 };
 size_t latent_prefill_workspace(int B, int Hq, int max_ctx);

@@ -676,30 +676,14 @@ Geometry geometry(int R, int B, int n_q, int Hq, int ctas) {
   return g;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, unsigned grid, int threads, size_t smem, const Params& P) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = P.a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P);
-}
-
 template <int R, int N>
 cudaError_t launch_rn(const Params& P) {
-  static_assert(sizeof(Params) <= 4096, "kernel parameters");
-  cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<R, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Plan<R, N>::kSmem);
+  static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is set
+  const cudaError_t e = tc_launch(latent_attn_kernel<R, N>, dim3((unsigned)(P.groups * P.n_rt)), kThreads,
+                                  (size_t)Plan<R, N>::kSmem, P.a.stream, P, P.a.device, &raised);
   if (e != cudaSuccess) return e;
-  e = launch(latent_attn_kernel<R, N>, (unsigned)(P.groups * P.n_rt), kThreads, Plan<R, N>::kSmem, P);
-  if (e != cudaSuccess) return e;
-  return launch(latent_combine_kernel<R, N>, (unsigned)((int64_t)P.a.B * P.rows), 128, 0, P);
+  return tc_launch(latent_combine_kernel<R, N>, dim3((unsigned)((int64_t)P.a.B * P.rows)), 128, (size_t)0, P.a.stream, P,
+                   P.a.device, &raised);
 }
 
 }  // namespace

@@ -62,7 +62,7 @@ __device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int 
 // (from L2, through a ring of 64-wide k-chunks); two accumulators of 256 columns let the
 // epilogue of one item run under the products of the next.
 // ---------------------------------------------------------------------------
-constexpr int kExpandThreads = 192;  // warps 0..3 epilogue, 4 copies, 5 MMAs
+constexpr int kExpandThreads = 320;  // warps 0..3 store keys, 4..7 values; 8 copies, 9 MMAs
 constexpr int kWStages = 3;
 constexpr int kWStage = 2 * kSlot;
 
@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C; ++i) mbar_init(&sm.a_full[i], 1), mbar_init(&sm.a_empty[i], 1);
     for (int i = 0; i < kWStages; ++i) mbar_init(&sm.w_full[i], 1), mbar_init(&sm.w_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_free[i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.d_full[i], 1), mbar_init(&sm.d_free[i], 256);
     mbar_init(&sm.drain, 1);
     sm.dead = 0;
     fence_mbar_init();
   }
-  if (warp == 5) tc_alloc(&sm.tmem, 512);
+  if (warp == 9) tc_alloc(&sm.tmem, 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
@@ -142,48 +142,58 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   it.start(P);
   bool new_tile;
 
-  if (warp < 4) {
+  if (warp < 8) {
+    const int kind = warp >> 2;  // 0: keys, 1: values
     for (int n = 0; it.next(P, n == 0, &new_tile); ++n) {
-      const int t = it.tile * kTile + threadIdx.x, L = it.len;
-      const int partner = t ^ 1;
+      const int t = it.tile * kTile + (threadIdx.x & 127), L = it.len;
       wait_or_die(&sm.d_full[n & 1], (n >> 1) & 1, dead, err);
       tc_fence_after();
-      const int64_t base = ((int64_t)it.b * P.a.Hq + it.h) * P.T;
-      // Pairs of lanes exchange 16-byte pieces so that each store of the pair fills a
-      // 32-byte sector of one row.  Rows past the context become zero: their values meet
-      // probabilities of zero in the attention, which a NaN would survive.
-      const bool odd = lane & 1;
+      // first of the eight rows that this lane's group of eight stores together
+      const int64_t row0 = ((int64_t)it.b * P.a.Hq + it.h) * P.T + (t & ~7);
 #pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        uint32_t r[32];
-        tc_ld_rows<32>(tmem + (n & 1) * 256 + q * 32 + ((uint32_t)(warp * 32) << 16), r);
-        tc_wait_ld();
-        uint32_t w[16];
+      for (int q = 0; q < 2; ++q) {
+        // 64 columns of this thread's row as eight 16-byte pieces.  Rows past the context
+        // become zero: their values meet probabilities of zero in the attention, which a
+        // NaN would survive.
+        uint32_t v[8][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = t < L ? bf2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
-        uint16_t* dst = (q < 4 ? P.k : P.v) + (q & 3) * 32;
-        uint4* own = reinterpret_cast<uint4*>(dst + (base + t) * DH);
-        uint4* other = reinterpret_cast<uint4*>(dst + (base + partner) * DH);
-        uint4* even_row = odd ? other : own;
-        uint4* odd_row = odd ? own : other;
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[32];
+          tc_ld_rows<32>(tmem + (n & 1) * 256 + kind * DH + q * 64 + half * 32 + ((uint32_t)((warp & 3) * 32) << 16), r);
+          tc_wait_ld();
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t got[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            got[i] = __shfl_xor_sync(0xffffffffu, odd ? w[8 * p + i] : w[8 * p + 4 + i], 1);
-          const uint4 g = make_uint4(got[0], got[1], got[2], got[3]);
-          const uint4 lo = make_uint4(w[8 * p], w[8 * p + 1], w[8 * p + 2], w[8 * p + 3]);
-          const uint4 hi = make_uint4(w[8 * p + 4], w[8 * p + 5], w[8 * p + 6], w[8 * p + 7]);
-          even_row[2 * p + odd] = odd ? g : lo;
-          odd_row[2 * p + odd] = odd ? hi : g;
+          for (int i = 0; i < 16; ++i)
+            v[4 * half + (i >> 2)][i & 3] =
+                t < L ? bf2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
         }
+        // Transpose the pieces among eight lanes, so that lane l holds piece l of eight rows
+        // and a store of the group fills a 128-byte line (one thread's own row, 16 bytes a
+        // store, took twice as long as the products).
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1) {
+          const bool up = lane & s;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(i & s)) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[i][e] : v[i | s][e], s);
+                if (up)
+                  v[i][e] = got;
+                else
+                  v[i | s][e] = got;
+              }
+            }
+        }
+        uint16_t* dst = (kind ? P.v : P.k) + row0 * DH + q * 64 + (lane & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(dst + i * DH) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
       }
       tc_fence_before();
       mbar_arrive(&sm.d_free[n & 1]);
     }
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     const uint64_t keep = l2_policy_evict_normal();
     uint32_t nw = 0, na = 0, s = 0, round = 0, tiles = 0;
     const uint8_t* map = nullptr;
@@ -263,7 +273,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tc_dealloc(tmem, 512);
+  if (warp == 9) tc_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -619,22 +629,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
 
 int tile_up(int x) { return (x + kTile - 1) / kTile * kTile; }
 
-template <typename K>
-cudaError_t launch(K kernel, dim3 grid, int threads, size_t smem, const Params& P) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = P.a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, P);
-}
-
 }  // namespace
 
 size_t latent_prefill_workspace(int B, int Hq, int max_ctx) {
@@ -665,8 +659,10 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
     const int64_t items = (int64_t)tiles * a.B * a.Hq;  // at most
     const dim3 grid((unsigned)(items < a.ctas ? items : a.ctas));
     const size_t smem = kSmall + (size_t)(a.R / 64) * kSlot + kWStages * kWStage;
-    const cudaError_t e = a.R == 512 ? launch(latent_expand_kernel<512>, grid, kExpandThreads, smem, P)
-                                     : launch(latent_expand_kernel<256>, grid, kExpandThreads, smem, P);
+    static std::atomic<uint64_t> raised[2];
+    const cudaError_t e =
+        a.R == 512 ? tc_launch(latent_expand_kernel<512>, grid, kExpandThreads, smem, a.stream, P, a.device, &raised[0])
+                   : tc_launch(latent_expand_kernel<256>, grid, kExpandThreads, smem, a.stream, P, a.device, &raised[1]);
     if (e != cudaSuccess) return e;
   }
   static const int regs = [] {
@@ -674,8 +670,9 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
     return cudaFuncGetAttributes(&fa, latent_prefill_kernel) == cudaSuccess ? fa.numRegs : -1;
   }();
   if (regs != kAttnRegs) return cudaErrorInvalidDeviceFunction;
-  return launch(latent_prefill_kernel, dim3((unsigned)((int64_t)P.pairs * a.B * a.Hq)), kAttnThreads,
-                kSmall + 2 * kQTile + kSlots * kSlot, P);
+  static std::atomic<uint64_t> raised{0};
+  return tc_launch(latent_prefill_kernel, dim3((unsigned)((int64_t)P.pairs * a.B * a.Hq)), kAttnThreads,
+                   (size_t)(kSmall + 2 * kQTile + kSlots * kSlot), a.stream, P, a.device, &raised);
 }
 
 }  // namespace pkv

@@ -806,6 +806,7 @@ pkv_status pkv_paged_latent_attention(pkv_pool* p, int layer, int B, int n_q, in
     return PKV_ERR_INVALID;
   LatentAttnArgs a;
   a.ctas = decode_grid(p);
+  a.device = p->device;
   if (ws_bytes < latent_attn_workspace(R, B, n_q, Hq, a.ctas)) return PKV_ERR_INVALID;
   a.lv = layer_view(p, layer);
   a.R = R;
@@ -880,6 +881,7 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   a.out = (uint16_t*)out;
   a.ws = ws;
   a.ctas = p->n_sm;
+  a.device = p->device;
   a.stream = (cudaStream_t)stream;
   PKV_CUDA(launch_latent_prefill(a), "latent_prefill_attention launch");
   p->last_stream = a.stream;

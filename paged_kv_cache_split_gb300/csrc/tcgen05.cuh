@@ -5,6 +5,8 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -199,5 +201,29 @@ __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Launch with programmatic dependence on the stream's previous kernel (the kernels wait
+// for it before they touch global memory).  The shared-memory limit of a kernel is raised
+// once per device.
+template <typename P>
+inline cudaError_t tc_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p,
+                             int device, std::atomic<uint64_t>* raised) {
+  if (smem > 48 * 1024 && !(device < 64 && (raised->load(std::memory_order_relaxed) >> device & 1))) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) raised->fetch_or(1ull << device);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace pkv
