@@ -45,6 +45,7 @@ constexpr float kSlack = 8.0f;        // log2 of how far a logit may pass the re
 constexpr float kNoMax = -1e30f;      // the reference before any visible token
 constexpr int kSmemLimit = 232448;    // 227 KB opt-in shared memory per block
 constexpr int kSmall = 3072;          // alignment (1024), barriers and per-row values
+constexpr int kInFlight = 8;          // more tiles than the rings hold
 
 // Cost of a sequence's start in quarter tiles, in the split over the CTAs: its queries are
 // loaded and its output or record written.
@@ -67,11 +68,13 @@ struct Plan {
   static constexpr int kTmemUsed = (2 + kPairs) * N;  // two S^T buffers, O^T
   static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static_assert(kPairSlots >= 2 * kPairs && kRopeSlots >= 2, "two tiles have to fit");
+  static_assert(kRopeSlots < kInFlight && kPairSlots < kInFlight * kPairs, "tiles in flight");
   static_assert(kSmem <= kSmemLimit && kTmemUsed <= 512, "shared memory or TMEM");
 };
 
 struct Params {
   LatentAttnArgs a;
+  CUtensorMap ql_map, qr_map;  // the queries' rows, in boxes of 64 values x N rows
   int rows;     // n_q * Hq: rows of a sequence
   int n_rt;     // row tiles of a sequence
   int groups;   // CTAs along the token axis (each with n_rt row tiles)
@@ -125,16 +128,24 @@ struct Walk {
   }
 };
 
-// One warp: the CTA's positions and the sequence its walk starts at.
+// One warp: the CTA's positions and the sequence its walk starts at.  The lengths of the
+// first kHeld sequences are read once.
 template <int N>
 __device__ __forceinline__ Walk start_walk(const Params& P, int rt, int group) {
+  constexpr int kHeld = 128;
   const int lane = threadIdx.x & 31;
-  int32_t len;
+  auto tiles = [&](int b) -> int32_t {
+    int32_t len;
+    return b < P.a.B ? (visible<N>(P, b, rt, &len) + kTile - 1) / kTile : 0;
+  };
+  int32_t held[kHeld / 32];
   int64_t total = 0;
-  for (int base = 0; base < P.a.B; base += 32) {
-    const int b = base + lane;
-    total += b < P.a.B ? (visible<N>(P, b, rt, &len) + kTile - 1) / kTile : 0;
+#pragma unroll
+  for (int c = 0; c < kHeld / 32; ++c) {
+    held[c] = 32 * c < P.a.B ? tiles(32 * c + lane) : 0;
+    total += held[c];
   }
+  for (int b = kHeld + lane; b < P.a.B; b += 32) total += tiles(b);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   Walk w;
@@ -145,26 +156,31 @@ __device__ __forceinline__ Walk start_walk(const Params& P, int rt, int group) {
   w.b = P.a.B;
   w.up = total;
   int64_t carry = 0;
-  for (int base = 0; base < P.a.B; base += 32) {
-    const int b = base + lane;
-    const int64_t n = b < P.a.B ? (visible<N>(P, b, rt, &len) + kTile - 1) / kTile : 0;
-    int64_t inc = n;
+  // the first sequence whose last tile reaches the CTA's first position
+  auto found = [&](int base, int32_t n) {
+    int32_t inc = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      const int32_t y = __shfl_up_sync(0xffffffffu, inc, off);
       if (lane >= off) inc += y;
     }
-    // the first sequence whose last tile reaches the CTA's first position
+    const int b = base + lane;
     const unsigned hit = __ballot_sync(
         0xffffffffu, b < P.a.B && kCost * (carry + inc - 1) + (int64_t)kSegCost * (b + 1) >= w.lo);
     if (hit) {
       const int l = __ffs(hit) - 1;
       w.b = base + l;
       w.up = carry + __shfl_sync(0xffffffffu, inc - n, l);
-      break;
+      return true;
     }
     carry += __shfl_sync(0xffffffffu, inc, 31);
-  }
+    return false;
+  };
+#pragma unroll
+  for (int c = 0; c < kHeld / 32; ++c)
+    if (32 * c < P.a.B && found(32 * c, held[c])) return w;
+  for (int base = kHeld; base < P.a.B; base += 32)
+    if (found(base, tiles(base + lane))) return w;
   return w;
 }
 
@@ -172,9 +188,9 @@ __device__ __forceinline__ Walk start_walk(const Params& P, int rt, int group) {
 template <int R, int N>
 struct Small {
   using L = Plan<R, N>;
-  uint64_t pair_full[L::kPairSlots], pair_empty[L::kPairSlots];
-  uint64_t rope_full[L::kRopeSlots], rope_empty[L::kRopeSlots];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, drain;
+  uint64_t full[kInFlight];  // by tile: its position keys and all of its latent slots
+  uint64_t pair_empty[L::kPairSlots], rope_empty[L::kRopeSlots];
+  uint64_t s_full[2], p_full, pv_done, q_full, q_empty, drain;
   Walk walk;
   uint32_t tmem;
   int dead;          // a wait gave up: every role runs on without waiting or issuing
@@ -211,12 +227,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   int32_t* err = P.a.lv.err;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kPairSlots; ++i) mbar_init(&sm.pair_full[i], 1), mbar_init(&sm.pair_empty[i], 1);
-    for (int i = 0; i < L::kRopeSlots; ++i) mbar_init(&sm.rope_full[i], 1), mbar_init(&sm.rope_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1), mbar_init(&sm.s_free[i], kSoftmaxThreads);
+    for (int i = 0; i < kInFlight; ++i) mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < L::kPairSlots; ++i) mbar_init(&sm.pair_empty[i], 1);
+    for (int i = 0; i < L::kRopeSlots; ++i) mbar_init(&sm.rope_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1);
     mbar_init(&sm.p_full, kSoftmaxThreads);
     mbar_init(&sm.pv_done, 1);
-    mbar_init(&sm.q_full, kSoftmaxThreads);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.drain, 1);
     sm.dead = 0;
     fence_mbar_init();
@@ -245,25 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     int it = 0;
     while (walk.next<N>(P, rt, seg)) {
       const int row0 = rt * N, nrow = min(N, P.rows - row0);
-      // The queries of the tile, in chunks of 64 values, swizzled as the copies are.
-      constexpr int CH = (R + kRope) / 8;
       const int64_t qrow = (int64_t)seg.b * P.rows + row0;
-      for (int i = tid; i < N * CH; i += kSoftmaxThreads) {
-        const int r = i / CH, ch = i - r * CH;
-        const bool ok = r < nrow;
-        const uint16_t* src = !ok            ? P.a.ql
-                              : ch < R / 8   ? P.a.ql + (qrow + r) * P.a.ql_stride + ch * 8
-                                             : P.a.qr + (qrow + r) * P.a.qr_stride + (ch - R / 8) * 8;
-        cp_async16(smem_u32(qs) + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, ok);
-      }
       if (tid < N) {
         const int r = min(row0 + tid, P.rows - 1);
         sm.vis[tid] = seg.len - P.a.n_q + r / P.a.Hq + 1;
       }
       const int vis_first = seg.len - P.a.n_q + row0 / P.a.Hq + 1;
-      cp_async_wait_all();
-      fence_async_shared();
-      mbar_arrive(&sm.q_full);
       softmax_any(false);  // sm.vis is ready
 #pragma unroll
       for (int k = 0; k < N / 4; ++k) m[k] = kNoMax, l[k] = 0.f;
@@ -277,8 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           uint32_t r[N / 2];
           tc_ld_frag16<N>(tm_s + buf * N + lanes, r);
           tc_wait_ld();
-          tc_fence_before();
-          mbar_arrive(&sm.s_free[buf]);
 #pragma unroll
           for (int k = 0; k < N / 2; ++k) x[k] = __uint_as_float(r[k]) * P.a.scale_log2;
         }
@@ -430,13 +433,28 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------------ copies
-    const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t keep = l2_policy_evict_normal();
+    const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : keep;
     uint32_t ps_ = 0, pround = 0, rs_ = 0, rround = 0;  // next slot and round of each ring
-    uint32_t np = 0, nr = 0;                            // slots filled so far
+    int n_tile = 0, n_seg = 0;                          // started so far
     bool alive = true;
+    // The row tile's queries (rows past the sequence's are other rows, or zero: unused).
+    auto copy_queries = [&](int qrow) {
+      if (n_seg > 0) alive = warp_wait(&sm.q_empty, (n_seg - 1) & 1, dead, err);
+      if (!alive) return;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.q_full, L::kQBytes);
+#pragma unroll 1
+        for (int c = 0; c < R / 64; ++c) tma_load_2d(qs + c * N * 128, &P.ql_map, 64 * c, qrow, &sm.q_full, keep);
+        tma_load_2d(qs + (R / 64) * N * 128, &P.qr_map, 0, qrow, &sm.q_full, keep);
+      }
+      ++n_seg;
+    };
     while (alive && walk.next<N>(P, rt, seg)) {
       const int nblk = (seg.vis + kBlockTokens - 1) / kBlockTokens;
       const int k0 = uniform(seg.k0), k1 = uniform(seg.k1);
+      const int qrow = uniform(seg.b * P.rows + rt * N);
+      if (n_seg == 0) copy_queries(qrow);
       for (int ub = k0; alive && ub < k1; ub += 16) {
         // lane l looks up block 2 ub + l of the sequence
         const int j = 2 * ub + lane;
@@ -458,16 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           const int i = 2 * (u - ub);
           const uint8_t *m0 = lane_ptr(map, i), *m1 = lane_ptr(map, i + 1);
           const int ya = __shfl_sync(0xffffffffu, y0, i), yb = __shfl_sync(0xffffffffu, y0, i + 1);
-          const uint32_t bytes = ((m0 != nullptr) + (m1 != nullptr)) * kBlockBytes;
+          const uint32_t bytes = ((m0 != nullptr) + (m1 != nullptr)) * kBlockBytes * (R / 64 + 1);
+          uint64_t* full = &sm.full[n_tile % kInFlight];
           if (rround > 0) alive = warp_wait(&sm.rope_empty[rs_], (rround - 1) & 1, dead, err);
           if (!alive) break;
           if (elect_one()) {
             uint8_t* dst = ropes + rs_ * kChunkBytes;
-            mbar_arrive_expect_tx(&sm.rope_full[rs_], bytes);
-            if (m0) tma_load_3d(dst, m0, 0, ya, R / 64, &sm.rope_full[rs_], policy);
-            if (m1) tma_load_3d(dst + kBlockBytes, m1, 0, yb, R / 64, &sm.rope_full[rs_], policy);
+            mbar_arrive_expect_tx(full, bytes);
+            if (m0) tma_load_3d(dst, m0, 0, ya, R / 64, full, policy);
+            if (m1) tma_load_3d(dst + kBlockBytes, m1, 0, yb, R / 64, full, policy);
           }
-          ++nr;
+          ++n_tile;
           if (++rs_ == L::kRopeSlots) rs_ = 0, ++rround;
 #pragma unroll 1
           for (int p = 0; p < L::kPairs; ++p) {
@@ -475,28 +494,30 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             if (!alive) break;
             if (elect_one()) {
               uint8_t* dst = pairs + ps_ * kPairBytes;
-              mbar_arrive_expect_tx(&sm.pair_full[ps_], 2 * bytes);
               if (m0) {
-                tma_load_3d(dst, m0, 0, ya, 2 * p, &sm.pair_full[ps_], policy);
-                tma_load_3d(dst + kChunkBytes, m0, 0, ya, 2 * p + 1, &sm.pair_full[ps_], policy);
+                tma_load_3d(dst, m0, 0, ya, 2 * p, full, policy);
+                tma_load_3d(dst + kChunkBytes, m0, 0, ya, 2 * p + 1, full, policy);
               }
               if (m1) {
-                tma_load_3d(dst + kBlockBytes, m1, 0, yb, 2 * p, &sm.pair_full[ps_], policy);
-                tma_load_3d(dst + kChunkBytes + kBlockBytes, m1, 0, yb, 2 * p + 1, &sm.pair_full[ps_], policy);
+                tma_load_3d(dst + kBlockBytes, m1, 0, yb, 2 * p, full, policy);
+                tma_load_3d(dst + kChunkBytes + kBlockBytes, m1, 0, yb, 2 * p + 1, full, policy);
               }
             }
-            ++np;
             if (++ps_ == L::kPairSlots) ps_ = 0, ++pround;
           }
+          if (!alive) break;
+          // a later segment's queries wait for the products of the one before: after its
+          // first tile, which needs no wait
+          if (u == k0 && n_tile > 1) copy_queries(qrow);
           if (!alive) break;
         }
       }
     }
-    // no copy may be in flight when the CTA ends
-    for (uint32_t i = np > L::kPairSlots ? np - L::kPairSlots : 0; i < np; ++i)
-      mbar_wait_bounded(&sm.pair_full[i % L::kPairSlots], (i / L::kPairSlots) & 1, err);
-    for (uint32_t i = nr > L::kRopeSlots ? nr - L::kRopeSlots : 0; i < nr; ++i)
-      mbar_wait_bounded(&sm.rope_full[i % L::kRopeSlots], (i / L::kRopeSlots) & 1, err);
+    // No copy may be in flight when the CTA ends.  (A role that gave up in the middle of a
+    // tile leaves its barrier short of bytes: that wait runs into its limit.)
+    for (int i = max(0, n_tile - kInFlight); i < n_tile; ++i)
+      mbar_wait_bounded(&sm.full[i % kInFlight], (i / kInFlight) & 1, err);
+    if (n_seg > 0) mbar_wait_bounded(&sm.q_full, (n_seg - 1) & 1, err);
   } else {
     // -------------------------------------------------------------------- MMAs
     constexpr uint32_t id_s = tc_idesc(64, N, false, false);
@@ -505,70 +526,64 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_p = tc_desc(smem_u32(ps), 16, 1024);
     const uint64_t d_v = tc_desc(smem_u32(pairs), kChunkBytes, 1024);
     int it = 0, n_seg = 0;
-    uint32_t ks = 0, kround = 0, vs = 0, rs_ = 0, rround = 0;  // slots of the next K, V and position keys
-    bool alive = true, pending = false, pending_first = false;
+    uint32_t ks = 0, vs = 0, rs_ = 0;  // slots of the next tile's K, V and position keys
+    bool alive = true, pending_first = false;
     // O^T (+)= V^T P^T of tile i
     auto add_values = [&](int i, bool first) {
       alive = alive && warp_wait(&sm.p_full, i & 1, dead, err);
       if (!alive) return;
       tc_fence_after();
-#pragma unroll 1
-      for (int mb = 0; mb < L::kPairs; ++mb) {
-        if (elect_one()) {
-          const uint64_t a = d_v + ((vs * kPairBytes) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int mb = 0; mb < L::kPairs; ++mb) {
+          const uint32_t slot = vs + mb < L::kPairSlots ? vs + mb : vs + mb - L::kPairSlots;
+          const uint64_t a = d_v + ((slot * kPairBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma(tm_o + mb * N, a + (k * 2048 >> 4), d_p + (k * 32 >> 4), id_o, !(first && k == 0));
-          tc_commit(&sm.pair_empty[vs]);
-          if (mb == L::kPairs - 1) tc_commit(&sm.pv_done);
+          tc_commit(&sm.pair_empty[slot]);
         }
-        if (++vs == L::kPairSlots) vs = 0;
+        tc_commit(&sm.pv_done);
       }
+      vs = vs + L::kPairs < L::kPairSlots ? vs + L::kPairs : vs + L::kPairs - L::kPairSlots;
     };
+    // The next tile's S^T is issued before this tile's values: it runs under the softmax.
+    // Its buffer is free: the softmax of the tile two before handed its P over, and the
+    // values of that P were issued.
     while (alive && walk.next<N>(P, rt, seg)) {
       const int k0 = uniform(seg.k0), k1 = uniform(seg.k1);
       for (int u = k0; alive && u < k1; ++u, ++it) {
         const bool first = u == k0;
-        if (first) {
-          if (pending) add_values(it - 1, pending_first);
-          pending = false;
-          alive = alive && warp_wait(&sm.q_full, n_seg & 1, dead, err);
-          ++n_seg;
-        }
         const int buf = it & 1;
-        if (it >= 2) alive = alive && warp_wait(&sm.s_free[buf], ((it >> 1) - 1) & 1, dead, err);
-        alive = alive && warp_wait(&sm.rope_full[rs_], rround & 1, dead, err);
+        if (first) alive = warp_wait(&sm.q_full, n_seg++ & 1, dead, err);
+        alive = alive && warp_wait(&sm.full[it % kInFlight], (it / kInFlight) & 1, dead, err);
         if (!alive) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t a = d_rope + ((rs_ * kChunkBytes) >> 4);
+          const uint64_t ar = d_rope + ((rs_ * kChunkBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma(tm_s + buf * N, a + (k * 32 >> 4), d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
+            tc_mma(tm_s + buf * N, ar + (k * 32 >> 4), d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
           tc_commit(&sm.rope_empty[rs_]);
-        }
-        if (++rs_ == L::kRopeSlots) rs_ = 0, ++rround;
-#pragma unroll 1
-        for (int p = 0; p < L::kPairs; ++p) {
-          alive = alive && warp_wait(&sm.pair_full[ks], kround & 1, dead, err);
-          if (!alive) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t a = d_pair + ((ks * kPairBytes) >> 4), q = d_q + ((2 * p * N * 128) >> 4);
+#pragma unroll
+          for (int p = 0; p < L::kPairs; ++p) {
+            const uint32_t slot = ks + p < L::kPairSlots ? ks + p : ks + p - L::kPairSlots;
+            const uint64_t a = d_pair + ((slot * kPairBytes) >> 4), q = d_q + ((2 * p * N * 128) >> 4);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               tc_mma(tm_s + buf * N, a + (((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
                      q + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), id_s, true);
-            if (p == L::kPairs - 1) tc_commit(&sm.s_full[buf]);
           }
-          if (++ks == L::kPairSlots) ks = 0, ++kround;
+          tc_commit(&sm.s_full[buf]);
+          if (u == k1 - 1) tc_commit(&sm.q_empty);
         }
-        if (pending) add_values(it - 1, pending_first);
-        pending = true;
+        if (++rs_ == L::kRopeSlots) rs_ = 0;
+        ks = ks + L::kPairs < L::kPairSlots ? ks + L::kPairs : ks + L::kPairs - L::kPairSlots;
+        if (it > 0) add_values(it - 1, pending_first);
         pending_first = first;
       }
     }
-    if (pending && alive) add_values(it - 1, pending_first);
+    if (it > 0 && alive) add_values(it - 1, pending_first);
     __syncwarp();
     if (elect_one()) tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
     mbar_wait_bounded(&sm.drain, 0, err);
@@ -590,6 +605,8 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_consta
   const int64_t row = blockIdx.x;
   const int b = (int)(row / P.rows), r = (int)(row % P.rows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = r / N, rr = r % N;
+  const int2 meta = P.meta[(size_t)b * P.n_rt + rt];  // (garbage where L is 0)
   bool bad;
   const int32_t L = latent_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
   uint16_t* out = P.a.out + row * R;
@@ -598,8 +615,6 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_consta
     for (int i = threadIdx.x; i < R / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int rt = r / N, rr = r % N;
-  const int2 meta = P.meta[(size_t)b * P.n_rt + rt];
   if (meta.x < 0) return;
   // records: the first in slot meta.x, then slot 0 of every later group's CTA
   const int g0 = (meta.x >> 1) / P.n_rt, n = meta.y - g0 + 1;
@@ -702,6 +717,12 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a) {
   P.meta = reinterpret_cast<int2*>(a.ws);
   P.ml = reinterpret_cast<float2*>((uint8_t*)a.ws + g.meta);
   P.acc = reinterpret_cast<float*>((uint8_t*)a.ws + g.ml);
+  const uint64_t rows = (uint64_t)a.B * g.rows;
+  const uint64_t ld[2] = {(uint64_t)a.R, rows}, rd[2] = {kRope, rows};
+  const uint64_t ls[1] = {(uint64_t)a.ql_stride * 2}, rs[1] = {(uint64_t)a.qr_stride * 2};
+  const uint32_t box[2] = {64, (uint32_t)g.N};
+  if (!encode_bf16_map(&P.ql_map, a.ql, 2, ld, ls, box) || !encode_bf16_map(&P.qr_map, a.qr, 2, rd, rs, box))
+    return cudaErrorInvalidValue;
   if (a.R == 512) {
     if (g.N == 16) return launch_rn<512, 16>(P);
     if (g.N == 32) return launch_rn<512, 32>(P);

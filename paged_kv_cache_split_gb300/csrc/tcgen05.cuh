@@ -197,11 +197,6 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Launch with programmatic dependence on the stream's previous kernel (the kernels wait
 // for it before they touch global memory).  The shared-memory limit of a kernel is raised
 // once per device.
