@@ -547,16 +547,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       }
       vs = vs + L::kPairs < L::kPairSlots ? vs + L::kPairs : vs + L::kPairs - L::kPairSlots;
     };
-    // The next tile's S^T is issued before this tile's values: it runs under the softmax.
-    // Its buffer is free: the softmax of the tile two before handed its P over, and the
-    // values of that P were issued.
+    // The next tile's S^T is issued before this tile's values where its rows have arrived: it
+    // runs under the softmax.  Where they have not, the values go first, so that their
+    // slots are refilled while the rows are on the way.  The S^T buffer is free either way:
+    // the softmax of the tile two before handed its P over, and its values were issued.
     while (alive && walk.next<N>(P, rt, seg)) {
       const int k0 = uniform(seg.k0), k1 = uniform(seg.k1);
       for (int u = k0; alive && u < k1; ++u, ++it) {
         const bool first = u == k0;
         const int buf = it & 1;
-        if (first) alive = warp_wait(&sm.q_full, n_seg++ & 1, dead, err);
-        alive = alive && warp_wait(&sm.full[it % kInFlight], (it / kInFlight) & 1, dead, err);
+        uint64_t* full = &sm.full[it % kInFlight];
+        const uint32_t par = (it / kInFlight) & 1;
+        const bool late = it > 0 && !__all_sync(0xffffffffu, mbar_test_wait(full, par));
+        if (late) add_values(it - 1, pending_first);
+        if (first) alive = alive && warp_wait(&sm.q_full, n_seg++ & 1, dead, err);
+        alive = alive && warp_wait(full, par, dead, err);
         if (!alive) break;
         tc_fence_after();
         if (elect_one()) {
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         }
         if (++rs_ == L::kRopeSlots) rs_ = 0;
         ks = ks + L::kPairs < L::kPairSlots ? ks + L::kPairs : ks + L::kPairs - L::kPairSlots;
-        if (it > 0) add_values(it - 1, pending_first);
+        if (it > 0 && !late) add_values(it - 1, pending_first);
         pending_first = first;
       }
     }
