@@ -12,6 +12,7 @@
 namespace pkv {
 
 constexpr int kRope = 64;        // values of the position key
+constexpr int kLatentQuad = 4;   // 64-value columns that one copy of a latent block's row moves
 constexpr int kLatentHead = 128; // expanded form: values of a head's key part and of its value
 
 // Limits checked at the entry points: they keep every index of the kernels' grids and
@@ -97,6 +98,30 @@ __device__ __forceinline__ uint8_t* latent_row(const LayerView& lv, int32_t row,
   const int32_t slab = row / lv.slab_blocks;
   const int32_t r = row - slab * lv.slab_blocks;
   return lv.tab.base[(size_t)slab * lv.tab.stride] + (size_t)(r * kBlockTokens + slot) * (size_t)lv.row_bytes[0];
+}
+
+// Copies of a block's 32 tokens into shared memory: four 64-value columns from column c
+// on, as [4 x 8 tokens][4 columns][8][128 bytes] (16 KB), or one column, as [32][128 bytes]
+// (4 KB).  `map` is the slab's first tensor map, y8 the block's first row / 8.
+__device__ __forceinline__ void latent_copy(void* dst, const void* map, int c, int y8, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(0), "r"(c), "r"(y8), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void latent_copy_quad(void* dst, const uint8_t* map, int c, int y8, uint64_t* bar,
+                                                 uint64_t policy) {
+  latent_copy(dst, map, c, y8, bar, policy);
+}
+__device__ __forceinline__ void latent_copy_column(void* dst, const uint8_t* map, int c, int y8, uint64_t* bar,
+                                                   uint64_t policy) {
+  latent_copy(dst, map + 128, c, y8, bar, policy);
+}
+// Both maps become visible to this thread's copies.
+__device__ __forceinline__ void latent_maps_acquire(const uint8_t* map) {
+  tensormap_acquire(map);
+  tensormap_acquire(map + 128);
 }
 
 // A context length as the attention uses it: 0 (an unused batch slot) stays 0; a

@@ -16,10 +16,10 @@
 // O^T stays in tensor memory (R / 128 blocks of N columns), S^T is double-buffered there.
 //
 // A CTA runs one warp that issues copies, one that issues MMAs and four for the softmax.
-// Cache rows arrive by TMA in boxes of 32 tokens x 64 values into a ring of 16 KB slots
-// (64 tokens x 128 latent values) and one of 8 KB slots (64 tokens' position keys); the
+// Cache rows arrive by TMA, 32 tokens x 256 values a copy, into a ring of 32 KB slots
+// (64 tokens x 256 latent values) and one of 8 KB slots (64 tokens' position keys); the
 // next tile's S^T product runs while the softmax works on this one, and a slot is refilled
-// as soon as its block of O^T has been added to.  The softmax reference m moves only when
+// as soon as its blocks of O^T have been added to.  The softmax reference m moves only when
 // a logit passes it by more than 2^8 (all rescaling of O^T is skipped otherwise): p is
 // then at most 2^8 and loses nothing in bf16, and the sums are FP32.
 //
@@ -38,9 +38,9 @@ namespace {
 constexpr int kTile = 64;             // tokens a tile
 constexpr int kSoftmaxThreads = 128;  // warps 0..3
 constexpr int kThreads = 192;         // + warp 4: copies, warp 5: MMAs
-constexpr int kChunkBytes = kTile * 128;      // 64 tokens x 64 values: one swizzled box column
-constexpr int kPairBytes = 2 * kChunkBytes;   // 64 tokens x 128 latent values
-constexpr int kBlockBytes = kBlockTokens * 128;  // what one copy moves: 32 tokens x 64 values
+constexpr int kChunkBytes = kTile * 128;               // 64 tokens x 64 values
+constexpr int kQuadBytes = kLatentQuad * kChunkBytes;  // 64 tokens x 256 values: [8 x 8 tokens][4][8][128 bytes]
+constexpr int kAtom = 1024;                            // eight tokens of a column: the swizzle's atom
 constexpr float kSlack = 8.0f;        // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -1e30f;      // the reference before any visible token
 constexpr int kSmemLimit = 232448;    // 227 KB opt-in shared memory per block
@@ -56,19 +56,19 @@ constexpr int kCost = 4;
 // slots are still held, so two tiles at least; what is left of shared memory goes to more.
 template <int R, int N>
 struct Plan {
-  static constexpr int kPairs = R / 128;  // latent slots a tile
+  static constexpr int kQuads = R / 256;  // latent slots a tile
   static constexpr int kQBytes = N * (R + kRope) * 2;
   static constexpr int kPBytes = N * 128;
   static constexpr int kRoom = kSmemLimit - kSmall - kQBytes - kPBytes;
-  static constexpr int kTileBytes = kPairs * kPairBytes + kChunkBytes;
+  static constexpr int kTileBytes = kQuads * kQuadBytes + kChunkBytes;
   static constexpr int kRopeSlots =
-      kRoom / kTileBytes + (kRoom % kTileBytes >= kPairBytes + kChunkBytes ? 1 : 0);
-  static constexpr int kPairSlots = (kRoom - kRopeSlots * kChunkBytes) / kPairBytes;
-  static constexpr int kSmem = kSmall + kQBytes + kPBytes + kPairSlots * kPairBytes + kRopeSlots * kChunkBytes;
-  static constexpr int kTmemUsed = (2 + kPairs) * N;  // two S^T buffers, O^T
+      kRoom / kTileBytes + (kRoom % kTileBytes >= kQuadBytes + kChunkBytes ? 1 : 0);
+  static constexpr int kQuadSlots = (kRoom - kRopeSlots * kChunkBytes) / kQuadBytes;
+  static constexpr int kSmem = kSmall + kQBytes + kPBytes + kQuadSlots * kQuadBytes + kRopeSlots * kChunkBytes;
+  static constexpr int kTmemUsed = (2 + R / 128) * N;  // two S^T buffers, O^T
   static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-  static_assert(kPairSlots >= 2 * kPairs && kRopeSlots >= 2, "two tiles have to fit");
-  static_assert(kRopeSlots < kInFlight && kPairSlots < kInFlight * kPairs, "tiles in flight");
+  static_assert(kQuadSlots >= 2 * kQuads && kRopeSlots >= 2, "two tiles have to fit");
+  static_assert(kRopeSlots < kInFlight && kQuadSlots < kInFlight * kQuads, "tiles in flight");
   static_assert(kSmem <= kSmemLimit && kTmemUsed <= 512, "shared memory or TMEM");
 };
 
@@ -189,7 +189,7 @@ template <int R, int N>
 struct Small {
   using L = Plan<R, N>;
   uint64_t full[kInFlight];  // by tile: its position keys and all of its latent slots
-  uint64_t pair_empty[L::kPairSlots], rope_empty[L::kRopeSlots];
+  uint64_t quad_empty[L::kQuadSlots], rope_empty[L::kRopeSlots];
   uint64_t s_full[2], p_full, pv_done, q_full, q_empty, drain;
   Walk walk;
   uint32_t tmem;
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   using L = Plan<R, N>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* pairs = smem;
-  uint8_t* ropes = pairs + L::kPairSlots * kPairBytes;
+  uint8_t* quads = smem;
+  uint8_t* ropes = quads + L::kQuadSlots * kQuadBytes;
   uint8_t* qs = ropes + L::kRopeSlots * kChunkBytes;
   uint8_t* ps = qs + L::kQBytes;
   Small<R, N>& sm = *reinterpret_cast<Small<R, N>*>(ps + L::kPBytes);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kInFlight; ++i) mbar_init(&sm.full[i], 1);
-    for (int i = 0; i < L::kPairSlots; ++i) mbar_init(&sm.pair_empty[i], 1);
+    for (int i = 0; i < L::kQuadSlots; ++i) mbar_init(&sm.quad_empty[i], 1);
     for (int i = 0; i < L::kRopeSlots; ++i) mbar_init(&sm.rope_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1);
     mbar_init(&sm.p_full, kSoftmaxThreads);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           softmax_any(false);
           if (u > seg.k0) {
 #pragma unroll 1
-            for (int mb = 0; mb < L::kPairs; ++mb)
+            for (int mb = 0; mb < R / 128; ++mb)
 #pragma unroll 1
               for (int q = 0; q < N; q += 16) {
                 uint32_t o[16];
@@ -367,12 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         // become zero; their keys only reached logits that were masked.
         const int valid = seg.vis - u * kTile;
         if (valid < kTile) {
-          const int per = (kTile - valid) * 8;  // 16-byte pieces of a chunk
-          for (int i = tid; i < per * 2 * L::kPairs; i += kSoftmaxThreads) {
-            const int ch = i / per, w = i - ch * per;
-            const int slot = (int)(((unsigned)it * L::kPairs + (ch >> 1)) % L::kPairSlots);
-            *reinterpret_cast<uint4*>(pairs + slot * kPairBytes + (ch & 1) * kChunkBytes + valid * 128 + w * 16) =
-                make_uint4(0, 0, 0, 0);
+          constexpr int per = R / 8;  // 16-byte pieces of a token's latent
+          for (int i = tid; i < (kTile - valid) * per; i += kSoftmaxThreads) {
+            const int t = valid + i / per, w = i % per;
+            const int slot = (int)(((unsigned)it * L::kQuads + w / (8 * kLatentQuad)) % L::kQuadSlots);
+            const int col = (w >> 3) % kLatentQuad;
+            *reinterpret_cast<uint4*>(quads + slot * kQuadBytes + ((t >> 3) * kLatentQuad + col) * kAtom +
+                                      (t & 7) * 128 + (w & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
         fence_async_shared();
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       wait_or_die(&sm.pv_done, (it - 1) & 1, dead, err);
       tc_fence_after();
 #pragma unroll 1
-      for (int mb = 0; mb < L::kPairs; ++mb)
+      for (int mb = 0; mb < R / 128; ++mb)
 #pragma unroll 1
         for (int q = 0; q < nrow; q += 16) {
           uint32_t o[16];
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     // ------------------------------------------------------------------ copies
     const uint64_t keep = l2_policy_evict_normal();
     const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : keep;
-    uint32_t ps_ = 0, pround = 0, rs_ = 0, rround = 0;  // next slot and round of each ring
+    uint32_t qs_ = 0, qround = 0, rs_ = 0, rround = 0;  // next slot and round of each ring
     int n_tile = 0, n_seg = 0;                          // started so far
     bool alive = true;
     // The row tile's queries (rows past the sequence's are other rows, or zero: unused).
@@ -464,9 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           const int32_t row = P.a.bt[(int64_t)seg.b * P.a.max_blocks + j];
           if (latent_row_ok(P.a.lv, row)) {
             const int32_t slab = row / P.a.lv.slab_blocks;
-            y0 = (row - slab * P.a.lv.slab_blocks) * kBlockTokens;
+            y0 = (row - slab * P.a.lv.slab_blocks) * (kBlockTokens / 8);
             map = P.a.lv.tab.base[(size_t)slab * P.a.lv.tab.stride] + P.a.lv.map_delta;
-            tensormap_acquire(map);
+            latent_maps_acquire(map);
           } else {
             atomicOr(err, ERR_ROW);
           }
@@ -476,34 +477,28 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
           const int i = 2 * (u - ub);
           const uint8_t *m0 = lane_ptr(map, i), *m1 = lane_ptr(map, i + 1);
           const int ya = __shfl_sync(0xffffffffu, y0, i), yb = __shfl_sync(0xffffffffu, y0, i + 1);
-          const uint32_t bytes = ((m0 != nullptr) + (m1 != nullptr)) * kBlockBytes * (R / 64 + 1);
+          const uint32_t bytes = ((m0 != nullptr) + (m1 != nullptr)) * kBlockTokens * (R + kRope) * 2;
           uint64_t* full = &sm.full[n_tile % kInFlight];
           if (rround > 0) alive = warp_wait(&sm.rope_empty[rs_], (rround - 1) & 1, dead, err);
           if (!alive) break;
           if (elect_one()) {
             uint8_t* dst = ropes + rs_ * kChunkBytes;
             mbar_arrive_expect_tx(full, bytes);
-            if (m0) tma_load_3d(dst, m0, 0, ya, R / 64, full, policy);
-            if (m1) tma_load_3d(dst + kBlockBytes, m1, 0, yb, R / 64, full, policy);
+            if (m0) latent_copy_column(dst, m0, R / 64, ya, full, policy);
+            if (m1) latent_copy_column(dst + kChunkBytes / 2, m1, R / 64, yb, full, policy);
           }
           ++n_tile;
           if (++rs_ == L::kRopeSlots) rs_ = 0, ++rround;
 #pragma unroll 1
-          for (int p = 0; p < L::kPairs; ++p) {
-            if (pround > 0) alive = warp_wait(&sm.pair_empty[ps_], (pround - 1) & 1, dead, err);
+          for (int p = 0; p < L::kQuads; ++p) {
+            if (qround > 0) alive = warp_wait(&sm.quad_empty[qs_], (qround - 1) & 1, dead, err);
             if (!alive) break;
             if (elect_one()) {
-              uint8_t* dst = pairs + ps_ * kPairBytes;
-              if (m0) {
-                tma_load_3d(dst, m0, 0, ya, 2 * p, full, policy);
-                tma_load_3d(dst + kChunkBytes, m0, 0, ya, 2 * p + 1, full, policy);
-              }
-              if (m1) {
-                tma_load_3d(dst + kBlockBytes, m1, 0, yb, 2 * p, full, policy);
-                tma_load_3d(dst + kChunkBytes + kBlockBytes, m1, 0, yb, 2 * p + 1, full, policy);
-              }
+              uint8_t* dst = quads + qs_ * kQuadBytes;
+              if (m0) latent_copy_quad(dst, m0, kLatentQuad * p, ya, full, policy);
+              if (m1) latent_copy_quad(dst + kQuadBytes / 2, m1, kLatentQuad * p, yb, full, policy);
             }
-            if (++ps_ == L::kPairSlots) ps_ = 0, ++pround;
+            if (++qs_ == L::kQuadSlots) qs_ = 0, ++qround;
           }
           if (!alive) break;
           // a later segment's queries wait for the products of the one before: after its
@@ -522,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     // -------------------------------------------------------------------- MMAs
     constexpr uint32_t id_s = tc_idesc(64, N, false, false);
     constexpr uint32_t id_o = tc_idesc(128, N, true, false);
-    const uint64_t d_rope = tc_desc(smem_u32(ropes), 16, 1024), d_pair = tc_desc(smem_u32(pairs), 16, 1024);
-    const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_p = tc_desc(smem_u32(ps), 16, 1024);
-    const uint64_t d_v = tc_desc(smem_u32(pairs), kChunkBytes, 1024);
+    const uint64_t d_rope = tc_desc(smem_u32(ropes), 16, kAtom), d_quad = tc_desc(smem_u32(quads), 16, kLatentQuad * kAtom);
+    const uint64_t d_q = tc_desc(smem_u32(qs), 16, kAtom), d_p = tc_desc(smem_u32(ps), 16, kAtom);
+    const uint64_t d_v = tc_desc(smem_u32(quads), kAtom, kLatentQuad * kAtom);
     int it = 0, n_seg = 0;
     uint32_t ks = 0, vs = 0, rs_ = 0;  // slots of the next tile's K, V and position keys
     bool alive = true, pending_first = false;
@@ -535,17 +530,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int mb = 0; mb < L::kPairs; ++mb) {
-          const uint32_t slot = vs + mb < L::kPairSlots ? vs + mb : vs + mb - L::kPairSlots;
-          const uint64_t a = d_v + ((slot * kPairBytes) >> 4);
+        for (int p = 0; p < L::kQuads; ++p) {
+          const uint32_t slot = vs + p < L::kQuadSlots ? vs + p : vs + p - L::kQuadSlots;
+          const uint64_t a = d_v + ((slot * kQuadBytes) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma(tm_o + mb * N, a + (k * 2048 >> 4), d_p + (k * 32 >> 4), id_o, !(first && k == 0));
-          tc_commit(&sm.pair_empty[slot]);
+          for (int h = 0; h < 2; ++h)  // 128 latent values at a time
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 tokens
+              tc_mma(tm_o + (2 * p + h) * N, a + ((h * 2 * kAtom + k * 2 * kLatentQuad * kAtom) >> 4),
+                     d_p + (k * 32 >> 4), id_o, !(first && k == 0));
+          tc_commit(&sm.quad_empty[slot]);
         }
         tc_commit(&sm.pv_done);
       }
-      vs = vs + L::kPairs < L::kPairSlots ? vs + L::kPairs : vs + L::kPairs - L::kPairSlots;
+      vs = vs + L::kQuads < L::kQuadSlots ? vs + L::kQuads : vs + L::kQuads - L::kQuadSlots;
     };
     // The next tile's S^T is issued before this tile's values where its rows have arrived: it
     // runs under the softmax.  Where they have not, the values go first, so that their
@@ -571,19 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             tc_mma(tm_s + buf * N, ar + (k * 32 >> 4), d_q + (((R / 64) * N * 128 + k * 32) >> 4), id_s, k > 0);
           tc_commit(&sm.rope_empty[rs_]);
 #pragma unroll
-          for (int p = 0; p < L::kPairs; ++p) {
-            const uint32_t slot = ks + p < L::kPairSlots ? ks + p : ks + p - L::kPairSlots;
-            const uint64_t a = d_pair + ((slot * kPairBytes) >> 4), q = d_q + ((2 * p * N * 128) >> 4);
+          for (int p = 0; p < L::kQuads; ++p) {
+            const uint32_t slot = ks + p < L::kQuadSlots ? ks + p : ks + p - L::kQuadSlots;
+            const uint64_t a = d_quad + ((slot * kQuadBytes) >> 4), q = d_q + ((kLatentQuad * p * N * 128) >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma(tm_s + buf * N, a + (((k >> 2) * kChunkBytes + (k & 3) * 32) >> 4),
+            for (int k = 0; k < 4 * kLatentQuad; ++k)
+              tc_mma(tm_s + buf * N, a + (((k >> 2) * kAtom + (k & 3) * 32) >> 4),
                      q + (((k >> 2) * N * 128 + (k & 3) * 32) >> 4), id_s, true);
           }
           tc_commit(&sm.s_full[buf]);
           if (u == k1 - 1) tc_commit(&sm.q_empty);
         }
         if (++rs_ == L::kRopeSlots) rs_ = 0;
-        ks = ks + L::kPairs < L::kPairSlots ? ks + L::kPairs : ks + L::kPairs - L::kPairSlots;
+        ks = ks + L::kQuads < L::kQuadSlots ? ks + L::kQuads : ks + L::kQuads - L::kQuadSlots;
         if (it > 0 && !late) add_values(it - 1, pending_first);
         pending_first = first;
       }

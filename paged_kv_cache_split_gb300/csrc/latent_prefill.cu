@@ -20,7 +20,8 @@ namespace {
 constexpr int DH = kLatentHead;
 constexpr int kTile = 128;               // tokens (keys) a tile, queries a tile
 constexpr int kSlot = kTile * 128;       // 128 rows x 64 values: one swizzled box column
-constexpr int kBlockBytes = kBlockTokens * 128;
+constexpr int kBlockBytes = kBlockTokens * 128;  // one column of a block
+constexpr int kAtom = 1024;              // eight tokens of a column: the swizzle's atom
 constexpr int kSmall = 3072;             // alignment (1024) and barriers
 constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -1e30f;
@@ -41,17 +42,18 @@ __device__ __forceinline__ int32_t context(const Params& P, int b, bool* bad) {
   return latent_ctx(__ldg(P.a.ctx + b), all < P.a.max_ctx ? all : (int64_t)P.a.max_ctx, P.a.n_q, bad);
 }
 
-// Block j of sequence b: its tensor map (null outside the pool) and first row in it.
-__device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int j, int* y0) {
+// Block j of sequence b: its slab's tensor maps (null outside the pool) and its first row
+// there, in eights.
+__device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int j, int* y8) {
   const int32_t row = P.a.bt[(int64_t)b * P.a.max_blocks + j];
   if (!latent_row_ok(P.a.lv, row)) {
     atomicOr(P.a.lv.err, ERR_ROW);
     return nullptr;
   }
   const int32_t slab = row / P.a.lv.slab_blocks;
-  *y0 = (row - slab * P.a.lv.slab_blocks) * kBlockTokens;
+  *y8 = (row - slab * P.a.lv.slab_blocks) * (kBlockTokens / 8);
   const uint8_t* map = P.a.lv.tab.base[(size_t)slab * P.a.lv.tab.stride] + P.a.lv.map_delta;
-  tensormap_acquire(map);
+  latent_maps_acquire(map);
   return map;
 }
 
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
             const uint8_t* mk = lane_ptr(map, k);
             const int yk = __shfl_sync(0xffffffffu, y0, k);
             if (mk && elect_one())
-              tma_load_3d(as + c * kSlot + k * kBlockBytes, mk, 0, yk, c, &sm.a_full[c], keep);
+              latent_copy_column(as + c * kSlot + k * kBlockBytes, mk, c, yk, &sm.a_full[c], keep);
           }
           ++na;
         }
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
     for (uint32_t i = na > C ? na - C : 0; i < na; ++i) mbar_wait_bounded(&sm.a_full[i % C], (i / C) & 1, err);
   } else {
     constexpr uint32_t id = tc_idesc(128, 256, false, false);
-    const uint64_t d_a = tc_desc(smem_u32(as), 16, 1024), d_w = tc_desc(smem_u32(ws), 16, 1024);
+    const uint64_t d_a = tc_desc(smem_u32(as), 16, kAtom), d_w = tc_desc(smem_u32(ws), 16, kAtom);
     uint32_t s = 0, round = 0, tiles = 0;
     bool alive = true;
     for (int n = 0; alive && it.next(P, n == 0, &new_tile); ++n) {
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         for (int k = 0; k < 4; ++k) {
           const uint8_t* mk = lane_ptr(map, i + k);
           const int yk = __shfl_sync(0xffffffffu, y0, i + k);
-          if (mk && elect_one()) tma_load_3d(slot(2) + k * kBlockBytes, mk, 0, yk, R / 64, &sm.k_full[par], keep);
+          if (mk && elect_one()) latent_copy_column(slot(2) + k * kBlockBytes, mk, R / 64, yk, &sm.k_full[par], keep);
         }
         if (j >= 1) alive = warp_wait(&sm.k_empty[par ^ 1], ((j - 1) >> 1) & 1, dead, err);
         if (!alive) break;

@@ -35,6 +35,7 @@ struct pkv_pool {
   int n_sm = 0;
   size_t smem_optin = 0;
   int n_kinds = 2;
+  int n_maps = 2;                        // tensor maps per slab and layer (latent: two of its one tensor)
   int64_t row_bytes[4] = {0, 0, 0, 0};
   int64_t slab_bytes[4] = {0, 0, 0, 0};  // one slab of one layer, per kind
   int64_t group_bytes = 0;               // one slab index across layers and kinds
@@ -95,7 +96,7 @@ static LayerView layer_view(const pkv_pool* p, int layer) {
   lv.rows_capacity = (int64_t)p->groups.size() * p->cfg.slab_blocks;
   for (int k = 0; k < 4; ++k) lv.row_bytes[k] = (int)p->row_bytes[k];
   lv.err = p->err_dev;
-  lv.map_delta = p->maps_offset - (int64_t)layer * p->layer_bytes + (int64_t)layer * p->n_kinds * 128;
+  lv.map_delta = p->maps_offset - (int64_t)layer * p->layer_bytes + (int64_t)layer * p->n_maps * 128;
   for (int k = 0; k < 4; ++k)
     lv.box_bytes[k] = k < p->n_kinds ? tma_box_bytes(p->row_bytes[k] * p->cfg.n_kv_heads) : 0;
   return lv;
@@ -139,13 +140,32 @@ bool pkv::encode_bf16_map(CUtensorMap* map, const void* base, int rank, const ui
 // Tensor maps of one slab group: for every layer and stored tensor, the slab
 // [slab_blocks * 32 tokens][Hkv * row] bytes viewed in 3-D as [column block][token]
 // [W bytes] (W = box_bytes), read in boxes of 16 tokens x the whole row, which land
-// as row/W boxes of 16 x W bytes with the matching shared-memory swizzle.
+// as row/W boxes of 16 x W bytes with the matching shared-memory swizzle.  A latent
+// slab has two maps, of the same [token][row] bytes in 4-D as [eight tokens][column
+// block][token of the eight][128 bytes]: a copy of 32 tokens x `cols` column blocks lands
+// as [4][cols][8][128], each eight tokens of a column block a 1024-byte swizzle atom.
+// The first map copies four column blocks at a time, the second one.
 static bool encode_group_maps(const pkv_pool* p, uint8_t* group, std::vector<CUtensorMap>& maps) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   const int L = p->cfg.n_layers, K = p->n_kinds;
-  maps.resize((size_t)L * K);
+  maps.resize((size_t)L * p->n_maps);
   int64_t off = 0;
+  if (p->cfg.format == PKV_FMT_LATENT) {
+    const cuuint64_t row = (cuuint64_t)p->row_bytes[PKV_KIND_K];
+    const cuuint64_t dims[4] = {128, 8, row / 128, (cuuint64_t)p->cfg.slab_blocks * kBlockTokens / 8};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    for (int l = 0; l < L; ++l, off += p->slab_bytes[PKV_KIND_K])
+      for (int m = 0; m < 2; ++m) {
+        const cuuint32_t boxd[4] = {128u, 8u, m == 0 ? (cuuint32_t)kLatentQuad : 1u, kBlockTokens / 8};
+        if (enc(&maps[(size_t)l * 2 + m], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, group + off, dims, strides, boxd, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+          return false;
+      }
+    return true;
+  }
   for (int l = 0; l < L; ++l)
     for (int k = 0; k < K; ++k) {
       const int64_t row = p->row_bytes[k] * p->cfg.n_kv_heads;
@@ -155,14 +175,11 @@ static bool encode_group_maps(const pkv_pool* p, uint8_t* group, std::vector<CUt
                                     : box == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
       // 3-D view [column block][token][W bytes] of the [token][row] tensor: one copy
-      // moves 16 tokens of the whole row and lands as nx boxes of 16 x W bytes.  A
-      // latent pool's kernels take one column block of a 32-token block at a time.
+      // moves 16 tokens of the whole row and lands as nx boxes of 16 x W bytes.
       const cuuint64_t nx = (cuuint64_t)(row / box);
       const cuuint64_t dims[3] = {(cuuint64_t)box, (cuuint64_t)p->cfg.slab_blocks * kBlockTokens, nx};
       const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)box};
-      const bool latent = p->cfg.format == PKV_FMT_LATENT;
-      const cuuint32_t boxd[3] = {(cuuint32_t)box, latent ? (cuuint32_t)kBlockTokens : 16u,
-                                  latent ? 1u : (cuuint32_t)nx};
+      const cuuint32_t boxd[3] = {(cuuint32_t)box, 16u, (cuuint32_t)nx};
       const cuuint32_t estr[3] = {1u, 1u, 1u};
       if (enc(&maps[(size_t)l * K + k], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, group + off, dims, strides, boxd, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -234,6 +251,7 @@ pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_allocator* allo
   p->smem_optin = (size_t)optin;
 
   p->n_kinds = latent ? 1 : (cfg->format == PKV_FMT_BF16) ? 2 : 4;
+  p->n_maps = latent ? 2 : p->n_kinds;
   p->row_bytes[PKV_KIND_K] = latent ? (int64_t)(D + kRope) * 2 : (int64_t)D * fb.k / 8;
   p->row_bytes[PKV_KIND_V] = latent ? 0 : (int64_t)D * fb.v / 8;
   if (p->n_kinds == 4) {
@@ -249,7 +267,7 @@ pkv_status pkv_pool_create(const pkv_pool_config* cfg, const pkv_allocator* allo
   p->group_bytes = p->layer_bytes * cfg->n_layers;
   // Tensor maps (128 bytes each, 64-byte aligned) after the slab data.
   p->maps_offset = (p->group_bytes + 127) / 128 * 128;
-  p->group_bytes = p->maps_offset + (int64_t)cfg->n_layers * p->n_kinds * 128;
+  p->group_bytes = p->maps_offset + (int64_t)cfg->n_layers * p->n_maps * 128;
   for (int k = 0; k < p->n_kinds; ++k)
     if (tma_box_bytes(p->row_bytes[k] * cfg->n_kv_heads) == 0) return fail(PKV_ERR_INVALID);
 
