@@ -174,10 +174,12 @@ def _stream(stream=None) -> int:
 
 
 def _dev(t, dtype, name: str, shape=None):
+    try:
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     torch = _torch()
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() \
-            and (shape is None or t.shape == shape):
-        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -191,9 +193,12 @@ def _dev(t, dtype, name: str, shape=None):
 
 def _dev_strided(t, dtype, name: str, shape):
     """Like _dev, for a tensor whose last dimension alone has to be contiguous."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.stride(-1) == 1:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     torch = _torch()
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.stride(-1) == 1:
-        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -207,15 +212,17 @@ def _dev_strided(t, dtype, name: str, shape):
 
 def _row_stride(t, name: str) -> int:
     """The one distance between consecutive rows (every leading dimension) of `t`."""
+    shape, strides = t.shape, t.stride()
     step, rows = None, 1
-    for n, st in zip(t.shape[-2::-1], t.stride()[-2::-1]):
+    for i in range(len(shape) - 2, -1, -1):
+        n = shape[i]
         if n != 1:
             if step is None:
-                step = st
-            elif st != step * rows:
-                raise ValueError(f"{name}: its rows must be evenly spaced (strides {tuple(t.stride())})")
+                step = strides[i]
+            elif strides[i] != step * rows:
+                raise ValueError(f"{name}: its rows must be evenly spaced (strides {strides})")
         rows *= n
-    return t.shape[-1] if step is None else step
+    return shape[-1] if step is None else step
 
 
 def slab_runs(rows, slab_blocks: int = 32) -> np.ndarray:
@@ -260,7 +267,8 @@ class Pool:
         _check(st, "pool_create")
         self._h = h
         self._ws = {}
-        self._ws_bytes = {}  # latent_workspace_bytes by (B, n_q, Hq)
+        self._ws_bytes = {}  # workspace sizes of the latent calls by their arguments
+        self._latent_dims = (head_dim, int(group_size)) if self.format == "latent" else None
         s = self.stats()
         self.row_bytes = s["row_bytes"][: s["n_kinds"]]
 
@@ -447,9 +455,9 @@ class Pool:
 
     # -- latent pools ----------------------------------------------------------
     def _latent(self):
-        if self.format != "latent":
+        if self._latent_dims is None:
             raise PkvError(PKV_ERR_FORMAT, f"a {self.format} pool has no latent rows")
-        return self.head_dim, int(self.cfg.group_size)
+        return self._latent_dims
 
     def write_latent(self, layer: int, rows, slots, kv, positions, cos_sin, norm_weight=None, eps: float = 1e-6,
                      interleaved: bool = True, q_rope=None, q_out=None, stream=None):
@@ -460,28 +468,37 @@ class Pool:
         strides, in multiples of 8 values.  Returns q_out (None without q_rope)."""
         torch = _torch()
         R, P = self._latent()
-        n = int(rows.numel())
+        bf16, i32 = torch.bfloat16, torch.int32
+        n = rows.numel()
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [positions, P]")
-        kvp = _dev_strided(kv, torch.bfloat16, "kv", (n, R + P))
-        Hq, q, qs, o, os_ = 0, None, (0, 0), None, (0, 0)
+        one = (n,)
+        kvp = _dev_strided(kv, bf16, "kv", (n, R + P))
+        Hq, q, o = 0, None, None
+        qt = qh = ot = oh = 0  # a dimension of one entry is never stepped over: its stride says nothing
         if q_rope is not None:
             if q_rope.dim() != 3:
                 raise ValueError("q_rope must be [n, Hq, P]")
-            Hq = int(q_rope.shape[1])
+            Hq = q_rope.shape[1]
+            shape = (n, Hq, P)
             if q_out is None:
-                q_out = torch.empty((n, Hq, P), dtype=torch.bfloat16, device=q_rope.device)
-            q, o = (_dev_strided(t, torch.bfloat16, name, (n, Hq, P)) for t, name in ((q_rope, "q_rope"), (q_out, "q_out")))
-            # a dimension of one entry is never stepped over: its stride says nothing
-            qs, os_ = (((t.stride(0) if n > 1 else 0), (t.stride(1) if Hq > 1 else 0)) for t in (q_rope, q_out))
+                q_out = self._own(shape, bf16, q_rope.device, stream)
+            q, o = _dev_strided(q_rope, bf16, "q_rope", shape), _dev_strided(q_out, bf16, "q_out", shape)
+            if n > 1:
+                qt, ot = q_rope.stride(0), q_out.stride(0)
+            if Hq > 1:
+                qh, oh = q_rope.stride(1), q_out.stride(1)
         elif q_out is not None:
             raise ValueError("q_out without q_rope")
-        _check(self._lib.pkv_write_latent(
-            self._h, layer, n, _dev(rows, torch.int32, "rows", (n,)), _dev(slots, torch.int32, "slots", (n,)), kvp,
-            int(kv.stride(0)) if n > 1 else R + P, _dev(positions, torch.int32, "positions", (n,)),
-            _dev(cos_sin, torch.float32, "cos_sin", (cos_sin.shape[0], P)), int(cos_sin.shape[0]),
-            None if norm_weight is None else _dev(norm_weight, torch.bfloat16, "norm_weight", (R,)), float(eps),
-            int(bool(interleaved)), Hq, q, *qs, o, *os_, _stream(stream)), "write_latent")
+        n_pos = cos_sin.shape[0]
+        st = self._lib.pkv_write_latent(
+            self._h, layer, n, _dev(rows, i32, "rows", one), _dev(slots, i32, "slots", one), kvp,
+            kv.stride(0) if n > 1 else R + P, _dev(positions, i32, "positions", one),
+            _dev(cos_sin, torch.float32, "cos_sin", (n_pos, P)), n_pos,
+            None if norm_weight is None else _dev(norm_weight, bf16, "norm_weight", (R,)), float(eps),
+            1 if interleaved else 0, Hq, q, qt, qh, o, ot, oh, _stream(stream))
+        if st:
+            _check(st, "write_latent")
         return q_out
 
     def latent_workspace_bytes(self, B: int, n_q: int, Hq: int) -> int:
@@ -496,28 +513,36 @@ class Pool:
         of one [.., R + P] tensor, for instance).  Returns out, shaped as q_latent."""
         torch = _torch()
         R, P = self._latent()
-        if q_latent.dim() not in (3, 4):
+        bf16, i32 = torch.bfloat16, torch.int32
+        lead = tuple(q_latent.shape)[:-1]
+        if len(lead) == 3:
+            B, n_q, Hq = lead
+        elif len(lead) == 2:
+            (B, Hq), n_q = lead, 1
+        else:
             raise ValueError("q_latent must be [B, Hq, R] or [B, n_q, Hq, R]")
-        lead = tuple(q_latent.shape[:-1])
-        B, Hq, n_q = lead[0], lead[-1], (lead[1] if len(lead) == 3 else 1)
-        ql = _dev_strided(q_latent, torch.bfloat16, "q_latent", lead + (R,))
-        qr = _dev_strided(q_rope, torch.bfloat16, "q_rope", lead + (P,))
+        rows = lead + (R,)
+        ql = _dev_strided(q_latent, bf16, "q_latent", rows)
+        qr = _dev_strided(q_rope, bf16, "q_rope", lead + (P,))
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError("block_table must be [B, max_blocks]")
         if out is None:
-            out = torch.empty(lead + (R,), dtype=torch.bfloat16, device=q_latent.device)
+            out = self._own(rows, bf16, q_latent.device, stream)
+            o = out.data_ptr()
+        else:
+            o = _dev(out, bf16, "out", rows)
         if workspace is None:
             key = (B, n_q, Hq)
             need = self._ws_bytes.get(key)
             if need is None:
                 need = self._ws_bytes[key] = self.latent_workspace_bytes(B, n_q, Hq)
-            workspace = self._own_workspace(need, q_latent.device, stream)
-        _check(self._lib.pkv_paged_latent_attention(
+            workspace = self._own(need, torch.uint8, q_latent.device, stream)
+        st = self._lib.pkv_paged_latent_attention(
             self._h, layer, B, n_q, Hq, ql, _row_stride(q_latent, "q_latent"), qr, _row_stride(q_rope, "q_rope"),
-            _dev(block_table, torch.int32, "block_table"), int(block_table.shape[1]),
-            _dev(ctx_lens, torch.int32, "ctx_lens", (B,)), int(max_ctx), float(scale),
-            _dev(out, torch.bfloat16, "out", lead + (R,)), _dev(workspace, torch.uint8, "workspace"),
-            workspace.numel(), _stream(stream)), "paged_latent_attention")
+            _dev(block_table, i32, "block_table"), block_table.shape[1], _dev(ctx_lens, i32, "ctx_lens", (B,)),
+            int(max_ctx), float(scale), o, _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+        if st:
+            _check(st, "paged_latent_attention")
         return out
 
     def latent_prefill_workspace_bytes(self, B: int, n_q: int, Hq: int, max_blocks: int, max_ctx: int = 0) -> int:
@@ -541,10 +566,13 @@ class Pool:
             raise ValueError("block_table must be [B, max_blocks]")
         mb = int(block_table.shape[1])
         if out is None:
-            out = torch.empty((B, n_q, Hq, D), dtype=torch.bfloat16, device=q.device)
+            out = self._own((B, n_q, Hq, D), torch.bfloat16, q.device, stream)
         if workspace is None:
-            need = self.latent_prefill_workspace_bytes(B, n_q, Hq, mb, int(max_ctx))
-            workspace = self._own_workspace(need, q.device, stream)
+            key = (B, n_q, Hq, mb, int(max_ctx))
+            need = self._ws_bytes.get(key)
+            if need is None:
+                need = self._ws_bytes[key] = self.latent_prefill_workspace_bytes(*key)
+            workspace = self._own(need, torch.uint8, q.device, stream)
         _check(self._lib.pkv_latent_prefill_attention(
             self._h, layer, B, n_q, Hq, _dev(q, torch.bfloat16, "q", (B, n_q, Hq, D + P)),
             _dev(w_k, torch.bfloat16, "w_k", (Hq, D, R)), _dev(w_v, torch.bfloat16, "w_v", (Hq, D, R)),
@@ -554,18 +582,18 @@ class Pool:
         return out
 
     @staticmethod
-    def _own_workspace(nbytes: int, device, stream):
-        """Memory of one call alone: two calls on two streams, or in two captured graphs, share
-        none."""
+    def _own(shape, dtype, device, stream):
+        """Memory of one call alone (its output, its workspace): two calls on two streams, or in
+        two captured graphs, share none."""
         torch = _torch()
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
         if stream is not None:
             # made on the current stream, used on another
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
             if s != torch.cuda.current_stream():
                 s.wait_stream(torch.cuda.current_stream())
-                workspace.record_stream(s)
-        return workspace
+                t.record_stream(s)
+        return t
 
     # -- introspection -------------------------------------------------------
     def stats(self) -> dict:
