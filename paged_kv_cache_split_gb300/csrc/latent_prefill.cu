@@ -68,34 +68,37 @@ constexpr int kExpandThreads = 320;  // warps 0..3 store keys, 4..7 values; 8 co
 constexpr int kWStages = 3;
 constexpr int kWStage = 2 * kSlot;
 
-// The items of one CTA, in order.  Every role walks them by itself.
+// The items of one CTA, in order.  Every role walks them by itself.  (Fewer than 2^24 of
+// them, as B Hq T < 2^31: 32-bit divisions.)
 struct Items {
-  int64_t item, end, base;  // next item; last + 1; tiles before sequence b
+  uint32_t item, end, base;  // next item; last + 1; tiles before sequence b
   int b, len, tile, h;
   __device__ __forceinline__ void start(const Params& P) {
     const int lane = threadIdx.x & 31;
     bool bad;
-    int64_t n = 0;
+    uint32_t n = 0;
     for (int i = lane; i < P.a.B; i += 32) n += (context(P, i, &bad) + kTile - 1) / kTile;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
     n *= P.a.Hq;
-    item = n * blockIdx.x / gridDim.x;
-    end = n * (blockIdx.x + 1) / gridDim.x;
+    // an even share, the remainder over the first CTAs
+    const uint32_t each = n / gridDim.x, more = n - each * gridDim.x;
+    item = blockIdx.x * each + min(blockIdx.x, more);
+    end = item + each + (blockIdx.x < more ? 1 : 0);
     base = 0;
     b = 0;
   }
   // Whole warp.  new_tile: the tile differs from the item's before.
   __device__ __forceinline__ bool next(const Params& P, bool first, bool* new_tile) {
     if (item >= end) return false;
-    h = uniform((int)(item % P.a.Hq));
+    const uint32_t t = uniform(item / (uint32_t)P.a.Hq);
+    h = (int)(uniform(item) - t * P.a.Hq);
     *new_tile = first || h == 0;
     if (*new_tile) {
-      const int64_t t = item / P.a.Hq;
       for (;; ++b) {
         bool bad;
         len = uniform(context(P, b, &bad));
-        const int n = (len + kTile - 1) / kTile;
+        const uint32_t n = (len + kTile - 1) / kTile;
         if (t < base + n) break;
         base += n;
       }
@@ -326,12 +329,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Units (sequence, 256 queries) up to which a CTA ranks them by their key tiles.
+constexpr int kRanked = 384;
+
 struct AttnSmall {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // by parity of the key tile
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain, done;
   uint32_t tmem;
   int dead;
+  int pick;            // ranked launch: the unit of this CTA
+  int cost[kRanked];   // ranked launch: key tiles of each unit
 };
+static_assert(sizeof(AttnSmall) <= kSmall - 1024, "small state");
 
 __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
@@ -342,12 +351,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* dead = &sm.dead;
   int32_t* err = P.a.lv.err;
-  // the last queries see most: their tiles go first
-  const int bh = P.a.B * P.a.Hq;
-  const int pair = P.pairs - 1 - (int)(blockIdx.x / bh), rest = (int)(blockIdx.x % bh);
-  const int b = rest / P.a.Hq, h = rest % P.a.Hq;
   const int R = P.a.R, n_q = P.a.n_q;
-  const int i0 = pair * 2 * kTile;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -365,10 +369,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // The units with most key tiles go first (heads fastest).  In one sequence those are the
+  // last queries; over several, whose lengths only the device knows, each CTA ranks them.
+  const int units = P.pairs * P.a.B;
+  const int place = (int)(blockIdx.x / P.a.Hq), h = (int)(blockIdx.x % P.a.Hq);
+  int unit = units - 1 - place;  // b fastest
+  if (P.a.B > 1 && units <= kRanked) {
+    bool bad;
+    const int u = threadIdx.x;
+    int mine = 0;
+    if (u < units) {
+      const int32_t L = context(P, u % P.a.B, &bad);
+      mine = L == 0 ? 0 : (L - n_q + min(n_q, (u / P.a.B + 1) * 2 * kTile) + kTile - 1) / kTile;
+      sm.cost[u] = mine;
+    }
+    __syncthreads();
+    if (u < units) {
+      int before = 0;
+      for (int k = 0; k < units; ++k) before += sm.cost[k] > mine || (sm.cost[k] == mine && k < u);
+      if (before == place) sm.pick = u;
+    }
+    __syncthreads();
+    unit = sm.pick;
+  }
+  unit = uniform(unit);
+  const int pair = unit / P.a.B, b = unit % P.a.B;
+  const int i0 = pair * 2 * kTile;
   bool bad;
-  const int32_t L = context(P, b, &bad);
+  const int32_t L = uniform(context(P, b, &bad));
   if (L == 0) {
-    if (bad && blockIdx.x / bh == 0 && h == 0 && threadIdx.x == 0) atomicOr(err, ERR_CTX);
+    if (bad && pair == 0 && h == 0 && threadIdx.x == 0) atomicOr(err, ERR_CTX);
     const int n = min(2 * kTile, n_q - i0);
     for (int i = threadIdx.x; i < n * (DH / 8); i += kAttnThreads)
       reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i0 + i / (DH / 8)) * P.a.Hq + h) * DH)[i % (DH / 8)] =
