@@ -429,7 +429,8 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  *                  q_out may be q_rope with the same strides (in place)
  * Arithmetic in fp32, one rounding to bf16 per stored value.  Pointers 16-byte
  * aligned; strides in values, non-negative multiples of 8, kv_stride >= R + P; output
- * rows of q_out at least P apart; 0 <= Hq <= 1024 (else PKV_ERR_INVALID).  Two tokens
+ * rows of q_out at least P apart; 0 <= Hq <= 1024, n_tokens * (1 + ceil(Hq / 32)) < 2^31
+ * (else PKV_ERR_INVALID).  Two tokens
  * with the same (row, slot) leave either one's values.  A row, slot or position out
  * of range sets the device error word (bit 1, 4 or 16): the row is then not written
  * and, for a bad position, neither are the token's q_out rows.  n_tokens 0 returns

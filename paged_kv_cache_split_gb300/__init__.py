@@ -213,6 +213,11 @@ def _dev_strided(t, dtype, name: str, shape):
 def _row_stride(t, name: str) -> int:
     """The one distance between consecutive rows (every leading dimension) of `t`."""
     shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        a, b, c, _ = shape
+        sa, sb, sc, _ = strides
+        if c > 1 and (b == 1 or sb == c * sc) and (a == 1 or sa == b * c * sc):
+            return sc
     step, rows = None, 1
     for i in range(len(shape) - 2, -1, -1):
         n = shape[i]

@@ -24,6 +24,10 @@ constexpr int kLatentMaxBlocks = 1 << 20;     // block-table width of the expand
 
 enum : int32_t { ERR_POS = 16 };  // a rotary position outside the table (pkv_pool_check_errors)
 
+// Warps of the write per token: one for the latent row, one for every 32 heads.
+constexpr int kLatentWriteHeads = 32;
+inline int latent_write_units(int Hq) { return 1 + (Hq + kLatentWriteHeads - 1) / kLatentWriteHeads; }
+
 struct LatentWriteArgs {
   LayerView lv;
   int R;                     // 256 or 512
@@ -43,6 +47,7 @@ struct LatentWriteArgs {
   int64_t q_tok, q_head;
   uint16_t* qo;
   int64_t o_tok, o_head;
+  int per_token;             // set by the launch
   cudaStream_t stream;
 };
 cudaError_t launch_latent_write(const LatentWriteArgs& a);

@@ -103,6 +103,8 @@ struct Segment {
   int k0, k1, n;     // this CTA's tiles of it, and all of them
 };
 
+// The walk's values are warp-uniform and known as such: what the copies and MMAs are issued
+// with follows from them.
 struct Walk {
   int b;
   int64_t up;      // tiles before sequence b
@@ -114,7 +116,8 @@ struct Walk {
       const int64_t base = kCost * up + (int64_t)kSegCost * (b + 1);
       if (base >= hi) return false;
       s.b = b;
-      s.vis = visible<N>(P, b, rt, &s.len);
+      s.vis = uniform(visible<N>(P, b, rt, &s.len));
+      s.len = uniform(s.len);
       s.n = (s.vis + kTile - 1) / kTile;
       const int64_t f = base >= lo ? 0 : (lo - base + kCost - 1) / kCost;
       const int64_t e = (hi - base + kCost - 1) / kCost;
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem);
   const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
-  Walk walk = sm.walk;
+  Walk walk = {uniform(sm.walk.b), uniform(sm.walk.up), uniform(sm.walk.lo), uniform(sm.walk.hi)};
   Segment seg;
 
   if (warp < 4) {

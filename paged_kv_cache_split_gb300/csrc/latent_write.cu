@@ -16,11 +16,12 @@
 #include <cuda_runtime.h>
 
 #include "latent.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kHeadsPerUnit = 32;
+constexpr int kHeadsPerUnit = kLatentWriteHeads;
 
 struct Vec8 {
   float x[8];
@@ -83,33 +84,34 @@ struct Angles {
 };
 
 template <int R, bool IL>
-__global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteArgs a, const int per_token) {
+__global__ void __launch_bounds__(256) latent_write_kernel(const __grid_constant__ LatentWriteArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t i64 = u / per_token;
-  if (i64 >= a.n) return;
-  const int i = (int)i64, part = (int)(u - i64 * per_token);
+  const uint32_t u = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t i = u / (uint32_t)a.per_token;
+  if (i >= (uint32_t)a.n) return;
+  const int part = (int)(u - i * a.per_token);
+  // What is loaded from the token's own rows is asked for before its position and place are
+  // checked: one memory latency instead of three.
   const int32_t pos = a.positions[i];
   const bool pos_ok = pos >= 0 && pos < a.n_pos;
-  if (!pos_ok) {
-    if (lane == 0 && part == 0) atomicOr(a.lv.err, ERR_POS);
-    return;
-  }
   const int j = lane & 7;
   Angles<IL> ang;
   if (part == 0) {
-    const int32_t row = a.rows[i], slot = a.slots[i];
-    if (!latent_row_ok(a.lv, row) || slot < 0 || slot >= kBlockTokens) {
-      if (lane == 0) atomicOr(a.lv.err, latent_row_ok(a.lv, row) ? ERR_SLOT : ERR_ROW);
-      return;
-    }
     constexpr int CH = R / 8 / 32;  // 16-byte chunks of the latent per lane
     const uint4* src = reinterpret_cast<const uint4*>(a.kv + (int64_t)i * a.kv_stride);
-    uint4* dst = reinterpret_cast<uint4*>(latent_row(a.lv, row, slot));
     uint4 raw[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) raw[k] = src[lane + 32 * k];
     const uint4 rr = src[R / 8 + j];  // the eight lanes of a row, four copies of it
+    const int32_t row = a.rows[i], slot = a.slots[i];
+    const bool row_ok = latent_row_ok(a.lv, row), slot_ok = slot >= 0 && slot < kBlockTokens;
+    if (!pos_ok || !row_ok || !slot_ok) {
+      if (lane == 0) atomicOr(a.lv.err, !pos_ok ? ERR_POS : row_ok ? ERR_SLOT : ERR_ROW);
+      return;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(latent_row(a.lv, row, slot));
     ang.load(a.cos_sin + (int64_t)pos * kRope, j);
     if (a.weight) {
       Vec8 v[CH];
@@ -138,7 +140,6 @@ __global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteArgs
     if (lane < 8) dst[R / 8 + j] = turned;
     return;
   }
-  ang.load(a.cos_sin + (int64_t)pos * kRope, j);
   const int h0 = (part - 1) * kHeadsPerUnit + (lane >> 3);
   const uint16_t* q = a.q + (int64_t)i * a.q_tok + 8 * j;
   uint16_t* qo = a.qo + (int64_t)i * a.o_tok + 8 * j;
@@ -148,6 +149,8 @@ __global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteArgs
     const int h = h0 + 4 * k;
     v[k] = h < a.Hq ? *reinterpret_cast<const uint4*>(q + h * a.q_head) : make_uint4(0, 0, 0, 0);
   }
+  if (!pos_ok) return;  // flagged with the token's row
+  ang.load(a.cos_sin + (int64_t)pos * kRope, j);
 #pragma unroll
   for (int k = 0; k < kHeadsPerUnit / 4; ++k) {
     const int h = h0 + 4 * k;
@@ -157,26 +160,22 @@ __global__ void __launch_bounds__(256) latent_write_kernel(const LatentWriteArgs
 }
 
 template <int R>
-void launch_r(const LatentWriteArgs& a) {
-  const int per_token = 1 + (a.Hq + kHeadsPerUnit - 1) / kHeadsPerUnit;
-  const int64_t units = (int64_t)a.n * per_token;
+cudaError_t launch_r(const LatentWriteArgs& a) {
+  const int64_t units = (int64_t)a.n * a.per_token;
   // a step's few tokens spread over the SMs, one warp per CTA
   const int threads = units < 2048 ? 32 : 256;
-  const unsigned grid = (unsigned)((units * 32 + threads - 1) / threads);
-  if (a.interleaved)
-    latent_write_kernel<R, true><<<grid, threads, 0, a.stream>>>(a, per_token);
-  else
-    latent_write_kernel<R, false><<<grid, threads, 0, a.stream>>>(a, per_token);
+  const dim3 grid((unsigned)((units * 32 + threads - 1) / threads));
+  static std::atomic<uint64_t> none{0};
+  return tc_launch(a.interleaved ? latent_write_kernel<R, true> : latent_write_kernel<R, false>, grid, threads, (size_t)0,
+                   a.stream, a, 0, &none);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_write(const LatentWriteArgs& a) {
-  if (a.R == 512)
-    launch_r<512>(a);
-  else
-    launch_r<256>(a);
-  return cudaGetLastError();
+cudaError_t launch_latent_write(const LatentWriteArgs& args) {
+  LatentWriteArgs a = args;
+  a.per_token = latent_write_units(a.Hq);
+  return a.R == 512 ? launch_r<512>(a) : launch_r<256>(a);
 }
 
 }  // namespace pkv

@@ -755,6 +755,7 @@ pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, 
   if (st != PKV_OK) return st;
   const int R = p->cfg.head_dim;
   if (n < 0 || Hq < 0 || Hq > kLatentMaxHeads || n_positions < 0) return PKV_ERR_INVALID;
+  if ((int64_t)n * latent_write_units(Hq) >= (int64_t)1 << 31) return PKV_ERR_INVALID;
   if (n == 0) return PKV_OK;
   if (!rows || !slots || !kv || !positions || !cos_sin) return PKV_ERR_INVALID;
   if (misaligned(kv, 16) || misaligned(cos_sin, 16) || misaligned(norm_weight, 16) || misaligned(q_rope, 16) ||
@@ -790,6 +791,7 @@ pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, 
   a.qo = (uint16_t*)q_out;
   a.o_tok = out_token_stride;
   a.o_head = out_head_stride;
+  a.per_token = 0;
   a.stream = (cudaStream_t)stream;
   PKV_CUDA(launch_latent_write(a), "write_latent launch");
   p->last_stream = a.stream;

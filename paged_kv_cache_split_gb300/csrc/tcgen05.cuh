@@ -180,6 +180,7 @@ __device__ __forceinline__ bool elect_one() {
 // A value every lane holds, known to the compiler as warp-uniform.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int64_t uniform(int64_t x) { return __shfl_sync(0xffffffffu, (long long)x, 0); }
 __device__ __forceinline__ const uint8_t* lane_ptr(const uint8_t* p, int lane) {
   return reinterpret_cast<const uint8_t*>(
       (uintptr_t)__shfl_sync(0xffffffffu, (unsigned long long)(uintptr_t)p, lane));
