@@ -42,7 +42,7 @@ constexpr int kChunkBytes = kTile * 128;               // 64 tokens x 64 values
 constexpr int kQuadBytes = kLatentQuad * kChunkBytes;  // 64 tokens x 256 values: [8 x 8 tokens][4][8][128 bytes]
 constexpr int kAtom = 1024;                            // eight tokens of a column: the swizzle's atom
 constexpr float kSlack = 8.0f;        // log2 of how far a logit may pass the reference
-constexpr float kNoMax = -1e30f;      // the reference before any visible token
+constexpr float kNoMax = -3e38f;      // the reference before any visible token
 constexpr int kSmemLimit = 232448;    // 227 KB opt-in shared memory per block
 constexpr int kSmall = 3072;          // alignment (1024), barriers and per-row values
 constexpr int kInFlight = 8;          // more tiles than the rings hold
@@ -690,7 +690,8 @@ Geometry geometry(int R, int B, int n_q, int Hq, int ctas) {
   g.n_rt = (g.rows + g.N - 1) / g.N;
   g.groups = ctas / g.n_rt > 1 ? ctas / g.n_rt : 1;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t slots = 2 * (size_t)g.groups * g.n_rt;
+  // a single group walks every sequence whole: no records
+  const size_t slots = g.groups > 1 ? 2 * (size_t)g.groups * g.n_rt : 0;
   g.meta = up(sizeof(int2) * (size_t)B * g.n_rt);
   g.ml = g.meta + up(sizeof(float2) * slots * g.N);
   g.total = g.ml + sizeof(float) * slots * g.N * R;

@@ -24,7 +24,7 @@ constexpr int kBlockBytes = kBlockTokens * 128;  // one column of a block
 constexpr int kAtom = 1024;              // eight tokens of a column: the swizzle's atom
 constexpr int kSmall = 3072;             // alignment (1024) and barriers
 constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3e38f;
 
 struct Params {
   LatentPrefillArgs a;
@@ -479,7 +479,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
           }
         }
       }
-      const uint64_t sc = pair2(P.scale, P.scale), mm = pair2(-m, -m);
+      // x scale - m in one rounding.  Beyond 2^24 the product's and the reference's roundings
+      // could differ by more than the exponential can take: there the product is rounded first.
+      float mul = P.scale;
+      if (__any_sync(0xffffffffu, fabsf(m) > 16777216.f)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] *= P.scale;
+        mul = 1.f;
+      }
+      const uint64_t sc = pair2(mul, mul), mm = pair2(-m, -m);
       uint64_t sum = l, sum1 = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

@@ -620,6 +620,46 @@ def test_expanded_magnitudes(factor):
     expanded_check(case, 50, 4, scale=SCALE / factor, factor=factor)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_expanded_zero_and_negative_scale(scale):
+    case, n_q, H = Case([40, 300], 512, seed=49), 40, 3
+    g = gen(51)
+    q = normal(g, 2, n_q, H, DH + P)
+    wk, wv = normal(g, H, DH, 512) / 22, normal(g, H, DH, 512) / 22
+    out = case.pool.latent_prefill_attention(0, q, wk, wv, case.table, case.ctx, scale)
+    for b in range(2):
+        ref, tol = expanded_ref(case, q[b], wk, wv, b, scale)
+        _, room = expanded_ref(case, q[b], wk, wv, b, abs(scale))  # the bounds count |scale|
+        err = (out[b].double() - ref).abs()
+        assert (err <= torch.maximum(tol, tol.clamp_min(0) + 2 * room)).all()
+
+
+@pytest.mark.parametrize("x", [1e29, -1e31, 2e37])
+def test_logits_near_the_end_of_fp32(x):
+    """Every logit the same huge value (an equal softmax), through the position part alone."""
+    case = Case([100], 512, seed=52)
+    rows = case.seq[0].clone()
+    rows[:, 512:] = 0
+    rows[:, 512] = 2.0 ** 60
+    tok = torch.arange(100, device="cuda")
+    one = torch.cat((torch.ones(1, 32), torch.zeros(1, 32)), 1).cuda()
+    case.pool.write_latent(0, case.table[0][(tok // 32).long()], (tok % 32).int(), rows, tok.int() * 0, one)
+    q = torch.zeros(1, 1, 4, 576, dtype=torch.bfloat16, device="cuda")
+    q[..., 512] = x / 2.0 ** 60
+    want = rows[:, :512].double().mean(0)
+    for ctas in (0, 1):
+        case.pool.decode_set_ctas(ctas)
+        out = case.pool.paged_latent_attention(0, q[..., :512], q[..., 512:], case.table, case.ctx, 1.0)
+        assert ((out[0, 0].double() - want).abs() <= U * want.abs() + U * rows[:, :512].double().abs().mean(0)).all()
+    wv = torch.zeros(4, 128, 512, dtype=torch.bfloat16, device="cuda")
+    wv[:, torch.arange(128), torch.arange(128)] = 1
+    qe = torch.zeros(1, 1, 4, 192, dtype=torch.bfloat16, device="cuda")
+    qe[..., 128] = x / 2.0 ** 60
+    out = case.pool.latent_prefill_attention(0, qe, wv, wv, case.table, case.ctx, 1.0)
+    assert ((out[0, 0].double() - want[:128]).abs() <=
+            U * want[:128].abs() + 2 * U * rows[:, :128].double().abs().mean(0)).all()
+
+
 def test_expanded_context_beyond_its_bound():
     case = Case([64, 90], 512, seed=47)
     g = gen(48)
