@@ -627,38 +627,42 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const __grid_consta
   auto slot_of = [&](int i) -> size_t {
     return i == 0 ? (size_t)meta.x : 2 * ((size_t)(g0 + i) * P.n_rt + rt);
   };
+  // the first records are asked for together with every record's reference
+  constexpr int U = 4;  // records in flight per warp
+  float4 v[U][V];
+  float2 ml[U];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + 4 * k;
+      if (i < n) {
+        const size_t at = slot_of(i) * N + rr;
+        ml[k] = P.ml[at];
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[k][e] = reinterpret_cast<const float4*>(P.acc + at * R)[lane + 32 * e];
+      }
+    }
+  };
+  load(warp);
   float M = kNoMax;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, P.ml[slot_of(i) * N + rr].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float s = 0.f;
   float4 acc[V] = {};
-  constexpr int U = 4;  // records in flight
   for (int i0 = warp; i0 < n; i0 += 4 * U) {
-    float4 v[U][V];
-    float w[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + 4 * k;
-      w[k] = 0.f;
-      if (i < n) {
-        const size_t at = slot_of(i) * N + rr;
-        const float2 ml = P.ml[at];
-        w[k] = ex2(ml.x - M);
-        s += w[k] * ml.y;
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[k][e] = reinterpret_cast<const float4*>(P.acc + at * R)[lane + 32 * e];
-      }
-    }
+    if (i0 != warp) load(i0);
 #pragma unroll
     for (int k = 0; k < U; ++k)
       if (i0 + 4 * k < n) {
+        const float w = ex2(ml[k].x - M);
+        s += w * ml[k].y;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          acc[e].x += w[k] * v[k][e].x;
-          acc[e].y += w[k] * v[k][e].y;
-          acc[e].z += w[k] * v[k][e].z;
-          acc[e].w += w[k] * v[k][e].w;
+          acc[e].x += w * v[k][e].x;
+          acc[e].y += w * v[k][e].y;
+          acc[e].z += w * v[k][e].z;
+          acc[e].w += w * v[k][e].w;
         }
       }
   }

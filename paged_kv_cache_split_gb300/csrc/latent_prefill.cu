@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int vis = off + i + 1;
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
     float m = kNoMax;
-    uint64_t l = 0;  // two partial sums
+    uint64_t l = 0;    // two partial sums
+    bool big = false;  // the warp has a reference beyond 2^24
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
@@ -466,6 +467,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         const float f = ex2(m - mn);
         m = mn;
         l = mul2(l, pair2(f, f));
+        big = __any_sync(0xffffffffu, fabsf(m) > 16777216.f);
         if (j > 0) {
           // the products of the tile before are complete: this S was issued after them
 #pragma unroll 1
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       // x scale - m in one rounding.  Beyond 2^24 the product's and the reference's roundings
       // could differ by more than the exponential can take: there the product is rounded first.
       float mul = P.scale;
-      if (__any_sync(0xffffffffu, fabsf(m) > 16777216.f)) {
+      if (big) {
 #pragma unroll
         for (int c = 0; c < 128; ++c) x[c] *= P.scale;
         mul = 1.f;
