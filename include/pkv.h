@@ -474,7 +474,8 @@ pkv_status pkv_paged_latent_attention(pkv_pool* pool, int layer, int B, int n_q,
                                       void* stream);
 
 /* Workspace bytes of pkv_latent_prefill_attention: the expanded keys and values of B
- * contexts of at most max_ctx tokens (0 or above max_blocks * 32: max_blocks * 32).
+ * contexts of at most max_ctx tokens (0 or above max_blocks * 32: max_blocks * 32), and,
+ * where few queries leave SMs idle, the partial results of a split over the context.
  * Host only; the limits are those of that call. */
 pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq, int max_blocks,
                                               int max_ctx, size_t* bytes);

@@ -87,7 +87,7 @@ struct LatentPrefillArgs {
   int device;
   cudaStream_t stream;
 };
-size_t latent_prefill_workspace(int B, int Hq, int max_ctx);
+size_t latent_prefill_workspace(int B, int n_q, int Hq, int max_ctx, int ctas);
 // A bf16 tensor map of `rank` dimensions (dims[0] contiguous, strides in bytes from the
 // second on), read in boxes with the 128-byte swizzle; false if the driver refuses it.
 bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,

@@ -34,6 +34,9 @@ struct Params {
   int negative;         // scale < 0
   uint16_t* k;          // [B, Hq, T, DH]
   uint16_t* v;
+  int splits;           // parts of a unit's key tiles; more than one leave records to be merged
+  float* acc;           // [units * Hq][splits][2 * kTile][DH]
+  float2* ml;           // [units * Hq][splits][2 * kTile]: (reference, sum)
   CUtensorMap wk_map, wv_map, q_map, k_map, v_map;
 };
 
@@ -290,6 +293,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
 // than 2^8, which is when the row's O is rescaled.  Keys and values arrive in 16 KB
 // slots (K: two of 64 dims and one of the position keys, straight from the pool's blocks;
 // V: two of 64 keys, so that one MMA covers all 128 value columns), eight in the ring.
+//
+// Few queries over long contexts make fewer CTAs than there are SMs: the key tiles are then
+// split over several CTAs (blockIdx.y), which leave FP32 records (reference, sum, O) for a
+// merge kernel (SPLIT; without it the launch has one part and writes the output itself).
 // ---------------------------------------------------------------------------
 // Warps 0..3 and 4..7: softmax of a tile each; 8: copies; 9: MMAs; 10, 11 fill the third
 // warpgroup, which gives registers to the other two: 2 x 200 + 104 = 3 x 168, the launch
@@ -342,6 +349,7 @@ struct AttnSmall {
 };
 static_assert(sizeof(AttnSmall) <= kSmall - 1024, "small state");
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -398,6 +406,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   bool bad;
   const int32_t L = uniform(context(P, b, &bad));
   if (L == 0) {
+    if (blockIdx.y > 0) return;
     if (bad && pair == 0 && h == 0 && threadIdx.x == 0) atomicOr(err, ERR_CTX);
     const int n = min(2 * kTile, n_q - i0);
     for (int i = threadIdx.x; i < n * (DH / 8); i += kAttnThreads)
@@ -416,7 +425,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int last = min(n_q, i0 + (t + 1) * kTile) - 1;
     return last < i0 + t * kTile ? 0 : uniform((off + last + 1 + kTile - 1) / kTile);
   };
-  const int nt0 = key_tiles(0), nt1 = key_tiles(1), nmax = max(nt0, nt1);
+  const int all0 = key_tiles(0), all1 = key_tiles(1), all = max(all0, all1);
+  // this CTA's key tiles: from j0 on, numbered from 0 below
+  int j0 = 0, nmax = all, nt0 = all0, nt1 = all1;
+  if constexpr (SPLIT) {
+    const int per = (all + P.splits - 1) / P.splits;
+    j0 = uniform((int)blockIdx.y * per);
+    nmax = uniform(max(0, min(per, all - j0)));
+    nt0 = uniform(max(0, min(nmax, all0 - j0)));
+    nt1 = uniform(max(0, min(nmax, all1 - j0)));
+  }
 
   // The warpgroups' paths do not rejoin: each ends in a return.
   if (warp < 8) {
@@ -448,8 +466,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
 #pragma unroll
         for (int c = 0; c < 128; ++c) x[c] = -x[c];
       }
-      if ((j + 1) * kTile > vis_first) {
-        const int n = vis - j * kTile;  // this query sees the tile's first n keys
+      if ((j0 + j + 1) * kTile > vis_first) {
+        const int n = vis - (j0 + j) * kTile;  // this query sees the tile's first n keys
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (c >= n) x[c] = -INFINITY;
@@ -514,19 +532,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       }
       l = add2(sum, sum1);
     }
+    float l0, l1;
+    split2(l, l0, l1);
+    const float sum = l0 + l1;
+    int64_t rec = 0;
+    if constexpr (SPLIT) {
+      rec = (((int64_t)unit * P.a.Hq + h) * P.splits + blockIdx.y) * (2 * kTile) + t * kTile + (warp & 3) * 32 + lane;
+      P.ml[rec] = make_float2(m, sum);  // a sum of 0: no tile here, and no O
+    }
     if (ntt > 0) {
       wait_or_die(&sm.o_full[t], 0, dead, err);
       tc_fence_after();
-      float l0, l1;
-      split2(l, l0, l1);
-      const float inv = 1.f / (l0 + l1);
+      const float inv = 1.f / sum;
       uint4* out = reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i) * P.a.Hq + h) * DH);
+      float4* acc = reinterpret_cast<float4*>(P.acc + rec * DH);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t o[32];
         tc_ld_rows<32>(tm_o + 32 * q, o);
         tc_wait_ld();
-        if (i < n_q) {
+        if (SPLIT && i < n_q) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            acc[8 * q + c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                         __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+        } else if (i < n_q) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[4];
@@ -557,14 +587,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     }
     // Key tile j takes the ring's next five slots: K 0..2, V 3..4.  Eight slots before, slot
     // 0 held the last of K(j - 2), 1 and 2 V(j - 2), 3 and 4 the first of K(j - 1).
-    const int row0 = (b * P.a.Hq + h) * P.T;
+    const int row0 = (b * P.a.Hq + h) * P.T + j0 * kTile;
     int nk = 0, nv = 0;  // tiles whose copies were started
     bool alive = true;
     for (int jb = 0; alive && jb < nmax; jb += 8) {
       // lane l looks up block 4 jb + l
-      const int blk = 4 * jb + lane;
+      const int blk = 4 * (j0 + jb) + lane;
       int y0 = 0;
-      const uint8_t* map = blk < 4 * nmax && blk * kBlockTokens < L ? block_map(P, b, blk, &y0) : nullptr;
+      const uint8_t* map = blk < 4 * (j0 + nmax) && blk * kBlockTokens < L ? block_map(P, b, blk, &y0) : nullptr;
       const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
       const int je = min(jb + 8, nmax);
 #pragma unroll 1
@@ -669,20 +699,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   }
 }
 
+// Merge of a row's records, one warp per row.
+__global__ void __launch_bounds__(256) latent_prefill_merge_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // (b, i, h)
+  if (row >= (int64_t)P.a.B * P.a.n_q * P.a.Hq) return;
+  const int h = (int)(row % P.a.Hq), i = (int)(row / P.a.Hq % P.a.n_q), b = (int)(row / P.a.Hq / P.a.n_q);
+  const int unit = i / (2 * kTile) * P.a.B + b;
+  const int64_t rec = ((int64_t)unit * P.a.Hq + h) * P.splits * (2 * kTile) + i % (2 * kTile);
+  bool bad;
+  if (context(P, b, &bad) == 0) return;  // zeros are written
+  float M = kNoMax;
+  for (int k = lane; k < P.splits; k += 32) {
+    const float2 ml = P.ml[rec + (int64_t)k * (2 * kTile)];
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float sum = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < P.splits; ++k) {
+    const int64_t at = rec + (int64_t)k * (2 * kTile);
+    const float2 ml = P.ml[at];
+    if (ml.y != 0.f) {
+      const float w = ex2(ml.x - M);
+      const float4 o = reinterpret_cast<const float4*>(P.acc + at * DH)[lane];
+      sum += w * ml.y;
+      a.x += w * o.x, a.y += w * o.y, a.z += w * o.z, a.w += w * o.w;
+    }
+  }
+  const float inv = 1.f / sum;
+  reinterpret_cast<uint2*>(P.a.out + row * DH)[lane] = make_uint2(bf2(a.x * inv, a.y * inv), bf2(a.z * inv, a.w * inv));
+}
+
+// Parts of the key tiles: as many as fill the SMs once, each of at least four tiles (a part
+// costs about as much as three: its start, its records and their merge).
+int prefill_splits(int B, int n_q, int Hq, int max_ctx, int ctas) {
+  const int64_t launch = (int64_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * B * Hq;
+  const int tiles = (max_ctx + kTile - 1) / kTile;
+  const int64_t fill = ctas / launch, most = tiles / 4;
+  const int64_t n = fill < most ? fill : most;
+  return n > 1 ? (int)n : 1;
+}
+
 int tile_up(int x) { return (x + kTile - 1) / kTile * kTile; }
 
 }  // namespace
 
-size_t latent_prefill_workspace(int B, int Hq, int max_ctx) {
-  return 256 + (size_t)2 * B * Hq * (size_t)tile_up(max_ctx) * DH * sizeof(uint16_t);
+namespace {
+// Offsets of the workspace: keys, values, records.
+struct Layout {
+  int splits;
+  size_t v, acc, ml, total;
+};
+Layout prefill_layout(int B, int n_q, int Hq, int max_ctx, int ctas) {
+  Layout w;
+  w.splits = prefill_splits(B, n_q, Hq, max_ctx, ctas);
+  w.v = (size_t)B * Hq * (size_t)tile_up(max_ctx) * DH * sizeof(uint16_t);  // a multiple of 256
+  w.acc = 2 * w.v;
+  const size_t rows =
+      w.splits > 1 ? (size_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * B * Hq * w.splits * (2 * kTile) : 0;
+  w.ml = w.acc + rows * DH * sizeof(float);
+  w.total = w.ml + rows * sizeof(float2) + 256;
+  return w;
+}
+}  // namespace
+
+size_t latent_prefill_workspace(int B, int n_q, int Hq, int max_ctx, int ctas) {
+  return prefill_layout(B, n_q, Hq, max_ctx, ctas).total;
 }
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
   Params P;
   P.a = a;
   P.T = tile_up(a.max_ctx);
-  P.k = (uint16_t*)a.ws;
-  P.v = P.k + (size_t)a.B * a.Hq * P.T * DH;
+  const Layout lay = prefill_layout(a.B, a.n_q, a.Hq, a.max_ctx, a.ctas);
+  uint8_t* ws = (uint8_t*)a.ws;
+  P.k = (uint16_t*)ws;
+  P.v = (uint16_t*)(ws + lay.v);
+  P.acc = (float*)(ws + lay.acc);
+  P.ml = (float2*)(ws + lay.ml);
+  P.splits = lay.splits;
   // -inf (a hidden key) times 0 would be NaN: a scale of 0 becomes a tiny one
   P.scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
   P.negative = a.scale_log2 < 0.f;
@@ -707,14 +807,21 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
                    : tc_launch(latent_expand_kernel<256>, grid, kExpandThreads, smem, a.stream, P, a.device, &raised[1]);
     if (e != cudaSuccess) return e;
   }
-  static const int regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, latent_prefill_kernel) == cudaSuccess ? fa.numRegs : -1;
+  static const bool regs_ok = [] {
+    cudaFuncAttributes f0, f1;
+    return cudaFuncGetAttributes(&f0, latent_prefill_kernel<false>) == cudaSuccess && f0.numRegs == kAttnRegs &&
+           cudaFuncGetAttributes(&f1, latent_prefill_kernel<true>) == cudaSuccess && f1.numRegs == kAttnRegs;
   }();
-  if (regs != kAttnRegs) return cudaErrorInvalidDeviceFunction;
-  static std::atomic<uint64_t> raised{0};
-  return tc_launch(latent_prefill_kernel, dim3((unsigned)((int64_t)P.pairs * a.B * a.Hq)), kAttnThreads,
-                   (size_t)(kSmall + 2 * kQTile + kSlots * kSlot), a.stream, P, a.device, &raised);
+  if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+  static std::atomic<uint64_t> raised[2];
+  const bool split = P.splits > 1;
+  const cudaError_t e = tc_launch(split ? latent_prefill_kernel<true> : latent_prefill_kernel<false>,
+                                  dim3((unsigned)((int64_t)P.pairs * a.B * a.Hq), (unsigned)P.splits), kAttnThreads,
+                                  (size_t)(kSmall + 2 * kQTile + kSlots * kSlot), a.stream, P, a.device, &raised[split]);
+  if (e != cudaSuccess || !split) return e;
+  const int64_t rows = (int64_t)a.B * a.n_q * a.Hq;
+  return tc_launch(latent_prefill_merge_kernel, dim3((unsigned)((rows + 7) / 8)), 256, (size_t)0, a.stream, P, a.device,
+                   &raised[0]);
 }
 
 }  // namespace pkv

@@ -866,7 +866,7 @@ pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* p, int B, int n_q,
     return PKV_ERR_INVALID;
   if (p->cfg.format != PKV_FMT_LATENT) return PKV_ERR_FORMAT;
   if (!latent_prefill_fits(B, Hq, latent_prefill_ctx(max_blocks, max_ctx))) return PKV_ERR_INVALID;
-  *bytes = latent_prefill_workspace(B, Hq, latent_prefill_ctx(max_blocks, max_ctx));
+  *bytes = latent_prefill_workspace(B, n_q, Hq, latent_prefill_ctx(max_blocks, max_ctx), decode_grid(p));
   return PKV_OK;
 }
 
@@ -885,7 +885,8 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   LatentPrefillArgs a;
   a.max_ctx = latent_prefill_ctx(max_blocks, max_ctx);
   if (!latent_prefill_fits(B, Hq, a.max_ctx)) return PKV_ERR_INVALID;
-  if (ws_bytes < latent_prefill_workspace(B, Hq, a.max_ctx)) return PKV_ERR_INVALID;
+  a.ctas = decode_grid(p);
+  if (ws_bytes < latent_prefill_workspace(B, n_q, Hq, a.max_ctx, a.ctas)) return PKV_ERR_INVALID;
   a.lv = layer_view(p, layer);
   a.R = p->cfg.head_dim;
   a.B = B;
@@ -900,7 +901,6 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.out = (uint16_t*)out;
   a.ws = ws;
-  a.ctas = p->n_sm;
   a.device = p->device;
   a.stream = (cudaStream_t)stream;
   PKV_CUDA(launch_latent_prefill(a), "latent_prefill_attention launch");

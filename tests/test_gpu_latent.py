@@ -580,6 +580,18 @@ def test_expanded_lengths(L):
     expanded_check(Case([L], 512, seed=L, extra=3), 1, 2, seed=L, max_ctx=L)
 
 
+@pytest.mark.parametrize("ctas", [1, 7, 40, 152, 400])
+@pytest.mark.parametrize("n_q,H,lens", [(1, 1, [5000]), (3, 2, [4100, 4, 2000]), (300, 1, [3000, 301, 0]),
+                                        (129, 3, [1025])])
+def test_expanded_split_over_the_context(ctas, n_q, H, lens):
+    """Every number of parts the launch may choose, some of them past a sequence's last tile;
+    repeats are bit-identical."""
+    case = Case(lens, 512, seed=n_q + H)
+    case.pool.decode_set_ctas(ctas)
+    a = expanded_check(case, n_q, H, seed=ctas)
+    assert torch.equal(a, expanded_check(case, n_q, H, seed=ctas))
+
+
 def test_expanded_many_heads_and_a_long_context():
     expanded_check(Case([5000], 512, seed=41), 140, 40, max_ctx=5000)
 
