@@ -492,8 +492,10 @@ pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* pool, int B, int n
  *   workspace: 256-byte aligned, ws_bytes >= pkv_latent_prefill_workspace_bytes of the
  *              same arguments, not initialised
  * Lengths, errors, limits, alignment and B = 0 as for pkv_paged_latent_attention,
- * max_blocks <= 2^20 and B * Hq * (the bound on ctx_lens + 128) < 2^31.  Expanded keys and values and the probabilities are rounded
- * to bf16 once; sums and softmax state are fp32.  Deterministic.  Asynchronous. */
+ * max_blocks <= 2^20 and B * Hq * (the bound on ctx_lens + 128) < 2^31.  Expanded keys are rounded to bf16, and
+ * expanded values and the probabilities to fp16 (scaled by powers of two, so that any
+ * magnitude fits), once; sums and softmax state are fp32.  Deterministic.
+ * Asynchronous. */
 pkv_status pkv_latent_prefill_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_bf16,
                                         const void* w_k, const void* w_v, const int32_t* block_table_dev,
                                         int max_blocks, const int32_t* ctx_lens_dev, int max_ctx, float scale,

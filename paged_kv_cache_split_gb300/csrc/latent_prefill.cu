@@ -32,8 +32,9 @@ struct Params {
   int pairs;            // query tile pairs a sequence (attention)
   float scale;          // |scale| log2(e)
   int negative;         // scale < 0
-  uint16_t* k;          // [B, Hq, T, DH]
-  uint16_t* v;
+  uint16_t* k;          // [B, Hq, T, DH] bf16
+  uint16_t* v;          // [B, Hq, T, DH] fp16, each tile of 128 tokens divided by 2^its exponent
+  int32_t* v_exp;       // [B, Hq, T / 128]
   int splits;           // parts of a unit's key tiles; more than one leave records to be merged
   float* acc;           // [units * Hq][splits][2 * kTile][DH]
   float2* ml;           // [units * Hq][splits][2 * kTile]: (reference, sum)
@@ -66,6 +67,12 @@ __device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int 
 // CTAs.  A tile's latents stay in shared memory over its heads, so only the weights stream
 // (from L2, through a ring of 64-wide k-chunks); two accumulators of 256 columns let the
 // epilogue of one item run under the products of the next.
+//
+// Keys are stored in bf16, the type of the queries they meet.  Values meet probabilities,
+// which the attention makes itself: both are fp16, whose three more bits halve the output's
+// error (relative L2 0.0028 -> 0.0022; the bf16 output alone has 0.0017).  Any magnitude
+// fits, as a tile's values are divided by the power of two that puts the largest in
+// [2^13, 2^14), and the attention puts the power back into the probabilities' exponent.
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 320;  // warps 0..3 store keys, 4..7 values; 8 copies, 9 MMAs
 constexpr int kWStages = 3;
@@ -115,6 +122,7 @@ struct Items {
 template <int R>
 struct ExpandSmall {
   uint64_t a_full[R / 64], a_empty[R / 64], w_full[kWStages], w_empty[kWStages], d_full[2], d_free[2], drain;
+  float v_max[2][4];  // by parity of the item: the value warps' largest magnitudes
   uint32_t tmem;
   int dead;
 };
@@ -158,6 +166,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
       tc_fence_after();
       // first of the eight rows that this lane's group of eight stores together
       const int64_t row0 = ((int64_t)it.b * P.a.Hq + it.h) * P.T + (t & ~7);
+      const uint32_t acc = tmem + (n & 1) * 256 + kind * DH + ((uint32_t)((warp & 3) * 32) << 16);
+      float scale = 1.f;
+      if (kind) {
+        float mx = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[32];
+          tc_ld_rows<32>(acc + q * 32, r);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(__uint_as_float(r[i])));
+        }
+        if (t >= L) mx = 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        if (lane == 0) sm.v_max[n & 1][warp & 3] = mx;
+        named_barrier_sync(1, 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sm.v_max[n & 1][i]);
+        const int e = mx > 0.f ? max(-110, min(110, (int)(__float_as_uint(mx) >> 23) - 127 - 13)) : 0;
+        scale = pow2(-e);
+        if (threadIdx.x == 128) P.v_exp[((int64_t)it.b * P.a.Hq + it.h) * (P.T / kTile) + it.tile] = e;
+      }
 #pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         // 64 columns of this thread's row as eight 16-byte pieces.  Rows past the context
@@ -167,12 +198,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t r[32];
-          tc_ld_rows<32>(tmem + (n & 1) * 256 + kind * DH + q * 64 + half * 32 + ((uint32_t)((warp & 3) * 32) << 16), r);
+          tc_ld_rows<32>(acc + q * 64 + half * 32, r);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            v[4 * half + (i >> 2)][i & 3] =
-                t < L ? bf2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
+          for (int i = 0; i < 16; ++i) {
+            const float lo = __uint_as_float(r[2 * i]), hi = __uint_as_float(r[2 * i + 1]);
+            v[4 * half + (i >> 2)][i & 3] = t >= L ? 0u : kind ? fp16x2(lo * scale, hi * scale) : bf2(lo, hi);
+          }
         }
         // Transpose the pieces among eight lanes, so that lane l holds piece l of eight rows
         // and a store of the group fills a 128-byte line (one thread's own row, 16 bytes a
@@ -288,9 +320,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
 // Attention: a CTA takes two tiles of 128 queries of one head.  S = Q K^T (12 k-steps)
 // and O += P V (8 k-steps) of the two tiles alternate on the tensor cores, so that one
 // tile's softmax runs under the other's products.  A thread owns a query: its row of S
-// comes from tensor memory into registers, P goes back over it in bf16 and is the next
-// product's A operand there.  The reference m moves only when a logit passes it by more
-// than 2^8, which is when the row's O is rescaled.  Keys and values arrive in 16 KB
+// comes from tensor memory into registers, P goes back over it in fp16 and is the next
+// product's A operand there.  The reference m, a whole number, moves only when a logit
+// passes it by more than 2^8, which is when the row's O is rescaled.  P carries 2^(7 + the
+// key tile's exponent - the largest tile's), at most 2^15.5, so that O is in units of
+// 2^(largest - 7) throughout; a part of P below 2^-21 of the largest loses bits.  Keys and values arrive in 16 KB
 // slots (K: two of 64 dims and one of the position keys, straight from the pool's blocks;
 // V: two of 64 keys, so that one MMA covers all 128 value columns), eight in the ring.
 //
@@ -446,11 +480,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int i = i0 + t * kTile + (warp & 3) * 32 + lane;
     const int vis = off + i + 1;
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
+    const int32_t* v_exp = P.v_exp + ((int64_t)b * P.a.Hq + h) * (P.T / kTile);
+    int top_exp = -110;
+    for (int k = lane; k < all; k += 32) top_exp = max(top_exp, __ldg(v_exp + k));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top_exp = max(top_exp, __shfl_xor_sync(0xffffffffu, top_exp, d));
     float m = kNoMax;
     uint64_t l = 0;    // two partial sums
     bool big = false;  // the warp has a reference beyond 2^24
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
+      const int lift = max(-110, __ldg(v_exp + j0 + j) - top_exp) + 7;  // this tile's power in P
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
       tc_fence_after();
       float x[128];
@@ -481,11 +521,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
       const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale;
       if (__any_sync(0xffffffffu, top > m + kSlack)) {
-        const float mn = fmaxf(m, top);
+        const float mn = fmaxf(m, rintf(top));
         const float f = ex2(m - mn);
         m = mn;
         l = mul2(l, pair2(f, f));
-        big = __any_sync(0xffffffffu, fabsf(m) > 16777216.f);
+        big = __any_sync(0xffffffffu, fabsf(m) > 16777216.f && m > kNoMax);
         if (j > 0) {
           // the products of the tile before are complete: this S was issued after them
 #pragma unroll 1
@@ -507,8 +547,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         for (int c = 0; c < 128; ++c) x[c] *= P.scale;
         mul = 1.f;
       }
-      const uint64_t sc = pair2(mul, mul), mm = pair2(-m, -m);
-      uint64_t sum = l, sum1 = 0;
+      const float ref = (float)lift - m;  // exact below 2^24, and the sum takes the same P
+      const uint64_t sc = pair2(mul, mul), mm = pair2(ref, ref);
+      uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t w[16];
@@ -518,9 +559,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
           split2(fma2(pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]), sc, mm), e0, e1);
           e0 = ex2(e0);
           e1 = ex2(e1);
-          uint64_t& s = c & 1 ? sum1 : sum;
+          uint64_t& s = c & 1 ? sum1 : sum0;
           s = add2(s, pair2(e0, e1));
-          w[c] = bf2(e0, e1);
+          w[c] = fp16x2(e0, e1);
         }
         tc_st_rows<16>(tm_s + 16 * q, w);
         if (q & 1) {
@@ -530,7 +571,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
           mbar_arrive(&sm.p_full[t][q >> 1]);
         }
       }
-      l = add2(sum, sum1);
+      const float back = pow2(-lift);
+      l = fma2(add2(sum0, sum1), pair2(back, back), l);
     }
     float l0, l1;
     split2(l, l0, l1);
@@ -543,7 +585,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     if (ntt > 0) {
       wait_or_die(&sm.o_full[t], 0, dead, err);
       tc_fence_after();
-      const float inv = 1.f / sum;
+      const float unit_o = pow2(top_exp - 7), inv = unit_o / sum;
       uint4* out = reinterpret_cast<uint4*>(P.a.out + (((int64_t)b * n_q + i) * P.a.Hq + h) * DH);
       float4* acc = reinterpret_cast<float4*>(P.acc + rec * DH);
 #pragma unroll 1
@@ -554,8 +596,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         if (SPLIT && i < n_q) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            acc[8 * q + c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                         __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+            acc[8 * q + c] =
+                make_float4(__uint_as_float(o[4 * c]) * unit_o, __uint_as_float(o[4 * c + 1]) * unit_o,
+                            __uint_as_float(o[4 * c + 2]) * unit_o, __uint_as_float(o[4 * c + 3]) * unit_o);
         } else if (i < n_q) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -637,7 +680,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
   } else if (warp == 9) {
     // -------------------------------------------------------------------- MMAs
     constexpr uint32_t id_s = tc_idesc(128, 128, false, false);
-    constexpr uint32_t id_o = tc_idesc(128, 128, false, true);
+    constexpr uint32_t id_o = tc_idesc(128, 128, false, true, true);
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ring), 16, 1024);
     const uint64_t d_v = tc_desc(smem_u32(ring), kSlot / 2, 1024);  // [2 x 64 values][64 keys], MN-major
     bool alive = true;
@@ -750,16 +793,17 @@ int tile_up(int x) { return (x + kTile - 1) / kTile * kTile; }
 }  // namespace
 
 namespace {
-// Offsets of the workspace: keys, values, records.
+// Offsets of the workspace: keys, values and their exponents, records.
 struct Layout {
   int splits;
-  size_t v, acc, ml, total;
+  size_t v, v_exp, acc, ml, total;
 };
 Layout prefill_layout(int B, int n_q, int Hq, int max_ctx, int ctas) {
   Layout w;
   w.splits = prefill_splits(B, n_q, Hq, max_ctx, ctas);
   w.v = (size_t)B * Hq * (size_t)tile_up(max_ctx) * DH * sizeof(uint16_t);  // a multiple of 256
-  w.acc = 2 * w.v;
+  w.v_exp = 2 * w.v;
+  w.acc = w.v_exp + ((size_t)B * Hq * (size_t)(tile_up(max_ctx) / kTile) * sizeof(int32_t) + 255) / 256 * 256;
   const size_t rows =
       w.splits > 1 ? (size_t)((n_q + 2 * kTile - 1) / (2 * kTile)) * B * Hq * w.splits * (2 * kTile) : 0;
   w.ml = w.acc + rows * DH * sizeof(float);
@@ -780,6 +824,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a) {
   uint8_t* ws = (uint8_t*)a.ws;
   P.k = (uint16_t*)ws;
   P.v = (uint16_t*)(ws + lay.v);
+  P.v_exp = (int32_t*)(ws + lay.v_exp);
   P.acc = (float*)(ws + lay.acc);
   P.ml = (float2*)(ws + lay.ml);
   P.splits = lay.splits;

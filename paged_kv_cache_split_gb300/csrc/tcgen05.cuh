@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -22,9 +23,9 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem_addr, uint32_t lbo, ui
          (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: bf16 A and B, FP32 D; a_mn: A is MN-major, b_mn: B is.
-__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+// Instruction descriptor: bf16 (or fp16) A and B, FP32 D; a_mn: A is MN-major, b_mn: B is.
+__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn, bool fp16 = false) {
+  return (1u << 4) | (fp16 ? 0u : (1u << 7) | (1u << 10)) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
@@ -193,6 +194,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^e, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t fp16x2(float lo, float hi) {
+  const __half2 t = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&t);

@@ -10,8 +10,10 @@ relative to the value):
   absorbed   u |y| for the output, u sum p |c| for the probabilities' rounding, and
              2 d sum p |c| for the logits, d the fp32 error of a dot product of W terms,
              W 2^-23 scale sum |q k| (the bound of any summation order, truncating or not);
-  expanded   the same with one more u sum p |v| for the values' rounding, and the keys'
-             rounding, u scale sum |q k|, inside d.
+  expanded   u |y| for the output, 2 h sum p |v| for the probabilities' and the values'
+             rounding to fp16 (h = 2^-11; values far below the largest of their 128 tokens
+             lose at most 2^-25 of that), the logits as above, with the keys' rounding, u
+             scale sum |q k|, inside d.
 The elementwise bounds are worst cases; a relative L2 bound holds the average: each
 rounding contributes at most u / sqrt(3) in the mean square, at most four of them with
 logits of unit size, so 2 u < 1e-2."""
@@ -27,6 +29,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 U = 2.0 ** -8
+H16 = 2.0 ** -11
 P, DH = 64, 128
 
 
@@ -126,7 +129,7 @@ def expanded_ref(case, q, wk, wv, b, scale):
         d = (U + (DH + P) * 2.0 ** -23) * scale * ((qh.abs() @ k.abs().t()) * seen).amax(-1, keepdim=True)
         out, mag = p @ v, p @ v.abs()
         outs.append(out)
-        tols.append(U * out.abs() + (2 * U + 2 * d) * mag + 1e-30)
+        tols.append(U * out.abs() + (2 * H16 + 2 * d) * mag + 2.0 ** -24 * v.abs().max() + 1e-30)
     return torch.stack(outs, 1), torch.stack(tols, 1)
 
 
@@ -670,6 +673,39 @@ def test_logits_near_the_end_of_fp32(x):
     out = case.pool.latent_prefill_attention(0, qe, wv, wv, case.table, case.ctx, 1.0)
     assert ((out[0, 0].double() - want[:128]).abs() <=
             U * want[:128].abs() + 2 * U * rows[:, :128].double().abs().mean(0)).all()
+
+
+@pytest.mark.parametrize("e", [-12, 12])
+def test_expanded_values_of_mixed_magnitudes(e):
+    """The first 200 tokens' latents 2^e times the others', and queries that look at either
+    part alone (through the position keys)."""
+    L, n_q, H = 700, 6, 2
+    case = Case([L], 512, seed=53)
+    rows = case.seq[0].clone()
+    rows[:200, :512] = (rows[:200, :512].float() * 2.0 ** e).bfloat16()
+    rows[:, 512:] = 0
+    rows[:200, 512] = 1
+    rows[200:, 513] = 1
+    tok = torch.arange(L, device="cuda")
+    one = torch.cat((torch.ones(1, 32), torch.zeros(1, 32)), 1).cuda()
+    case.pool.write_latent(0, case.table[0][(tok // 32).long()], (tok % 32).int(), rows, tok.int() * 0, one)
+    g = gen(54)
+    wv = normal(g, H, DH, 512) / 22
+    wk = torch.zeros_like(wv)
+    q = torch.zeros(1, n_q, H, DH + P, dtype=torch.bfloat16, device="cuda")
+    q[:, ::2, :, DH] = 400
+    q[:, 1::2, :, DH + 1] = 400
+    for ctas in (0, 1):
+        case.pool.decode_set_ctas(ctas)
+        out = case.pool.latent_prefill_attention(0, q, wk, wv, case.table, case.ctx, 1.0)
+        kv = rows.double()
+        for i in range(n_q):
+            part = kv[:200] if i % 2 == 0 else kv[200:L - n_q + i + 1]
+            for h in range(H):
+                v = part[:, :512] @ wv[h].double().t()
+                want = v.mean(0)
+                tol = U * want.abs() + 2 * H16 * v.abs().mean(0) + 2.0 ** -24 * v.abs().max()
+                assert ((out[0, i, h].double() - want).abs() <= tol).all(), (i, h, ctas)
 
 
 def test_expanded_context_beyond_its_bound():
