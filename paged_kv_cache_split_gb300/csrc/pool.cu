@@ -767,8 +767,17 @@ pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, 
     if (!q_rope || !q_out) return PKV_ERR_INVALID;
     for (int64_t x : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
       if (x < 0 || x % 8) return PKV_ERR_INVALID;
-    // output rows must not overlap one another
-    if ((Hq > 1 && out_head_stride < kRope) || (n > 1 && out_token_stride < kRope)) return PKV_ERR_INVALID;
+    // Output rows must not overlap one another: heads within a token's span, or tokens within
+    // a head's.
+    const int64_t t = n > 1 ? out_token_stride : 0, h = Hq > 1 ? out_head_stride : 0;
+    if ((n > 1 && t < kRope) || (Hq > 1 && h < kRope)) return PKV_ERR_INVALID;
+    if (n > 1 && Hq > 1) {
+      // (n - 1) t + kRope <= h, without the product's overflow
+      const bool tokens_inside = t <= (h - kRope) / (n - 1), heads_inside = h <= (t - kRope) / (Hq - 1);
+      if (!tokens_inside && !heads_inside) return PKV_ERR_INVALID;
+    }
+    // in place, a row's output is its own input
+    if (q_out == q_rope && ((n > 1 && t != q_token_stride) || (Hq > 1 && h != q_head_stride))) return PKV_ERR_INVALID;
   }
   LatentWriteArgs a;
   a.lv = layer_view(p, layer);
@@ -818,7 +827,8 @@ pkv_status pkv_paged_latent_attention(pkv_pool* p, int layer, int B, int n_q, in
   pkv_status st = latent_check(p, layer);
   if (st != PKV_OK) return st;
   const int R = p->cfg.head_dim;
-  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || !std::isfinite(scale)) return PKV_ERR_INVALID;
+  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || !std::isfinite(scale))
+    return PKV_ERR_INVALID;
   if (B == 0) return PKV_OK;
   if (!q_latent || !q_rope || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
   if (q_latent_stride < R || q_latent_stride % 8 || q_rope_stride < kRope || q_rope_stride % 8) return PKV_ERR_INVALID;
@@ -913,6 +923,8 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
     return PKV_ERR_INVALID;
   if (r->Hq % p->cfg.n_kv_heads) return PKV_ERR_INVALID;
   if (r->n_q > 1 && (int64_t)r->B * r->n_q > 4096) return PKV_ERR_INVALID;
+  const bool latent = p->cfg.format == PKV_FMT_LATENT;
+  if (latent && (!latent_sizes_ok(r->B, r->n_q, r->Hq) || r->max_blocks > kLatentMaxBlocks)) return PKV_ERR_INVALID;
   const int64_t free_rows = (int64_t)p->free_rows.size();
   const int64_t deficit = r->new_blocks > free_rows ? r->new_blocks - free_rows : 0;
   const int64_t slabs = (deficit + p->cfg.slab_blocks - 1) / p->cfg.slab_blocks;
@@ -924,7 +936,6 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
   out->free_rows = free_rows;
   out->storage_bytes = (uint64_t)slabs * (uint64_t)p->group_bytes;
   out->page_bytes = (uint64_t)r->new_blocks * (uint64_t)block_bytes * (uint64_t)p->cfg.n_layers;
-  const bool latent = p->cfg.format == PKV_FMT_LATENT;
   const uint64_t q_out = 2ull * (uint64_t)p->cfg.head_dim + (latent ? kRope : 0);  // values of a q and an output row
   out->fixed_bytes = (uint64_t)r->max_blocks * 4u + 4u + (uint64_t)r->n_q * (uint64_t)r->Hq * q_out * 2u;
   if (latent) {

@@ -927,3 +927,79 @@ def test_empty_calls():
     p.latent_prefill_attention(0, q[..., :192].contiguous(), w, w, bt0, i32([0, 0]), 0.1, out=out)
     assert not out.any()
     assert p.check_errors() == 0
+
+
+def test_limits_of_pricing_and_of_the_block_table():
+    a = Case([40], R=256)
+    for B, Hq, n_q, mb in ((1, 2048, 1, 2), (4097, 1, 1, 2), (1, 1 << 30, 4, 2), (1, 16, 1, (1 << 20) + 1)):
+        with pytest.raises(pkv.PkvError):
+            a.pool.price_request(1, B, Hq, n_q=n_q, max_blocks=mb)
+    q = torch.zeros(1, 1, 256 + P, dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros(1, (1 << 20) + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pkv.PkvError):
+        a.pool.paged_latent_attention(0, q[..., :256], q[..., 256:], wide, i32([40]), 1.0)
+
+
+@pytest.mark.parametrize("tok,head,ok", [(64, 64, False), (128, 64, False), (192, 64, True), (64, 192, True),
+                                         (64, 256, True), (200, 72, False), (208, 72, True), (1 << 62, 64, True)])
+def test_write_output_rows_do_not_overlap(tok, head, ok):
+    a = Case([40], R=256)
+    n, H = (1, 3) if tok > 1 << 40 else (3, 3)
+    span = ((n - 1) * tok if n > 1 else 0) + (H - 1) * head + P
+    out = torch.zeros(span, dtype=torch.bfloat16, device="cuda")
+    g = gen(5)
+    q, kv, tab = normal(g, n, H, P), normal(g, n, 256 + P), tables(8)
+    row, slot, pos = i32([int(a.table[0, 0])] * n), i32(list(range(n))), i32([3, 1, 2][:n])
+    st = a.pool._lib.pkv_write_latent(
+        a.pool._h, 0, n, row.data_ptr(), slot.data_ptr(), kv.data_ptr(), 256 + P, pos.data_ptr(), tab.data_ptr(), 8, None,
+        ctypes.c_float(0), 0, H, q.data_ptr(), H * P, P, out.data_ptr(), tok, head, pkv._stream(None))
+    assert st == (pkv.PKV_OK if ok else pkv.PKV_ERR_INVALID)
+    assert a.pool.check_errors() == 0
+    if ok:
+        got = torch.as_strided(out, (n, H, P), (tok if n > 1 else span, head, 1))
+        want = a.pool.write_latent(0, row, slot, kv, pos, tab, interleaved=False, q_rope=q)
+        assert torch.equal(got, want)
+    # in place with other strides than the input's
+    st = a.pool._lib.pkv_write_latent(
+        a.pool._h, 0, n, row.data_ptr(), slot.data_ptr(), kv.data_ptr(), 256 + P, pos.data_ptr(), tab.data_ptr(), 8, None,
+        ctypes.c_float(0), 0, H, q.data_ptr(), H * P, P, q.data_ptr(), H * 2 * P, 2 * P, pkv._stream(None))
+    assert st == pkv.PKV_ERR_INVALID
+
+
+def test_uneven_values_keep_the_documented_errors():
+    """128 tokens 2^-18 below the next 128's largest, whose others are as small: queries that see
+    only small values and queries that see the large ones too."""
+    L, H, R = 300, 2, 256
+    g = gen(11)
+    a = Case([L], R=R)
+    x = a.rows[:L].float()
+    x[:256, :R] *= 2.0 ** -18
+    x[200, :R] *= 2.0 ** 18
+    kv = x.bfloat16()
+    t = torch.arange(L, dtype=torch.int32, device="cuda")
+    still = torch.cat((torch.ones(1, P // 2, device="cuda"), torch.zeros(1, P // 2, device="cuda")), 1)
+    a.pool.write_latent(0, a.table[0][(t // 32).long()].contiguous(), t % 32, kv, torch.zeros_like(t), still)
+    q = normal(g, 1, L, H, DH + P)
+    q[..., :DH] = 0  # the logits hang on the position keys alone
+    wk, wv = ((normal(g, H, DH, R).float() / R ** 0.5).bfloat16() for _ in range(2))
+    out = a.pool.latent_prefill_attention(0, q, wk, wv, a.table, i32([L]), 0.1, max_ctx=L)
+    assert a.pool.check_errors() == 0
+    c, r, qr = kv[:, :R].double(), kv[:, R:].double(), q[0, :, :, DH:].double()
+    v = torch.einsum("tr,hdr->htd", c, wv.double())
+    v_mag = torch.einsum("tr,hdr->htd", c.abs(), wv.double().abs())
+    hidden = hidden_for(L, L)
+    s = (0.1 * torch.einsum("ihp,tp->hit", qr, r)).masked_fill(hidden, -math.inf)
+    p = s.softmax(-1)
+    want, mag = p @ v, p @ v.abs()
+    # besides the roundings of the other tests: P is off by 2^(k - 31) of the row's largest in
+    # tokens whose 128 have values 2^-k of the largest (k at most 19 for the first 128, as two
+    # maxima of scaled normal values are within a factor of two; 1 for the others), values by
+    # 2^-38 of the largest of their 128
+    part = torch.full((L,), 2.0 ** -30, dtype=torch.float64, device="cuda")
+    part[:128] = 2.0 ** (19 - 31)
+    p_abs = p.amax(-1, keepdim=True) * (((~hidden) * part).double()[None] @ v.abs())
+    v_abs = 2.0 ** -38 * v.abs().amax((1, 2), keepdim=True)
+    d = (P * 2.0 ** -23 * 0.1 * torch.einsum("ihp,tp->hit", qr.abs(), r.abs())).amax(-1, keepdim=True)
+    tol = U * want.abs() + (2 * H16 + 2 * d) * mag + p_abs + v_abs + R * 2.0 ** -23 * (p @ v_mag)
+    err = (out[0].permute(1, 0, 2).double() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
