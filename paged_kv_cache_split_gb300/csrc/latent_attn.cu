@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         mbar_arrive(&sm.p_full);
       }
       // Output of the segment: O^T / sum, or a record (reference, sum, O^T) to be merged.
+      softmax_any(false);  // a warp may still be rescaling O^T by sm.fac, raised in the last tile
 #pragma unroll
       for (int k = 0; k < N / 4; ++k) {
 #pragma unroll
