@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     for (int d = 16; d > 0; d >>= 1) top_exp = max(top_exp, __shfl_xor_sync(0xffffffffu, top_exp, d));
     float m = kNoMax;
     uint64_t l = 0;    // two partial sums
-    bool big = false;  // the warp has a reference beyond 2^24
+    bool big = false;  // the warp has a reference beyond 2^23
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
       const int lift = max(-110, __ldg(v_exp + j0 + j) - top_exp) + 7;  // this tile's power in P
@@ -528,12 +528,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
       const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale;
-      if (__any_sync(0xffffffffu, top > m + kSlack)) {
+      if (__any_sync(0xffffffffu, top - m > kSlack)) {
         const float mn = fmaxf(m, rintf(top));
         const float f = ex2(m - mn);
         m = mn;
         l = mul2(l, pair2(f, f));
-        big = __any_sync(0xffffffffu, fabsf(m) > 16777216.f && m > kNoMax);
+        big = __any_sync(0xffffffffu, fabsf(m) > 8388608.f && m > kNoMax);
         if (j > 0) {
           // the products of the tile before are complete: this S was issued after them
 #pragma unroll 1
@@ -547,15 +547,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
           }
         }
       }
-      // x scale - m in one rounding.  Beyond 2^24 the product's and the reference's roundings
-      // could differ by more than the exponential can take: there the product is rounded first.
-      float mul = P.scale;
+      // x scale + (lift - m) in one rounding.  Up to 2^23 lift - m is exact.  Beyond, it would be
+      // rounded by a power of two's worth and more, differently from tile to tile: there the
+      // product is rounded first, as the reference was, m is taken from it, and then lift added.
+      float mul = P.scale, ref = (float)lift - m;
       if (big) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] *= P.scale;
+        for (int c = 0; c < 128; ++c) x[c] = __fsub_rn(__fmul_rn(x[c], P.scale), m);
         mul = 1.f;
+        ref = (float)lift;
       }
-      const float ref = (float)lift - m;  // exact below 2^24, and the sum takes the same P
       const uint64_t sc = pair2(mul, mul), mm = pair2(ref, ref);
       uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll

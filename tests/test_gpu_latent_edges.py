@@ -3,9 +3,13 @@ and lowest logits, tiles of zero, uneven or non-finite values, memory that belon
 sequence, two tokens at one place, pricing at the calls' limits.
 
 References are the formulas in 64 bits, with the bounds derived in test_gpu_latent.py."""
+import math
+
+import numpy as np
 import pytest
 
-from test_gpu_latent import P, SCALE, Case, _needs_gpu, absorbed, check_absorbed, gen, normal  # noqa: F401
+from test_gpu_latent import (DH, H16, P, SCALE, U, Case, _needs_gpu, absorbed, check_absorbed, gen,
+                             normal)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -41,4 +45,51 @@ def test_absorbed_maximum_raised_in_every_last_tile(R, n_q, H):
         check_absorbed(case, out, q, SCALE)
         for _ in range(10):
             assert torch.equal(out, absorbed(case, q, SCALE))
+    assert case.pool.check_errors() == 0
+
+
+def picked_values(H, R=512):
+    """A value projection that takes the latent's first 128 values."""
+    w = torch.zeros(H, DH, R, dtype=torch.bfloat16, device="cuda")
+    w[:, torch.arange(DH), torch.arange(DH)] = 1
+    return w
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("k", [20, 23, 24, 25, 26, 27, 30, 100])
+def test_expanded_huge_logits_over_uneven_tiles(k, sign):
+    """Logits of 2^k or 2^k + step in log2 units, exact in fp32 (two products a logit, a scale
+    that becomes 1.0), over tiles whose values differ by powers of two.  The bound has no
+    term for the logits."""
+    L, n_q, H = 1280, 4, 2
+    step = max(8.0, 2.0 ** (k - 23))
+    case = Case([L], 512, seed=101)
+    rows = case.seq[0].clone()
+    tile = torch.arange(L, device="cuda") // 128
+    e = torch.tensor([0, -3, 2, -6, 1, 1, -1, 4, -2, 0], device="cuda")[tile]
+    up = torch.tensor([0, 1, 1, 0, 1, 0, 1, 1, 0, 1], device="cuda")[tile].double()
+    rows[:, :512] = (rows[:, :512].float() * 2.0 ** e[:, None]).bfloat16()
+    rows[:, 512:] = 0
+    half = min(60, k // 2)
+    rows[:, 512] = 2.0 ** half
+    rows[:, 513] = (up * step).bfloat16()
+    rewrite(case, 0, rows)
+    scale = float(np.float32(math.log(2)))
+    assert np.float32(scale * math.log2(math.e)) == 1.0
+    q = torch.zeros(1, n_q, H, DH + P, dtype=torch.bfloat16, device="cuda")
+    q[..., DH] = sign * 2.0 ** (k - half)
+    q[..., DH + 1] = 1
+    wv = picked_values(H)
+    v = rows[:, :DH].double()
+    for ctas in (1, 0):
+        case.pool.decode_set_ctas(ctas)
+        out = case.pool.latent_prefill_attention(0, q, torch.zeros_like(wv), wv, case.table, case.ctx, scale)
+        for i in range(n_q):
+            n = L - n_q + i + 1
+            p = torch.exp2((up[:n] - 1) * step)
+            p /= p.sum()
+            want, mag = p @ v[:n], p @ v[:n].abs()
+            tol = U * want.abs() + 2 * H16 * mag + 2.0 ** -24 * v.abs().max()
+            for h in range(H):
+                assert ((out[0, i, h].double() - want).abs() <= tol).all(), (i, h, ctas)
     assert case.pool.check_errors() == 0
