@@ -96,7 +96,7 @@ template <int N>
 __device__ __forceinline__ int32_t visible(const Params& P, int b, int rt, int32_t* len) {
   bool bad;
   const int32_t L =
-      latent_ctx(__ldg(P.a.ctx + b), (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
+      latent_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
   *len = L;
   if (L == 0) return 0;
   const int last = min(P.rows, (rt + 1) * N) - 1;

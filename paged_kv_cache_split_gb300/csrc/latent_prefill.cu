@@ -51,7 +51,7 @@ struct Params {
 
 __device__ __forceinline__ int32_t context(const Params& P, int b, bool* bad) {
   const int64_t all = (int64_t)P.a.max_blocks * kBlockTokens;
-  return latent_ctx(__ldg(P.a.ctx + b), all < P.a.max_ctx ? all : (int64_t)P.a.max_ctx, P.a.n_q, bad);
+  return latent_ctx(P.a.ctx[b], all < P.a.max_ctx ? all : (int64_t)P.a.max_ctx, P.a.n_q, bad);
 }
 
 // Block j of sequence b: its slab's tensor maps (null outside the pool) and its first row
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
     const int32_t* v_exp = P.v_exp + ((int64_t)b * P.a.Hq + h) * (P.T / kTile);
     int top_exp = -110;
-    for (int k = lane; k < all; k += 32) top_exp = max(top_exp, __ldg(v_exp + k));
+    for (int k = lane; k < all; k += 32) top_exp = max(top_exp, v_exp[k]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top_exp = max(top_exp, __shfl_xor_sync(0xffffffffu, top_exp, d));
     float m = kNoMax;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     bool big = false;  // the warp has a reference beyond 2^23
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
-      const int lift = max(-110, __ldg(v_exp + j0 + j) - top_exp) + 7;  // this tile's power in P
+      const int lift = max(-110, v_exp[j0 + j] - top_exp) + 7;  // this tile's power in P
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
       tc_fence_after();
       float x[128];

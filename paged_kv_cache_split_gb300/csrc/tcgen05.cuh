@@ -207,7 +207,9 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
 }
 
 // Launch with programmatic dependence on the stream's previous kernel (the kernels wait
-// for it before they touch global memory).  The shared-memory limit of a kernel is raised
+// for it before they touch global memory, and read that memory with ordinary loads: the
+// previous kernel may write it while they are resident, which a non-coherent load does not
+// allow).  The shared-memory limit of a kernel is raised
 // once per device.
 template <typename P>
 inline cudaError_t tc_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p,
