@@ -123,7 +123,9 @@ __device__ __forceinline__ void latent_copy_column(void* dst, const uint8_t* map
                                                    uint64_t policy) {
   latent_copy(dst, map + 128, c, y8, bar, policy);
 }
-// Both maps become visible to this thread's copies.
+// Both maps become visible to this thread's copies, and, past a __syncwarp, to those of the
+// lane that issues them: the fence then lies on the path from the maps' writing to the copy
+// (a shuffle of the address alone orders nothing).
 __device__ __forceinline__ void latent_maps_acquire(const uint8_t* map) {
   tensormap_acquire(map);
   tensormap_acquire(map + 128);

@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             atomicOr(err, ERR_ROW);
           }
         }
+        __syncwarp();  // the issuing lane's copies come after the lookups' acquires
         const int ue = min(ub + 16, k1);
         for (int u = ub; u < ue; ++u) {
           const int i = 2 * (u - ub);

@@ -55,7 +55,8 @@ __device__ __forceinline__ int32_t context(const Params& P, int b, bool* bad) {
 }
 
 // Block j of sequence b: its slab's tensor maps (null outside the pool) and its first row
-// there, in eights.
+// there, in eights.  The maps are acquired by the calling lane: a __syncwarp comes between
+// the calls and the copies.
 __device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int j, int* y8) {
   const int32_t row = P.a.bt[(int64_t)b * P.a.max_blocks + j];
   if (!latent_row_ok(P.a.lv, row)) {
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
         // lane l < 4 looks up block l of the tile
         const int j = it.tile * (kTile / kBlockTokens) + lane;
         map = lane < 4 && j * kBlockTokens < it.len ? block_map(P, it.b, j, &y0) : nullptr;
+        __syncwarp();
         bytes = __popc(__ballot_sync(0xffffffffu, map != nullptr)) * kBlockBytes;
         ++tiles;
       }
@@ -647,6 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
       const int blk = 4 * (j0 + jb) + lane;
       int y0 = 0;
       const uint8_t* map = blk < 4 * (j0 + nmax) && blk * kBlockTokens < L ? block_map(P, b, blk, &y0) : nullptr;
+      __syncwarp();
       const unsigned have = __ballot_sync(0xffffffffu, map != nullptr);
       const int je = min(jb + 8, nmax);
 #pragma unroll 1

@@ -8,8 +8,9 @@ import math
 import numpy as np
 import pytest
 
-from test_gpu_latent import (DH, H16, P, SCALE, U, Case, _needs_gpu, absorbed, check_absorbed, gen,
-                             normal)  # noqa: F401
+import paged_kv_cache_split_gb300 as pkv
+from test_gpu_latent import (DH, H16, P, SCALE, U, Case, _needs_gpu, absorbed, check, check_absorbed,
+                             expanded_ref, gen, i32, normal)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -93,3 +94,29 @@ def test_expanded_huge_logits_over_uneven_tiles(k, sign):
             for h in range(H):
                 assert ((out[0, i, h].double() - want).abs() <= tol).all(), (i, h, ctas)
     assert case.pool.check_errors() == 0
+
+
+def test_pools_that_follow_one_another_at_one_address():
+    """Slabs of two pools with other row widths at the same memory, their tensor maps at the
+    same addresses (20 blocks of 1152-byte rows, 36 of 640)."""
+    memory = torch.zeros(20 * 32 * 1152 + 4096, dtype=torch.uint8, device="cuda")
+    alloc = pkv.Allocator(pkv.ALLOC_FN(lambda ctx, n, stream: memory.data_ptr()),
+                          pkv.RELEASE_FN(lambda ctx, ptr, stream: None), None)
+    g = gen(123)
+    for turn in range(6):
+        R, blocks = ((512, 20), (256, 36))[turn % 2]
+        pool = pkv.Pool(1, 1, R, "latent", slab_blocks=blocks, max_slabs=1, allocator=alloc)
+        pool.reserve_rows(blocks)
+        L, H = 500, 4
+        case = Case.__new__(Case)
+        case.pool, case.R, case.W, case.layer, case.lens = pool, R, R + P, 0, [L]
+        case.table = torch.randperm(blocks, generator=g, device="cuda")[None, :16].int().contiguous()
+        case.ctx, case.seq = i32([L]), [None]
+        rewrite(case, 0, normal(g, L, R + P))
+        q = normal(g, 1, 1, H, R + P)
+        check_absorbed(case, absorbed(case, q, SCALE), q, SCALE)
+        qe, w = normal(g, 1, 3, H, DH + P), normal(g, H, DH, R) / 22
+        out = pool.latent_prefill_attention(0, qe, w, w, case.table, case.ctx, SCALE)
+        check(out[0], *expanded_ref(case, qe[0], w, w, 0, SCALE), f"turn {turn}")
+        assert pool.check_errors() == 0
+        pool.close()

@@ -31,3 +31,18 @@ def test_every_kernel_waits_before_it_reads():
             assert "griddepcontrol.wait" in body, name
             before = body[:body.index("griddepcontrol.wait")]
             assert not re.search(r"\b(P\.a|P|a)\.\w+\s*\[|\bstart_walk\b|\bcontext\(|\bvisible\b", before), name
+
+
+def test_acquired_maps_are_ordered_before_the_copies():
+    """Lanes look blocks up and acquire their slabs' tensor maps, an elected lane copies through
+    them: a warp barrier lies between every lookup and the copies after it."""
+    text = sources()
+    body = text["latent_attn.cu"]
+    calls = [m.start() for m in re.finditer(r"latent_maps_acquire\(map\);", body)]
+    assert len(calls) == 1
+    prefill = text["latent_prefill.cu"]
+    lookups = [m.start() for m in re.finditer(r"\? block_map\(", prefill)]
+    assert len(lookups) == 2
+    for src, at in [(body, calls[0])] + [(prefill, x) for x in lookups]:
+        rest = src[at:]
+        assert rest.index("__syncwarp();") < re.search(r"latent_copy_\w+\(", rest).start()
