@@ -298,7 +298,8 @@ pkv_status pkv_slab_address(const pkv_pool* pool, int layer, int kind, int slab,
  * A request fits a device budget of free bytes F when storage_bytes + fixed_bytes
  * plus the growth of the step's workspace over what the caller already holds is at
  * most F.  Errors: PKV_ERR_INVALID for NULL pointers, negative or zero sizes, Hq
- * not a multiple of n_kv_heads or B * n_q > 4096 with n_q > 1; PKV_ERR_RANGE when
+ * not a multiple of n_kv_heads or B * n_q > 4096 with n_q > 1 (latent pools have
+ * their own limits, given with their calls); PKV_ERR_RANGE when
  * the slabs to append would exceed max_slabs (the pool can never hold the request).
  *   [mlx-swift-lm #142, Summary: admission prices the growth of storage, the page
  *    and fixed costs and the step's guaranteed workspace each on its own; After:

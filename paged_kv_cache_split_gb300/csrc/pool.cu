@@ -922,8 +922,8 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
   if (!p || !r || !out || r->new_blocks < 0 || r->B < 1 || r->Hq < 1 || r->n_q < 1 || r->max_blocks < 0)
     return PKV_ERR_INVALID;
   if (r->Hq % p->cfg.n_kv_heads) return PKV_ERR_INVALID;
-  if (r->n_q > 1 && (int64_t)r->B * r->n_q > 4096) return PKV_ERR_INVALID;
   const bool latent = p->cfg.format == PKV_FMT_LATENT;
+  if (!latent && r->n_q > 1 && (int64_t)r->B * r->n_q > 4096) return PKV_ERR_INVALID;
   if (latent && (!latent_sizes_ok(r->B, r->n_q, r->Hq) || r->max_blocks > kLatentMaxBlocks)) return PKV_ERR_INVALID;
   const int64_t free_rows = (int64_t)p->free_rows.size();
   const int64_t deficit = r->new_blocks > free_rows ? r->new_blocks - free_rows : 0;

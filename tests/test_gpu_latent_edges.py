@@ -120,3 +120,11 @@ def test_pools_that_follow_one_another_at_one_address():
         check(out[0], *expanded_ref(case, qe[0], w, w, 0, SCALE), f"turn {turn}")
         assert pool.check_errors() == 0
         pool.close()
+
+
+def test_latent_requests_are_priced_under_the_calls_limits():
+    p = Case([40], 512, seed=117).pool
+    for B, n_q, H in ((1, 8192, 16), (64, 66, 1000), (4096, 1, 16), (4096, 2, 16)):
+        pr = p.price_request(3, B, H, n_q=n_q, max_blocks=256)
+        assert pr["workspace_bytes"] == p.latent_workspace_bytes(B, n_q, H)
+        assert pr["fixed_bytes"] == 256 * 4 + 4 + n_q * H * (576 + 512) * 2
