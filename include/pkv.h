@@ -414,9 +414,10 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  * Outputs and workspaces overlap no input, but for write_latent's q_out.
  * The pages describe no such format: the operators are written from the formulas
  * given with each call.  They require the pool's device to be the current one
- * (PKV_ERR_INVALID otherwise).  pkv_price_request prices a latent request's
- * workspace as pkv_latent_workspace_bytes, under that call's limits, and its q and
- * output rows as R + P and R values.
+ * (PKV_ERR_INVALID otherwise).  pkv_price_request prices a step in absorbed form: the
+ * workspace as pkv_latent_workspace_bytes, under that call's limits, and the q and
+ * output rows as R + P and R values.  pkv_price_latent_prefill prices one in expanded
+ * form, whose workspace is far larger.
  * --------------------------------------------------------------------------- */
 
 /* write_latent: token i's row goes to (rows_dev[i], slots_dev[i]) of `layer`:
@@ -484,6 +485,14 @@ pkv_status pkv_paged_latent_attention(pkv_pool* pool, int layer, int B, int n_q,
  * Host only; the limits are those of that call. */
 pkv_status pkv_latent_prefill_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq, int max_blocks,
                                               int max_ctx, size_t* bytes);
+
+/* pkv_price_request for a step in expanded form (a prompt or a long chunk) on a latent
+ * pool, with the same meaning of every field but these: workspace_bytes is
+ * pkv_latent_prefill_workspace_bytes of (B, n_q, Hq, max_blocks, max_ctx), and the q and
+ * output rows in fixed_bytes have 128 + P and 128 values.  Limits and errors are those of
+ * that query, B >= 1 and new_blocks >= 0 (PKV_ERR_INVALID), PKV_ERR_FORMAT on a pool of
+ * another format and PKV_ERR_RANGE as for pkv_price_request.  Host only. */
+pkv_status pkv_price_latent_prefill(const pkv_pool* pool, const pkv_request* req, int max_ctx, pkv_price* out);
 
 /* Expanded attention, for prompts and long chunks: every visible latent row becomes
  * per-head keys and values, then ordinary causal attention runs over them:

@@ -113,6 +113,7 @@ SIGNATURES = {
     "pkv_latent_workspace_bytes": ([_P, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "pkv_paged_latent_attention": ([_P, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
     "pkv_latent_prefill_workspace_bytes": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "pkv_price_latent_prefill": ([_P, ctypes.POINTER(Request), _I, ctypes.POINTER(Price)], _I),
     "pkv_latent_prefill_attention": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
     "pkv_status_string": ([_I], ctypes.c_char_p),
     "pkv_last_error": ([], ctypes.c_char_p),
@@ -617,6 +618,14 @@ class Pool:
         req = Request(int(new_blocks), int(B), int(Hq), int(n_q), int(max_blocks))
         out = Price()
         _check(self._lib.pkv_price_request(self._h, ctypes.byref(req), ctypes.byref(out)), "price_request")
+        return out.as_dict()
+
+    def price_latent_prefill(self, new_blocks: int, B: int, Hq: int, n_q: int, max_blocks: int, max_ctx: int = 0) -> dict:
+        """price_request for a step in expanded form (see pkv_price_latent_prefill)."""
+        req = Request(int(new_blocks), int(B), int(Hq), int(n_q), int(max_blocks))
+        out = Price()
+        _check(self._lib.pkv_price_latent_prefill(self._h, ctypes.byref(req), int(max_ctx), ctypes.byref(out)),
+               "price_latent_prefill")
         return out.as_dict()
 
     def check_identity(self, cfg: PoolConfig) -> bool:

@@ -918,13 +918,8 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   return PKV_OK;
 }
 
-pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price* out) {
-  if (!p || !r || !out || r->new_blocks < 0 || r->B < 1 || r->Hq < 1 || r->n_q < 1 || r->max_blocks < 0)
-    return PKV_ERR_INVALID;
-  if (r->Hq % p->cfg.n_kv_heads) return PKV_ERR_INVALID;
-  const bool latent = p->cfg.format == PKV_FMT_LATENT;
-  if (!latent && r->n_q > 1 && (int64_t)r->B * r->n_q > 4096) return PKV_ERR_INVALID;
-  if (latent && (!latent_sizes_ok(r->B, r->n_q, r->Hq) || r->max_blocks > kLatentMaxBlocks)) return PKV_ERR_INVALID;
+// What every price has in common: the storage growth and the pages of the new blocks.
+static pkv_status price_storage(const pkv_pool* p, const pkv_request* r, pkv_price* out) {
   const int64_t free_rows = (int64_t)p->free_rows.size();
   const int64_t deficit = r->new_blocks > free_rows ? r->new_blocks - free_rows : 0;
   const int64_t slabs = (deficit + p->cfg.slab_blocks - 1) / p->cfg.slab_blocks;
@@ -936,6 +931,18 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
   out->free_rows = free_rows;
   out->storage_bytes = (uint64_t)slabs * (uint64_t)p->group_bytes;
   out->page_bytes = (uint64_t)r->new_blocks * (uint64_t)block_bytes * (uint64_t)p->cfg.n_layers;
+  return PKV_OK;
+}
+
+pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price* out) {
+  if (!p || !r || !out || r->new_blocks < 0 || r->B < 1 || r->Hq < 1 || r->n_q < 1 || r->max_blocks < 0)
+    return PKV_ERR_INVALID;
+  if (r->Hq % p->cfg.n_kv_heads) return PKV_ERR_INVALID;
+  const bool latent = p->cfg.format == PKV_FMT_LATENT;
+  if (!latent && r->n_q > 1 && (int64_t)r->B * r->n_q > 4096) return PKV_ERR_INVALID;
+  if (latent && (!latent_sizes_ok(r->B, r->n_q, r->Hq) || r->max_blocks > kLatentMaxBlocks)) return PKV_ERR_INVALID;
+  const pkv_status st = price_storage(p, r, out);
+  if (st != PKV_OK) return st;
   const uint64_t q_out = 2ull * (uint64_t)p->cfg.head_dim + (latent ? kRope : 0);  // values of a q and an output row
   out->fixed_bytes = (uint64_t)r->max_blocks * 4u + 4u + (uint64_t)r->n_q * (uint64_t)r->Hq * q_out * 2u;
   if (latent) {
@@ -947,6 +954,18 @@ pkv_status pkv_price_request(const pkv_pool* p, const pkv_request* r, pkv_price*
     prefill_layout(p, r->B, r->n_q, r->Hq, r->max_blocks, &a, &b, &c, &t);
     out->workspace_bytes = t;
   }
+  return PKV_OK;
+}
+
+pkv_status pkv_price_latent_prefill(const pkv_pool* p, const pkv_request* r, int max_ctx, pkv_price* out) {
+  if (!p || !r || !out || r->new_blocks < 0 || r->B < 1) return PKV_ERR_INVALID;
+  size_t ws = 0;
+  pkv_status st = pkv_latent_prefill_workspace_bytes(p, r->B, r->n_q, r->Hq, r->max_blocks, max_ctx, &ws);
+  if (st == PKV_OK) st = price_storage(p, r, out);
+  if (st != PKV_OK) return st;
+  out->fixed_bytes = (uint64_t)r->max_blocks * 4u + 4u +
+                     (uint64_t)r->n_q * (uint64_t)r->Hq * (2ull * kLatentHead + kRope) * 2u;
+  out->workspace_bytes = ws;
   return PKV_OK;
 }
 

@@ -128,3 +128,34 @@ def test_latent_requests_are_priced_under_the_calls_limits():
         pr = p.price_request(3, B, H, n_q=n_q, max_blocks=256)
         assert pr["workspace_bytes"] == p.latent_workspace_bytes(B, n_q, H)
         assert pr["fixed_bytes"] == 256 * 4 + 4 + n_q * H * (576 + 512) * 2
+
+
+def test_pricing_of_the_expanded_form():
+    p = Case([40], 512, seed=125).pool
+    W = 512 + P
+    for B, n_q, H, mb, ctx in ((1, 8192, 16, 256, 0), (1, 8192, 16, 300, 8192), (4, 1000, 16, 128, 4096), (3, 1, 2, 40, 0)):
+        pr = p.price_latent_prefill(70, B, H, n_q, mb, max_ctx=ctx)
+        assert pr["workspace_bytes"] == p.latent_prefill_workspace_bytes(B, n_q, H, mb, ctx)
+        assert pr["workspace_bytes"] >= 2 * B * H * (ctx or 32 * mb) * DH * 2
+        assert pr["fixed_bytes"] == 4 * mb + 4 + n_q * H * (DH + P + DH) * 2
+        same = p.price_request(70, B, H, n_q=n_q, max_blocks=mb)
+        for k in ("slabs_to_append", "free_rows", "storage_bytes", "page_bytes"):
+            assert pr[k] == same[k]
+        assert pr["page_bytes"] == 70 * 32 * W * 2 and pr["slabs_to_append"] > 0
+    # the price covers the call
+    case = Case([300], 512, seed=127)
+    pr = case.pool.price_latent_prefill(0, 1, 2, 5, case.width)
+    g = gen(1)
+    ws = torch.empty(pr["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    w = normal(g, 2, DH, 512) / 22
+    case.pool.latent_prefill_attention(0, normal(g, 1, 5, 2, DH + P), w, w, case.table, case.ctx, SCALE, workspace=ws)
+    assert case.pool.check_errors() == 0
+    for bad in ((-1, 1, 1, 1, 1, 0), (1, 0, 1, 1, 1, 0), (1, 1, 0, 1, 1, 0), (1, 1, 1, 0, 1, 0), (1, 1, 1, 1, -1, 0),
+                (1, 1, 1, 1, 1, -1), (1, 4097, 1, 1, 1, 0), (1, 1, 1025, 1, 1, 0), (1, 1, 1, 1, (1 << 20) + 1, 0),
+                (1, 64, 1024, 1, 1 << 20, 0), (10 ** 8, 1, 1, 1, 1, 0)):
+        with pytest.raises(pkv.PkvError):
+            p.price_latent_prefill(*bad)
+    other = pkv.Pool(1, 1, 128, "bf16")
+    with pytest.raises(pkv.PkvError) as e:
+        other.price_latent_prefill(1, 1, 1, 1, 1)
+    assert e.value.status == pkv.PKV_ERR_FORMAT
