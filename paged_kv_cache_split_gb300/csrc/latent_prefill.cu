@@ -33,6 +33,11 @@ constexpr int kAtom = 1024;              // eight tokens of a column: the swizzl
 constexpr int kSmall = 3 * 1024;         // alignment (1024) and barriers
 constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3e38f;
+constexpr int kMaxExp = 110;             // value tiles' exponents lie within +-kMaxExp
+// The lowest power a tile's P is given, relative to the largest tile's.  At P <= 2^(7 + 8.5)
+// before it, fp16 keeps nothing of P (below 2^-25) at 2^-41 and lower: a tile further down adds
+// no value either way, while its P, as the sum takes it, is still far from FP32's lowest.
+constexpr int kLowest = -48;
 
 struct Params {
   LatentPrefillArgs a;
@@ -81,7 +86,8 @@ __device__ __forceinline__ const uint8_t* block_map(const Params& P, int b, int 
 // which the attention makes itself: both are fp16, whose three more bits halve the output's
 // error (relative L2 0.0028 -> 0.0022; the bf16 output alone has 0.0017).  Any magnitude
 // fits, as a tile's values are divided by the power of two that puts the largest in
-// [2^13, 2^14), and the attention puts the power back into the probabilities' exponent.
+// [2^13, 2^14), and the attention puts the power back into the probabilities' exponent.  A
+// tile without any value has the lowest exponent: it bears on no other tile's.
 // ---------------------------------------------------------------------------
 constexpr int kExpandThreads = 320;  // warps 0..3 store keys, 4..7 values; 8 copies, 9 MMAs
 constexpr int kWStages = 3;
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
         named_barrier_sync(1, 128);
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = fmaxf(mx, sm.v_max[n & 1][i]);
-        const int e = mx > 0.f ? max(-110, min(110, (int)(__float_as_uint(mx) >> 23) - 127 - 13)) : 0;
+        const int e = mx > 0.f ? max(-kMaxExp, min(kMaxExp, (int)(__float_as_uint(mx) >> 23) - 127 - 13)) : -kMaxExp;
         scale = pow2(-e);
         if (threadIdx.x == 128) P.v_exp[((int64_t)it.b * P.a.Hq + it.h) * (P.T / kTile) + it.tile] = e;
       }
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     const int vis = off + i + 1;
     const int vis_first = off + i0 + t * kTile + 1;  // of the tile's first query
     const int32_t* v_exp = P.v_exp + ((int64_t)b * P.a.Hq + h) * (P.T / kTile);
-    int top_exp = -110;
+    int top_exp = -kMaxExp;
     for (int k = lane; k < all; k += 32) top_exp = max(top_exp, v_exp[k]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top_exp = max(top_exp, __shfl_xor_sync(0xffffffffu, top_exp, d));
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
     bool big = false;  // the warp has a reference beyond 2^23
 #pragma unroll 1
     for (int j = 0; j < ntt; ++j) {
-      const int lift = max(-110, v_exp[j0 + j] - top_exp) + 7;  // this tile's power in P
+      const int lift = max(kLowest, v_exp[j0 + j] - top_exp) + 7;  // this tile's power in P
       wait_or_die(&sm.s_full[t], j & 1, dead, err);
       tc_fence_after();
       float x[128];

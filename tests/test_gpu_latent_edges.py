@@ -159,3 +159,42 @@ def test_pricing_of_the_expanded_form():
     with pytest.raises(pkv.PkvError) as e:
         other.price_latent_prefill(1, 1, 1, 1, 1)
     assert e.value.status == pkv.PKV_ERR_FORMAT
+
+
+@pytest.mark.parametrize("e", [0, -12, -40, -90])
+@pytest.mark.parametrize("ctas", [1, 0])
+def test_expanded_tile_of_zero_values(e, ctas):
+    """128 tokens without any value, beside values of 2^e."""
+    L, n_q, H = 900, 5, 2
+    case = Case([L], 512, seed=103)
+    case.pool.decode_set_ctas(ctas)
+    rows = case.seq[0].clone()
+    rows[128:256, :512] = 0
+    rewrite(case, 0, rows)
+    g = gen(104)
+    q = normal(g, 1, n_q, H, DH + P)
+    wk = normal(g, H, DH, 512) / 22
+    wv = (normal(g, H, DH, 512).float() / 22 * 2.0 ** e).bfloat16()
+    out = case.pool.latent_prefill_attention(0, q, wk, wv, case.table, case.ctx, SCALE)
+    check(out[0], *expanded_ref(case, q[0], wk, wv, 0, SCALE), f"values of 2^{e}")
+    assert case.pool.check_errors() == 0
+
+
+def test_expanded_many_zero_values_weigh_in_the_sum():
+    """One token with values and 400000 without, each with 2^-24.5 of its probability: together
+    they take 1.6% from the output, four times its rounding."""
+    L, H = 400001, 1
+    case = Case([L], 256, seed=129)
+    rows = torch.zeros(L, 256 + P, dtype=torch.bfloat16, device="cuda")
+    rows[0, :DH] = normal(gen(130), DH)
+    rows[1:, 256] = 1
+    rewrite(case, 0, rows)
+    q = torch.zeros(1, 1, H, DH + P, dtype=torch.bfloat16, device="cuda")
+    q[..., DH] = -24.5
+    wv = picked_values(H, 256)
+    want = rows[0, :DH].double() / (1 + (L - 1) * 2.0 ** -24.5)
+    for ctas in (1, 0):
+        case.pool.decode_set_ctas(ctas)
+        out = case.pool.latent_prefill_attention(0, q, torch.zeros_like(wv), wv, case.table, case.ctx, math.log(2))
+        assert ((out[0, 0, 0].double() - want).abs() <= (U + 2 * H16) * want.abs()).all()
+    assert case.pool.check_errors() == 0
