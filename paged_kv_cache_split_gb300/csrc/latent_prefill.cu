@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) latent_expand_kernel(const 
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(__uint_as_float(r[i])));
         }
-        if (t >= L) mx = 0.f;
+        // a row with an infinity stays one, as documented, but sets no exponent: the tiles
+        // beside it keep their bits (fmaxf passes NaN by)
+        if (t >= L || mx > 3.402823466e38f) mx = 0.f;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         if (lane == 0) sm.v_max[n & 1][warp & 3] = mx;

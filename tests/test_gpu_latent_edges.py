@@ -198,3 +198,25 @@ def test_expanded_many_zero_values_weigh_in_the_sum():
         out = case.pool.latent_prefill_attention(0, q, torch.zeros_like(wv), wv, case.table, case.ctx, math.log(2))
         assert ((out[0, 0, 0].double() - want).abs() <= (U + 2 * H16) * want.abs()).all()
     assert case.pool.check_errors() == 0
+
+
+@pytest.mark.parametrize("bits", [0x7F80, 0xFF80, 0x7FC0])
+def test_expanded_nonfinite_row_stays_in_its_tile(bits):
+    """A latent with an infinity or a NaN among tokens 128 to 255: the queries that see only the
+    first 128 tokens keep the formula's bounds."""
+    L = n_q = 256
+    H = 2
+    case = Case([L], 512, seed=105)
+    rows = case.seq[0].clone()
+    rows.view(torch.int16)[200, 77] = bits if bits < 0x8000 else bits - 0x10000
+    rewrite(case, 0, rows)
+    g = gen(106)
+    q = normal(g, 1, n_q, H, DH + P)
+    wk, wv = normal(g, H, DH, 512) / 22, normal(g, H, DH, 512) / 22
+    out = case.pool.latent_prefill_attention(0, q, wk, wv, case.table, case.ctx, SCALE)
+    assert not torch.isfinite(out[0, 200:]).all()
+
+    class Head:
+        seq, lens, R = [rows[:128]], [128], 512
+    check(out[0, :128], *expanded_ref(Head, q[0, :128], wk, wv, 0, SCALE), "queries of the first tile")
+    assert case.pool.check_errors() == 0
