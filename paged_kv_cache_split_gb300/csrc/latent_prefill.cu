@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_prefill_kernel(const _
         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
-      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale;
+      // Rows past the last query hold other sequences' queries and meet slots past the length:
+      // they must not move the references of this warp's other rows.
+      const float top = i < n_q ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * P.scale : -INFINITY;
       if (__any_sync(0xffffffffu, top - m > kSlack)) {
         const float mn = fmaxf(m, rintf(top));
         const float f = ex2(m - mn);

@@ -220,3 +220,25 @@ def test_expanded_nonfinite_row_stays_in_its_tile(bits):
         seq, lens, R = [rows[:128]], [128], 512
     check(out[0, :128], *expanded_ref(Head, q[0, :128], wk, wv, 0, SCALE), "queries of the first tile")
     assert case.pool.check_errors() == 0
+
+
+def test_expanded_results_do_not_hang_on_bytes_outside_the_sequence():
+    """Bit-identical whatever the slots past the lengths and the queries of unused slots hold."""
+    n_q, H = 3, 16
+    lens = [417, 0] * 16
+    g = gen(107)
+    q = normal(g, 32, n_q, H, DH + P)
+    wk, wv = normal(g, H, DH, 512) / 22, normal(g, H, DH, 512) / 22
+    ref = None
+    for ctas in (1, 0):
+        ref = None
+        for stale in (0x0000, 0x7F7F, 0x7FC0, 0x7F80):
+            for junk in (0.0, 1000.0, float("inf"), float("nan")):
+                case = Case(lens, 512, seed=109, stale=stale)
+                case.pool.decode_set_ctas(ctas)
+                qj = q.clone()
+                qj[1::2] = junk
+                out = case.pool.latent_prefill_attention(0, qj, wk, wv, case.table, case.ctx, SCALE)
+                if ref is None:
+                    ref = out
+                assert torch.equal(out, ref), (ctas, hex(stale), junk, int((out != ref).sum()))
