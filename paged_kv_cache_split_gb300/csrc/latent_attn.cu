@@ -281,8 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       }
       const int vis_first = seg.len - P.a.n_q + row0 / P.a.Hq + 1;
       softmax_any(false);  // sm.vis is ready
+      // A tile's rows past the sequence's are other sequences' queries: with a reference that
+      // no logit passes they never move the others' (their own columns hold anything).
 #pragma unroll
-      for (int k = 0; k < N / 4; ++k) m[k] = kNoMax, l[k] = 0.f;
+      for (int k = 0; k < N / 4; ++k) m[k] = 8 * (k >> 1) + c2 + (k & 1) < nrow ? kNoMax : INFINITY, l[k] = 0.f;
 
       for (int u = seg.k0; u < seg.k1; ++u, ++it) {
         const int buf = it & 1;

@@ -242,3 +242,21 @@ def test_expanded_results_do_not_hang_on_bytes_outside_the_sequence():
                 if ref is None:
                     ref = out
                 assert torch.equal(out, ref), (ctas, hex(stale), junk, int((out != ref).sum()))
+
+
+@pytest.mark.parametrize("n_q,H", [(1, 5), (1, 20), (3, 7), (1, 65)])
+def test_absorbed_results_do_not_hang_on_unused_queries(n_q, H):
+    """Bit-identical whatever the queries of unused batch slots hold, head counts that leave
+    a row tile partly empty."""
+    case = Case([417, 0] * 16, 512, seed=111)
+    q = normal(gen(112), 32, n_q, H, 576)
+    for ctas in (1, 0):
+        case.pool.decode_set_ctas(ctas)
+        ref = None
+        for junk in (0.0, 1000.0, float("inf"), float("nan")):
+            qj = q.clone()
+            qj[1::2] = junk
+            out = absorbed(case, qj, SCALE)
+            if ref is None:
+                ref = out
+            assert torch.equal(out, ref), (ctas, junk, int((out != ref).sum()))
