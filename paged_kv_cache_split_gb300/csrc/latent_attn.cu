@@ -50,7 +50,7 @@ constexpr int kChunkBytes = kTile * 128;               // 64 tokens x 64 values
 constexpr int kQuadBytes = kLatentQuad * kChunkBytes;  // 64 tokens x 256 values: [8 x 8 tokens][4][8][128 bytes]
 constexpr int kAtom = 1024;                            // eight tokens of a column: the swizzle's atom
 constexpr float kSlack = 8.0f;        // log2 of how far a logit may pass the reference
-constexpr float kNoMax = -3e38f;      // the reference before any visible token
+constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
 constexpr int kSmemLimit = 232448;    // 227 KB opt-in shared memory per block
 constexpr int kSmall = 3 * 1024;      // alignment (1024), barriers and per-row values
 constexpr int kInFlight = 8;          // more tiles than the rings hold

@@ -32,7 +32,7 @@ constexpr int kBlockBytes = kBlockTokens * 128;  // one column of a block
 constexpr int kAtom = 1024;              // eight tokens of a column: the swizzle's atom
 constexpr int kSmall = 3 * 1024;         // alignment (1024) and barriers
 constexpr float kSlack = 8.0f;           // log2 of how far a logit may pass the reference
-constexpr float kNoMax = -3e38f;
+constexpr float kNoMax = -3.402823466e38f;  // no logit is below it
 constexpr int kMaxExp = 110;             // value tiles' exponents lie within +-kMaxExp
 // The lowest power a tile's P is given, relative to the largest tile's.  At P <= 2^(7 + 8.5)
 // before it, fp16 keeps nothing of P (below 2^-25) at 2^-41 and lower: a tile further down adds

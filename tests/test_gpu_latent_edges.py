@@ -260,3 +260,26 @@ def test_absorbed_results_do_not_hang_on_unused_queries(n_q, H):
             if ref is None:
                 ref = out
             assert torch.equal(out, ref), (ctas, junk, int((out != ref).sum()))
+
+
+@pytest.mark.parametrize("ctas", [1, 0])
+def test_logits_at_the_lowest_of_fp32(ctas):
+    """Every logit the same, within 5% of the lowest finite value in log2 units."""
+    L, H, x = 700, 4, -2.25e38
+    case = Case([L], 512, seed=113)
+    rows = case.seq[0].clone()
+    rows[:, 512:] = 0
+    rows[:, 512] = 2.0 ** 60
+    rewrite(case, 0, rows)
+    case.pool.decode_set_ctas(ctas)
+    q = torch.zeros(1, 1, H, 576, dtype=torch.bfloat16, device="cuda")
+    q[..., 512] = x / 2.0 ** 60
+    assert -3.4e38 < float(q[0, 0, 0, 512]) * 2.0 ** 60 * math.log2(math.e) < -3e38
+    want, mag = rows[:, :512].double().mean(0), rows[:, :512].double().abs().mean(0)
+    out = absorbed(case, q, 1.0)
+    assert ((out[0, 0].double() - want).abs() <= U * want.abs() + U * mag).all()
+    qe = torch.zeros(1, 1, H, DH + P, dtype=torch.bfloat16, device="cuda")
+    qe[..., DH] = x / 2.0 ** 60
+    wv = picked_values(H)
+    out = case.pool.latent_prefill_attention(0, qe, torch.zeros_like(wv), wv, case.table, case.ctx, 1.0)
+    assert ((out[0, 0].double() - want[:DH]).abs() <= U * want[:DH].abs() + 2 * H16 * mag[:DH] + 2.0 ** -24 * 8).all()
