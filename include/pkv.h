@@ -470,9 +470,10 @@ pkv_status pkv_latent_workspace_bytes(const pkv_pool* pool, int B, int n_q, int 
  * gives zero rows; a block-table row outside the pool sets bit 1 (the sequence's
  * result is then undefined).  Slots past a sequence's length are never read into the
  * result, whatever they hold.  max_ctx is accepted for interface stability.
- * Probabilities enter the second product in bf16; sums and softmax state are fp32.
+ * Probabilities enter the second product in bf16; sums and softmax state are fp32, and
+ * the logits times log2(e) are expected to be finite in fp32.
  * Deterministic.  Limits: B <= 4096, Hq <= 1024, B * n_q * Hq <= 2^24, max_blocks <=
- * 2^20, scale finite, pointers 16-byte aligned.  B = 0 returns PKV_OK.  Asynchronous. */
+ * 2^20, |scale| log2(e) finite in fp32, pointers 16-byte aligned.  B = 0 returns PKV_OK.  Asynchronous. */
 pkv_status pkv_paged_latent_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_latent,
                                       int64_t q_latent_stride, const void* q_rope, int64_t q_rope_stride,
                                       const int32_t* block_table_dev, int max_blocks, const int32_t* ctx_lens_dev,

@@ -15,6 +15,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -744,6 +745,14 @@ static pkv_status latent_check(const pkv_pool* p, int layer) {
   return PKV_OK;
 }
 
+// scale log2(e), as the kernels take it; false where fp32 does not hold it.
+static bool latent_scale(float scale, float* out) {
+  const double s = (double)scale * 1.4426950408889634;
+  if (!(std::fabs(s) <= (double)FLT_MAX)) return false;
+  *out = (float)s;
+  return true;
+}
+
 static bool misaligned(const void* ptr, uintptr_t a) { return ((uintptr_t)ptr & (a - 1)) != 0; }
 
 pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, const int32_t* slots, const void* kv,
@@ -827,7 +836,9 @@ pkv_status pkv_paged_latent_attention(pkv_pool* p, int layer, int B, int n_q, in
   pkv_status st = latent_check(p, layer);
   if (st != PKV_OK) return st;
   const int R = p->cfg.head_dim;
-  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || !std::isfinite(scale))
+  float scale_log2;
+  if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks ||
+      !latent_scale(scale, &scale_log2))
     return PKV_ERR_INVALID;
   if (B == 0) return PKV_OK;
   if (!q_latent || !q_rope || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
@@ -850,7 +861,7 @@ pkv_status pkv_paged_latent_attention(pkv_pool* p, int layer, int B, int n_q, in
   a.qr_stride = q_rope_stride;
   a.bt = bt;
   a.ctx = ctx;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.out = (uint16_t*)out;
   a.ws = ws;
   a.stream = (cudaStream_t)stream;
@@ -885,8 +896,9 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
                                         int max_ctx, float scale, void* out, void* ws, size_t ws_bytes, void* stream) {
   pkv_status st = latent_check(p, layer);
   if (st != PKV_OK) return st;
+  float scale_log2;
   if (!latent_sizes_ok(B, n_q, Hq) || max_blocks < 0 || max_blocks > kLatentMaxBlocks || max_ctx < 0 ||
-      !std::isfinite(scale))
+      !latent_scale(scale, &scale_log2))
     return PKV_ERR_INVALID;
   if (B == 0) return PKV_OK;
   if (!q || !w_k || !w_v || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
@@ -908,7 +920,7 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   a.wv = (const uint16_t*)w_v;
   a.bt = bt;
   a.ctx = ctx;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.out = (uint16_t*)out;
   a.ws = ws;
   a.device = p->device;

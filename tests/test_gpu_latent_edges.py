@@ -283,3 +283,13 @@ def test_logits_at_the_lowest_of_fp32(ctas):
     wv = picked_values(H)
     out = case.pool.latent_prefill_attention(0, qe, torch.zeros_like(wv), wv, case.table, case.ctx, 1.0)
     assert ((out[0, 0].double() - want[:DH]).abs() <= U * want[:DH].abs() + 2 * H16 * mag[:DH] + 2.0 ** -24 * 8).all()
+
+
+def test_scales_beyond_fp32_in_powers_of_two_are_refused():
+    case = Case([40], 512, seed=115)
+    q, w = normal(gen(1), 1, 1, 4, 576), torch.zeros(4, DH, 512, dtype=torch.bfloat16, device="cuda")
+    for scale in (3e38, -3e38, 2.4e38):
+        with pytest.raises(pkv.PkvError):
+            absorbed(case, q, scale)
+        with pytest.raises(pkv.PkvError):
+            case.pool.latent_prefill_attention(0, q[..., :192].contiguous(), w, w, case.table, case.ctx, scale)
