@@ -437,10 +437,11 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  * aligned; strides in values, non-negative multiples of 8, kv_stride >= R + P; rows of
  * q_out that do not overlap (a token's heads together, or a head's tokens together);
  * 0 <= Hq <= 1024, n_tokens * (1 + ceil(Hq / 32)) < 2^31 (else PKV_ERR_INVALID).  Two
- * tokens with the same (row, slot) leave either one's values.  A row, slot or position out
- * of range sets the device error word (bit 1, 4 or 16): the row is then not written
- * and, for a bad position, neither are the token's q_out rows.  n_tokens 0 returns
- * PKV_OK.  Asynchronous. */
+ * tokens with the same (row, slot) leave a mix of their values there: each 16-byte piece
+ * of the row is one token's or the other's.  A row, slot or position out of range sets
+ * the device error word (bit 1, 4 or 16): the row is then not written and, for a bad
+ * position, neither are the token's q_out rows.  n_tokens 0 returns PKV_OK.
+ * Asynchronous. */
 pkv_status pkv_write_latent(pkv_pool* pool, int layer, int n_tokens, const int32_t* rows_dev,
                             const int32_t* slots_dev, const void* kv_bf16, int64_t kv_stride,
                             const int32_t* positions_dev, const float* cos_sin, int n_positions,

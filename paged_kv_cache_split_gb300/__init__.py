@@ -471,7 +471,8 @@ class Pool:
         normalised (with norm_weight), the position key turned by the angles of positions[i];
         q_rope [n, Hq, P] is turned by the same angles into q_out (which may be q_rope; a new
         tensor by default).  kv may have any row stride, q_rope and q_out any token and head
-        strides, in multiples of 8 values.  Returns q_out (None without q_rope)."""
+        strides, in multiples of 8 values.  Tokens of one call have places of their own: two at
+        one place leave a mix of both.  Returns q_out (None without q_rope)."""
         torch = _torch()
         R, P = self._latent()
         bf16, i32 = torch.bfloat16, torch.int32

@@ -10,7 +10,7 @@ import pytest
 
 import paged_kv_cache_split_gb300 as pkv
 from test_gpu_latent import (DH, H16, P, SCALE, U, Case, _needs_gpu, absorbed, check, check_absorbed,
-                             expanded_ref, gen, i32, normal)  # noqa: F401
+                             expanded_ref, gen, i32, normal, pool_rows)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -293,3 +293,21 @@ def test_scales_beyond_fp32_in_powers_of_two_are_refused():
             absorbed(case, q, scale)
         with pytest.raises(pkv.PkvError):
             case.pool.latent_prefill_attention(0, q[..., :192].contiguous(), w, w, case.table, case.ctx, scale)
+
+
+@pytest.mark.parametrize("R", [256, 512])
+def test_write_of_one_place_twice(R):
+    """64 tokens at one place: each 16-byte piece of the row is one token's, and nothing else
+    of the pool changes."""
+    case = Case([64], R, seed=121)
+    before = pool_rows(case.pool, 4, R + P).clone()
+    n = 64
+    kv = normal(gen(122), n, R + P)
+    row = int(case.table[0, 1])
+    case.pool.write_latent(0, i32([row] * n), i32([7] * n), kv, i32([0] * n), still())
+    after = pool_rows(case.pool, 4, R + P)
+    got = after[row, 7].view(torch.int16).view(-1, 8)
+    want = kv.view(torch.int16).view(n, -1, 8)
+    assert ((want == got).all(-1)).any(0).all()
+    after[row, 7] = before[row, 7]
+    assert torch.equal(after.view(torch.int16), before.view(torch.int16))
