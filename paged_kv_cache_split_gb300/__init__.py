@@ -542,7 +542,7 @@ class Pool:
             key = (B, n_q, Hq)
             need = self._ws_bytes.get(key)
             if need is None:
-                need = self._ws_bytes[key] = self.latent_workspace_bytes(B, n_q, Hq)
+                need = self._keep_size(key, self.latent_workspace_bytes(B, n_q, Hq))
             workspace = self._own(need, torch.uint8, q_latent.device, stream)
         st = self._lib.pkv_paged_latent_attention(
             self._h, layer, B, n_q, Hq, ql, _row_stride(q_latent, "q_latent"), qr, _row_stride(q_rope, "q_rope"),
@@ -578,7 +578,7 @@ class Pool:
             key = (B, n_q, Hq, mb, int(max_ctx))
             need = self._ws_bytes.get(key)
             if need is None:
-                need = self._ws_bytes[key] = self.latent_prefill_workspace_bytes(*key)
+                need = self._keep_size(key, self.latent_prefill_workspace_bytes(*key))
             workspace = self._own(need, torch.uint8, q.device, stream)
         _check(self._lib.pkv_latent_prefill_attention(
             self._h, layer, B, n_q, Hq, _dev(q, torch.bfloat16, "q", (B, n_q, Hq, D + P)),
@@ -587,6 +587,14 @@ class Pool:
             int(max_ctx), float(scale), _dev(out, torch.bfloat16, "out", (B, n_q, Hq, D)),
             _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "latent_prefill_attention")
         return out
+
+    def _keep_size(self, key, nbytes: int) -> int:
+        """Sizes are kept for the next call with the same arguments: 1024 at most, as
+        batches and bounds of a long-running server differ from step to step."""
+        if len(self._ws_bytes) >= 1024:
+            self._ws_bytes = {}
+        self._ws_bytes[key] = nbytes
+        return nbytes
 
     @staticmethod
     def _own(shape, dtype, device, stream):

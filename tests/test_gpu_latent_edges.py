@@ -311,3 +311,14 @@ def test_write_of_one_place_twice(R):
     assert ((want == got).all(-1)).any(0).all()
     after[row, 7] = before[row, 7]
     assert torch.equal(after.view(torch.int16), before.view(torch.int16))
+
+
+def test_workspace_sizes_kept_are_bounded():
+    case = Case([40], 256, seed=119)
+    q, w = normal(gen(1), 1, 1, 1, DH + P), torch.zeros(1, DH, 256, dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros(1, 64, dtype=torch.int32, device="cuda")
+    wide[0, :2] = case.table[0, :2]
+    for m in range(40, 2048):
+        case.pool.latent_prefill_attention(0, q, w, w, wide, case.ctx, SCALE, max_ctx=m)
+    assert len(case.pool._ws_bytes) <= 1024
+    assert case.pool.check_errors() == 0
