@@ -27,10 +27,10 @@
 // CTA per row tile in a group).  A sequence inside one CTA's share is written directly; a
 // split one leaves FP32 records that a second kernel merges in order.
 //
-// Measured (one GB300, both kernels, back to back): 16 x 16384 tokens, 32 heads 59.7 us,
-// 5.08 TB/s (the card copies at 6.79; DRAM reads equal the rows' bytes); 64 sequences of up
-// to 8192, 16 heads 55 us, 4.91 TB/s; 16 x 8192 with 16 / 32 / 64 / 128 heads 34 / 37 / 42 /
-// 67 us; 1 x 1000, 16 heads 8.7 us.  Up to 32 rows a CTA streams at 6 TB/s x 1/152 and the
+// Measured (one GB300, both kernels, in a captured graph): 16 x 16384 tokens, 32 heads 59.5 us,
+// 5.10 TB/s (the card copies at 6.79; DRAM reads equal the rows' bytes); 64 sequences of up
+// to 8192, 16 heads 55 us, 4.93 TB/s; 16 x 8192 with 16 / 32 / 64 / 128 heads 34 / 36 / 42 /
+// 67 us; 1 x 1000, 16 heads 8.9 us.  Up to 32 rows a CTA streams at 6 TB/s x 1/152 and the
 // rest is the start (5 us: lengths, block table, slab address, first rows) and the end
 // (records, merge: 6 us).  With 64 rows a tile the ring holds two tiles only and a copy's
 // latency shows (1.7 us a tile); 128 heads also read every row twice, the second time from L2.

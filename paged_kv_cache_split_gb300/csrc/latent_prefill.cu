@@ -7,12 +7,12 @@
 // Both kernels are bound by the tensor cores: the expansion takes 512 R operations per
 // token and head, the attention 640 per (query, key, head).
 //
-// Measured (one GB300, both kernels): a prompt of 8192 with 16 heads 271 us, 1394 TFLOP/s
-// (cuBLAS reaches 1888 in a burst); of 4096 with 32 heads 164 us; 1000 new tokens behind
-// four contexts of up to 4096, 16 heads 107 us; 100 tokens, 4 heads 16 us.  The attention runs
-// its tensor cores 65% of the time: a step of two tiles takes 3590 cycles of 2560, S with
+// Measured (one GB300, both kernels, in a captured graph): a prompt of 8192 with 16 heads
+// 273 us, 1383 TFLOP/s (cuBLAS reaches 1888 in a burst); of 4096 with 32 heads 165 us; 1000
+// new tokens behind four contexts of up to 4096, 16 heads 108 us; 100 tokens, 4 heads 16.5 us.  The attention runs
+// its tensor cores 63 to 65% of the time: a step of two tiles takes 3590 cycles of 2560, S with
 // both operands in shared memory (128 bytes a cycle, its whole bandwidth) 88 cycles an MMA
-// instead of 64.  The expansion, 37 us of the 271, runs them 46%: three stages in the ring
+// instead of 64.  The expansion, 37 us of the 273, runs them 43 to 46%: three stages in the ring
 // do not cover the copies' latency (2400 cycles under load), its start and end take 10 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -14,8 +14,10 @@
 // 16-byte loads per lane in flight before the first is used.
 //
 // Measured (one GB300): 16384 tokens with 128 heads 84.3 us, 6.87 TB/s of input and output
-// bytes (the card copies at 6.79); 4999 tokens with 16 heads 10.0 us, 3.3 TB/s, bound by
-// latency (one wave of warps, and table rows gathered from 33 MB); 8 tokens 1.9 us.
+// bytes (the card copies at 6.79); 4999 tokens with 16 heads, turned by halves, 10.1 us, 3.3
+// TB/s, bound by latency: 79 registers (61 interleaved) leave 24 warps to an SM, nearly
+// three waves of 9998, half of a query warp's loads are off with 16 heads, and the table's
+// rows are gathered from 33 MB; 8 tokens 1.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
