@@ -275,6 +275,7 @@ class Pool:
         self._ws = {}
         self._ws_bytes = {}  # workspace sizes of the latent calls by their arguments
         self._latent_dims = (head_dim, int(group_size)) if self.format == "latent" else None
+        self._device = _torch().cuda.current_device()
         s = self.stats()
         self.row_bytes = s["row_bytes"][: s["n_kinds"]]
 
@@ -465,6 +466,12 @@ class Pool:
             raise PkvError(PKV_ERR_FORMAT, f"a {self.format} pool has no latent rows")
         return self._latent_dims
 
+    def _same_device(self, *tensors):
+        """The kernels run on the pool's device and reach no other's memory."""
+        for t in tensors:
+            if t is not None and t.get_device() != self._device:
+                raise ValueError(f"a tensor on {t.device}, the pool is on cuda:{self._device}")
+
     def write_latent(self, layer: int, rows, slots, kv, positions, cos_sin, norm_weight=None, eps: float = 1e-6,
                      interleaved: bool = True, q_rope=None, q_out=None, stream=None):
         """Store token i's row kv[i] = (latent, position key) at (rows[i], slots[i]): the latent
@@ -497,6 +504,7 @@ class Pool:
                 qh, oh = q_rope.stride(1), q_out.stride(1)
         elif q_out is not None:
             raise ValueError("q_out without q_rope")
+        self._same_device(rows, slots, kv, positions, cos_sin, norm_weight, q_rope, q_out)
         n_pos = cos_sin.shape[0]
         st = self._lib.pkv_write_latent(
             self._h, layer, n, _dev(rows, i32, "rows", one), _dev(slots, i32, "slots", one), kvp,
@@ -533,6 +541,7 @@ class Pool:
         qr = _dev_strided(q_rope, bf16, "q_rope", lead + (P,))
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError("block_table must be [B, max_blocks]")
+        self._same_device(q_latent, q_rope, block_table, ctx_lens, out, workspace)
         if out is None:
             out = self._own(rows, bf16, q_latent.device, stream)
             o = out.data_ptr()
@@ -572,6 +581,7 @@ class Pool:
         if block_table.dim() != 2 or block_table.shape[0] != B:
             raise ValueError("block_table must be [B, max_blocks]")
         mb = int(block_table.shape[1])
+        self._same_device(q, w_k, w_v, block_table, ctx_lens, out, workspace)
         if out is None:
             out = self._own((B, n_q, Hq, D), torch.bfloat16, q.device, stream)
         if workspace is None:

@@ -322,3 +322,16 @@ def test_workspace_sizes_kept_are_bounded():
         case.pool.latent_prefill_attention(0, q, w, w, wide, case.ctx, SCALE, max_ctx=m)
     assert len(case.pool._ws_bytes) <= 1024
     assert case.pool.check_errors() == 0
+
+
+def test_tensors_of_another_device_are_refused():
+    """(The pool's device is moved instead of the tensors: one device is enough.)"""
+    case = Case([40], 256, seed=131)
+    q, w = normal(gen(1), 1, 1, 2, 256 + P), torch.zeros(2, DH, 256, dtype=torch.bfloat16, device="cuda")
+    case.pool._device += 1
+    with pytest.raises(ValueError, match="the pool is on"):
+        absorbed(case, q, SCALE)
+    with pytest.raises(ValueError, match="the pool is on"):
+        case.pool.latent_prefill_attention(0, q[..., :DH + P].contiguous(), w, w, case.table, case.ctx, SCALE)
+    with pytest.raises(ValueError, match="the pool is on"):
+        case.pool.write_latent(0, i32([0]), i32([0]), q[0, 0, :1], i32([0]), still())
