@@ -410,7 +410,8 @@ pkv_status pkv_import_blocks(pkv_pool* pool, const pkv_pool_config* identity, in
  * return PKV_ERR_FORMAT on a latent pool, and the calls below do so on any other.
  * Stored rows and queries are expected to be finite: a row that holds a NaN or an
  * infinity reaches the outputs of every query it shares a tile with, those that do not
- * see it included (rows past a sequence's length are no such rows).
+ * see it included (rows past a sequence's length are no such rows, and the queries of an
+ * unused batch slot may hold anything).
  * Outputs and workspaces overlap no input, but for write_latent's q_out, and a
  * workspace belongs to one call at a time (two streams or graphs take one each).
  * The pages describe no such format: the operators are written from the formulas
