@@ -524,9 +524,111 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* pool, int layer, int B, int n_
                                         int max_blocks, const int32_t* ctx_lens_dev, int max_ctx, float scale,
                                         void* out_bf16, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Drafted tokens on the per-head pools (bf16 and packed): a step that verifies a tree of
+ * drafted tokens writes their keys and values, attends with the tree's mask, and moves
+ * the accepted ones into place.  pkv_write_rotated serves prompts and single tokens as
+ * well.
+ *
+ * The n_q drafted tokens of a sequence are its last ones: ctx_lens counts them, and drafted
+ * token j lies at position ctx_lens[b] - n_q + j of the block table.  A sequence with fewer
+ * drafts than the batch's n_q still has n_q places; the unused ones are named by no mask.
+ * Outputs and workspaces overlap no input, but for write_rotated's q_out, and a workspace
+ * belongs to one call at a time (two streams or graphs take one each).  These calls require
+ * the pool's device to be the current one (PKV_ERR_INVALID otherwise).  The pages describe
+ * none of them: they are written from the formulas given here.
+ * --------------------------------------------------------------------------- */
+
+/* write_rotated: token i's keys and values go to (rows_dev[i], slots_dev[i]) of `layer`:
+ *   x' = x * rsqrt(mean(x^2) + eps) * w     (w = k_norm or q_norm; x' = x if it is NULL)
+ *   the pairs (a, b) of the first rotary_dim values of x' become
+ *   (a cos t - b sin t, a sin t + b cos t)
+ * for x each of the token's keys and, with Hq > 0, its queries, which go to q_out; values are
+ * stored as they are.  Pair j is (2j, 2j + 1) when `interleaved`, else (j, j + rotary_dim/2);
+ * its angle's cosine and sine are cos_sin[positions_dev[i]][j] and [rotary_dim/2 + j].
+ *   k_bf16, v_bf16: [n_tokens, n_kv_heads, head_dim], head h of token i at i * token_stride +
+ *                  h * head_stride (views of one projection's output, for instance)
+ *   positions_dev: [n_tokens] int32, each in [0, n_positions)
+ *   cos_sin:       [n_positions, rotary_dim] float32, on the device
+ *   k_norm, q_norm: [head_dim] bf16, or NULL
+ *   q_bf16, q_out: [n_tokens, Hq, head_dim], strided likewise; q_out may be q_bf16 with the
+ *                  same strides (in place)
+ * Arithmetic in fp32, one rounding to bf16 per value of a bf16 pool and of q_out; keys of a
+ * packed pool are not rounded before they are quantised (as pkv_write_block says, but for the
+ * scale, which is (max-min) times the rounded 1/(2^bits-1): an ulp apart at most; the turned
+ * key and its Hadamard transform carry about 40 bits).  Pointers 16-byte aligned;
+ * strides in values, non-negative multiples of 8; rows of q_out that do not overlap (a
+ * token's heads together, or a head's tokens together); rotary_dim a multiple of 32 in
+ * [32, head_dim]; 0 <= Hq <= 1024, n_tokens * (2 n_kv_heads + Hq) < 2^31 (else
+ * PKV_ERR_INVALID).  Two tokens with the same (row, slot) leave a mix of their values there.
+ * A row, slot or position out of range sets the device error word (bit 1, 4 or 16): nothing of
+ * the token is then stored and, for a bad position, its q_out rows are not written either.
+ * PKV_ERR_FORMAT on a latent pool (pkv_write_latent).  n_tokens 0 returns PKV_OK.
+ * Asynchronous. */
+pkv_status pkv_write_rotated(pkv_pool* pool, int layer, int n_tokens, const int32_t* rows_dev,
+                             const int32_t* slots_dev, const void* k_bf16, int64_t k_token_stride,
+                             int64_t k_head_stride, const void* v_bf16, int64_t v_token_stride,
+                             int64_t v_head_stride, const int32_t* positions_dev, const float* cos_sin,
+                             int n_positions, int rotary_dim, int interleaved, const void* k_norm,
+                             const void* q_norm, float eps, int Hq, const void* q_bf16, int64_t q_token_stride,
+                             int64_t q_head_stride, void* q_out, int64_t out_token_stride,
+                             int64_t out_head_stride, void* stream);
+
+/* Workspace bytes of pkv_paged_tree_attention for batches of B sequences with n_q queries of
+ * Hq heads each (split-K partials; no initialisation needed).  Host only; the limits are
+ * those of that call. */
+pkv_status pkv_tree_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq, size_t* bytes);
+
+/* Attention of the n_q drafted tokens of each sequence, arranged as a tree (or in any other
+ * way that a mask says):
+ *   out[b,i,h] = sum_t softmax_t(scale * q[b,i,h] . k_t) v_t
+ * over the tokens t < ctx_lens[b] - n_q, all of them, and the drafted tokens j for which bit
+ * j % 32 of word j / 32 of query i's mask row is set (its own bit too, if it is to see itself).
+ * A row that sees nothing gives zeros.
+ *   q_bf16:      [B, n_q, Hq, head_dim] (packed formats rotate it into K's basis internally)
+ *   tree_mask:   uint32 [n_q, ceil(n_q / 32)] a sequence, mask_stride words apart; 0: one
+ *                tree for the batch.  Bits from n_q on are not read.
+ *   block_table_dev: [B, max_blocks] int32 rows; ctx_lens_dev: [B] int32
+ *   out_bf16:    [B, n_q, Hq, head_dim]
+ *   workspace:   256-byte aligned, ws_bytes >= pkv_tree_workspace_bytes
+ * A length of 0 (an unused batch slot) gives zero rows.  A negative length, one beyond
+ * max_blocks * 32 or one in (0, n_q) sets the device error word (bit 2) and gives zero rows; a
+ * block-table row outside the pool sets bit 1 (the sequence's result is then undefined).
+ * Slots past a sequence's length, and drafted tokens that no query of the sequence sees, are
+ * never read into a result, whatever they hold; a drafted token whose value holds a NaN or an
+ * infinity may reach queries that do not see it, once one does.  max_ctx is accepted for
+ * interface stability.  Probabilities enter the second product in 16 bits; sums and softmax
+ * state are fp32.  Deterministic.  Limits: B <= 4096, n_q <= 1024, Hq <= 1024 and a multiple of
+ * n_kv_heads, B * n_q * Hq <= 2^24, max_blocks <= 2^20, |scale| log2(e) finite in fp32, pointers
+ * 16-byte aligned.  PKV_ERR_FORMAT on a latent pool.  B = 0 returns PKV_OK.  Asynchronous. */
+pkv_status pkv_paged_tree_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_bf16,
+                                    const uint32_t* tree_mask, int64_t mask_stride,
+                                    const int32_t* block_table_dev, int max_blocks, const int32_t* ctx_lens_dev,
+                                    int max_ctx, float scale, void* out_bf16, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* accept_drafts: the accepted path of each sequence's tree moves behind the tokens before
+ * it.  With first = ctx_lens[b] - n_q, the token at position first + path[b][k] goes to
+ * position first + k, for k < path_lens[b], in every layer and stored tensor (bit for bit), and
+ * new_lens[b] = first + path_lens[b], the length to go on with.  Places from there up to
+ * ctx_lens[b] keep what they held, or hold copies of moved tokens.
+ *   path_dev:  [B, max_path] int32, rising along a row, each in [0, n_q); path_lens_dev: [B]
+ *              int32 in [0, min(max_path, n_q)]
+ *   new_lens_dev: [B] int32, or NULL; must not overlap ctx_lens or path_lens
+ * Any format, latent pools included.  The blocks that hold a sequence's drafted tokens belong
+ * to it alone.  Lengths as for pkv_paged_tree_attention (a bad one sets bit 2, nothing moves and
+ * the new length is 0); a path that does not rise, an entry or a length out of range sets bit
+ * 32, nothing of the sequence moves and its new length is `first`; a block-table row outside
+ * the pool sets bit 1 and the token is not moved.  Limits: B <= 4096, n_q <= 1024, max_blocks <=
+ * 2^20.  Asynchronous. */
+pkv_status pkv_accept_drafts(pkv_pool* pool, int B, int n_q, int max_path, const int32_t* path_dev,
+                             const int32_t* path_lens_dev, const int32_t* block_table_dev, int max_blocks,
+                             const int32_t* ctx_lens_dev, int32_t* new_lens_dev, void* stream);
+
 /* Synchronise `stream`, read and clear the device error word.  PKV_ERR_DEVICE if it
  * was set (bits: 1 row out of range, 2 context too long, 4 slot out of range,
- * 8 wait limit reached, 16 rotary position out of range); *word_out (optional) receives the bits.  The kernels record
+ * 8 wait limit reached, 16 rotary position out of range, 32 accepted path out of range or
+ * not rising); *word_out (optional) receives the bits.  The kernels record
  * errors on the device instead of returning them, so that a decode step needs no
  * host synchronisation; the caller checks when it chooses.
  *   [mlxcel #2171, Implementation Notes: a decode step adds no host sync] */

@@ -27,7 +27,7 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "allocation failed", -3: "CUDA er
           -4: "format mismatch", -5: "out of range", -6: "device error word set"}
 PKV_OK, PKV_ERR_INVALID, PKV_ERR_OOM, PKV_ERR_CUDA, PKV_ERR_FORMAT, PKV_ERR_RANGE, PKV_ERR_DEVICE = \
     0, -1, -2, -3, -4, -5, -6
-ERR_ROW, ERR_CTX, ERR_SLOT, ERR_TIMEOUT, ERR_POS = 1, 2, 4, 8, 16
+ERR_ROW, ERR_CTX, ERR_SLOT, ERR_TIMEOUT, ERR_POS, ERR_PATH = 1, 2, 4, 8, 16, 32
 LATENT_HEAD = 128  # values of a head's expanded key (without its position part) and value
 
 
@@ -115,6 +115,11 @@ SIGNATURES = {
     "pkv_latent_prefill_workspace_bytes": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "pkv_price_latent_prefill": ([_P, ctypes.POINTER(Request), _I, ctypes.POINTER(Price)], _I),
     "pkv_latent_prefill_attention": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
+    "pkv_write_rotated": ([_P, _I, _I, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I, _I, _I, _P, _P, _F, _I, _P,
+                           _I64, _I64, _P, _I64, _I64, _P], _I),
+    "pkv_tree_workspace_bytes": ([_P, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "pkv_paged_tree_attention": ([_P, _I, _I, _I, _I, _P, _P, _I64, _P, _I, _P, _I, _F, _P, _P, _SZ, _P], _I),
+    "pkv_accept_drafts": ([_P, _I, _I, _I, _P, _P, _P, _I, _P, _P, _P], _I),
     "pkv_status_string": ([_I], ctypes.c_char_p),
     "pkv_last_error": ([], ctypes.c_char_p),
 }
@@ -239,6 +244,31 @@ def slab_runs(rows, slab_blocks: int = 32) -> np.ndarray:
     if n < 0:
         raise PkvError(PKV_ERR_INVALID, "slab_runs")
     return out[:n].copy()
+
+
+def tree_masks(parents):
+    """Mask words and depths of trees given by parents (host): parents [..., n_q] holds each
+    drafted token's parent, an earlier token of the tree, or a negative number for one that
+    follows the context.  Returns (masks [..., n_q, ceil(n_q / 32)] int32, depths [..., n_q]
+    int32): a token's mask names its ancestors and itself, and its position is that of the
+    first drafted token plus its depth."""
+    p = np.asarray(parents)
+    if p.ndim < 1 or not np.issubdtype(p.dtype, np.integer):
+        raise TypeError("parents must be integers, [..., n_q]")
+    n = p.shape[-1]
+    if n and (p >= np.arange(n)).any():
+        raise ValueError("a token's parent comes before it")
+    flat = p.reshape(int(np.prod(p.shape[:-1], dtype=np.int64)), n)
+    masks = np.zeros((flat.shape[0], n, -(-n // 32)), np.uint32)
+    depths = np.zeros(flat.shape, np.int32)
+    every = np.arange(flat.shape[0])
+    for i in range(n):
+        up = flat[:, i]
+        has = up >= 0
+        masks[has, i] = masks[every[has], up[has]]
+        depths[has, i] = depths[every[has], up[has]] + 1
+        masks[:, i, i // 32] |= np.uint32(1 << i % 32)
+    return masks.view(np.int32).reshape(*p.shape, masks.shape[-1]), depths.reshape(p.shape)
 
 
 def make_config(n_layers: int, n_kv_heads: int, head_dim: int, format="bf16", hadamard_seed: int = 0,
@@ -597,6 +627,114 @@ class Pool:
             int(max_ctx), float(scale), _dev(out, torch.bfloat16, "out", (B, n_q, Hq, D)),
             _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "latent_prefill_attention")
         return out
+
+    # -- drafted tokens --------------------------------------------------------
+    def write_rotated(self, layer: int, rows, slots, k, v, positions, cos_sin, q=None, k_norm=None, q_norm=None,
+                      eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
+        """Store token i's keys k[i], normalised (with k_norm) and turned by the angles of
+        positions[i], and its values v[i] at (rows[i], slots[i]); a packed pool quantises them.  The
+        queries q [n, Hq, D] are normalised (q_norm) and turned likewise into q_out (which may be
+        q; a new tensor by default).  cos_sin is [positions, rotary_dim]: the first rotary_dim
+        values of a head are turned.  k, v, q and q_out may have any token and head strides, in
+        multiples of 8 values.  Returns q_out (None without q)."""
+        torch = _torch()
+        bf16, i32 = torch.bfloat16, torch.int32
+        n, Hk, D = rows.numel(), self.n_kv_heads, self.head_dim
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [positions, rotary_dim]")
+        one, kv = (n,), (n, Hk, D)
+        kp, vp = _dev_strided(k, bf16, "k", kv), _dev_strided(v, bf16, "v", kv)
+        # a dimension of one entry is never stepped over: its stride says nothing
+        kt, kh, vt, vh = (x.stride(d) if x.shape[d] > 1 else 0 for x in (k, v) for d in (0, 1))
+        Hq, qp, op = 0, None, None
+        qt = qh = ot = oh = 0
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [n, Hq, head_dim]")
+            Hq = q.shape[1]
+            shape = (n, Hq, D)
+            if q_out is None:
+                q_out = self._own(shape, bf16, q.device, stream)
+            qp, op = _dev_strided(q, bf16, "q", shape), _dev_strided(q_out, bf16, "q_out", shape)
+            qt, qh, ot, oh = (x.stride(d) if x.shape[d] > 1 else 0 for x in (q, q_out) for d in (0, 1))
+        elif q_out is not None or q_norm is not None:
+            raise ValueError("q_out or q_norm without q")
+        self._same_device(rows, slots, k, v, positions, cos_sin, q, k_norm, q_norm, q_out)
+        n_pos, rot = cos_sin.shape
+        st = self._lib.pkv_write_rotated(
+            self._h, layer, n, _dev(rows, i32, "rows", one), _dev(slots, i32, "slots", one), kp, kt, kh, vp, vt, vh,
+            _dev(positions, i32, "positions", one), _dev(cos_sin, torch.float32, "cos_sin"), n_pos, rot,
+            1 if interleaved else 0, None if k_norm is None else _dev(k_norm, bf16, "k_norm", (D,)),
+            None if q_norm is None else _dev(q_norm, bf16, "q_norm", (D,)), float(eps), Hq, qp, qt, qh, op, ot, oh,
+            _stream(stream))
+        if st:
+            _check(st, "write_rotated")
+        return q_out
+
+    def tree_workspace_bytes(self, B: int, n_q: int, Hq: int) -> int:
+        n = _SZ()
+        _check(self._lib.pkv_tree_workspace_bytes(self._h, B, n_q, Hq, ctypes.byref(n)), "tree_workspace_bytes")
+        return int(n.value)
+
+    def paged_tree_attention(self, layer: int, q, tree_mask, block_table, ctx_lens, scale: float, max_ctx: int = 0,
+                             out=None, workspace=None, stream=None):
+        """Attention of each sequence's last n_q tokens, drafted as a tree: q [B, n_q, Hq, D];
+        tree_mask int32 [B, n_q, ceil(n_q / 32)], or [n_q, ceil(n_q / 32)] for one tree in all
+        sequences (tree_masks makes them from parents).  Query i sees every token before the
+        drafted ones and drafted token j where bit j of its mask row is set.  Returns out, shaped
+        as q."""
+        torch = _torch()
+        bf16, i32 = torch.bfloat16, torch.int32
+        if q.dim() != 4:
+            raise ValueError("q must be [B, n_q, Hq, head_dim]")
+        B, n_q, Hq, D = q.shape
+        if D != self.head_dim:
+            raise ValueError(f"q head_dim {D} != pool head_dim {self.head_dim}")
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [B, max_blocks]")
+        words = -(-n_q // 32)
+        shared = tree_mask.dim() == 2
+        maskp = _dev(tree_mask, i32, "tree_mask", (n_q, words) if shared else (B, n_q, words))
+        qp = _dev(q, bf16, "q")
+        self._same_device(q, tree_mask, block_table, ctx_lens, out, workspace)
+        if out is None:
+            out = self._own(q.shape, bf16, q.device, stream)
+            o = out.data_ptr()
+        else:
+            o = _dev(out, bf16, "out", q.shape)
+        if workspace is None:
+            key = ("tree", B, n_q, Hq)
+            need = self._ws_bytes.get(key)
+            if need is None:
+                need = self._keep_size(key, self.tree_workspace_bytes(B, n_q, Hq))
+            workspace = self._own(need, torch.uint8, q.device, stream)
+        st = self._lib.pkv_paged_tree_attention(
+            self._h, layer, B, n_q, Hq, qp, maskp, 0 if shared else n_q * words,
+            _dev(block_table, i32, "block_table"), block_table.shape[1], _dev(ctx_lens, i32, "ctx_lens", (B,)),
+            int(max_ctx), float(scale), o, _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+        if st:
+            _check(st, "paged_tree_attention")
+        return out
+
+    def accept_drafts(self, path, path_lens, block_table, ctx_lens, n_q: int, new_lens=None, stream=None):
+        """Move the drafted tokens of each sequence's accepted path, path[b, :path_lens[b]] (rising
+        indices of its n_q drafted tokens), to the places behind the tokens before them, in
+        every layer.  Returns the new lengths [B] int32 (new_lens, or a new tensor)."""
+        torch = _torch()
+        i32 = torch.int32
+        B = path_lens.numel()
+        if path.dim() != 2 or path.shape[0] != B:
+            raise ValueError("path must be [B, max_path]")
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError("block_table must be [B, max_blocks]")
+        self._same_device(path, path_lens, block_table, ctx_lens, new_lens)
+        if new_lens is None:
+            new_lens = self._own((B,), i32, ctx_lens.device, stream)
+        _check(self._lib.pkv_accept_drafts(
+            self._h, B, int(n_q), path.shape[1], _dev(path, i32, "path"), _dev(path_lens, i32, "path_lens", (B,)),
+            _dev(block_table, i32, "block_table"), block_table.shape[1], _dev(ctx_lens, i32, "ctx_lens", (B,)),
+            _dev(new_lens, i32, "new_lens", (B,)), _stream(stream)), "accept_drafts")
+        return new_lens
 
     def _keep_size(self, key, nbytes: int) -> int:
         """Sizes are kept for the next call with the same arguments: 1024 at most, as

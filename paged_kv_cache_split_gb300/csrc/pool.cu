@@ -23,6 +23,7 @@
 #include <string>
 #include <vector>
 
+#include "drafts.cuh"
 #include "latent.cuh"
 #include "pkv_internal.cuh"
 
@@ -755,6 +756,19 @@ static bool latent_scale(float scale, float* out) {
 
 static bool misaligned(const void* ptr, uintptr_t a) { return ((uintptr_t)ptr & (a - 1)) != 0; }
 
+// Whether output rows of `width` values, Hq a token, do not overlap one another: a token's
+// heads lie within its span, or a head's tokens within the head's.
+static bool rows_disjoint(int n, int Hq, int64_t token_stride, int64_t head_stride, int width) {
+  const int64_t t = n > 1 ? token_stride : 0, h = Hq > 1 ? head_stride : 0;
+  if ((n > 1 && t < width) || (Hq > 1 && h < width)) return false;
+  if (n > 1 && Hq > 1) {
+    // (n - 1) t + width <= h, without the product's overflow
+    const bool tokens_inside = t <= (h - width) / (n - 1), heads_inside = h <= (t - width) / (Hq - 1);
+    if (!tokens_inside && !heads_inside) return false;
+  }
+  return true;
+}
+
 pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, const int32_t* slots, const void* kv,
                             int64_t kv_stride, const int32_t* positions, const float* cos_sin, int n_positions,
                             const void* norm_weight, float eps, int interleaved, int Hq, const void* q_rope,
@@ -776,15 +790,8 @@ pkv_status pkv_write_latent(pkv_pool* p, int layer, int n, const int32_t* rows, 
     if (!q_rope || !q_out) return PKV_ERR_INVALID;
     for (int64_t x : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
       if (x < 0 || x % 8) return PKV_ERR_INVALID;
-    // Output rows must not overlap one another: heads within a token's span, or tokens within
-    // a head's.
+    if (!rows_disjoint(n, Hq, out_token_stride, out_head_stride, kRope)) return PKV_ERR_INVALID;
     const int64_t t = n > 1 ? out_token_stride : 0, h = Hq > 1 ? out_head_stride : 0;
-    if ((n > 1 && t < kRope) || (Hq > 1 && h < kRope)) return PKV_ERR_INVALID;
-    if (n > 1 && Hq > 1) {
-      // (n - 1) t + kRope <= h, without the product's overflow
-      const bool tokens_inside = t <= (h - kRope) / (n - 1), heads_inside = h <= (t - kRope) / (Hq - 1);
-      if (!tokens_inside && !heads_inside) return PKV_ERR_INVALID;
-    }
     // in place, a row's output is its own input
     if (q_out == q_rope && ((n > 1 && t != q_token_stride) || (Hq > 1 && h != q_head_stride))) return PKV_ERR_INVALID;
   }
@@ -926,6 +933,176 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* p, int layer, int B, int n_q, 
   a.device = p->device;
   a.stream = (cudaStream_t)stream;
   PKV_CUDA(launch_latent_prefill(a), "latent_prefill_attention launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Drafted tokens on the per-head pools
+// ---------------------------------------------------------------------------
+
+// What the entry points of this part check first: the layer, and the pool's device as the
+// current one (the kernels launch there).
+static pkv_status draft_check(const pkv_pool* p, int layer) {
+  if (!p || layer < 0 || layer >= p->cfg.n_layers) return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  int dev = -1;
+  PKV_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev != p->device) return PKV_ERR_INVALID;
+  return PKV_OK;
+}
+
+pkv_status pkv_write_rotated(pkv_pool* p, int layer, int n, const int32_t* rows, const int32_t* slots, const void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                             int64_t v_head_stride, const int32_t* positions, const float* cos_sin, int n_positions,
+                             int rotary_dim, int interleaved, const void* k_norm, const void* q_norm, float eps, int Hq,
+                             const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                             int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  pkv_status st = draft_check(p, layer);
+  if (st != PKV_OK) return st;
+  const int D = p->cfg.head_dim;
+  if (n < 0 || Hq < 0 || Hq > kDraftMaxHeads || n_positions < 0) return PKV_ERR_INVALID;
+  if ((int64_t)n * rotated_write_units(p->cfg.n_kv_heads, Hq) >= (int64_t)1 << 31) return PKV_ERR_INVALID;
+  if (rotary_dim < 32 || rotary_dim > D || rotary_dim % 32) return PKV_ERR_INVALID;
+  if (n == 0) return PKV_OK;
+  if (!rows || !slots || !k || !v || !positions || !cos_sin) return PKV_ERR_INVALID;
+  for (const void* x : {k, v, (const void*)cos_sin, k_norm, q_norm, q, (const void*)q_out})
+    if (misaligned(x, 16)) return PKV_ERR_INVALID;
+  for (int64_t x : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+    if (x < 0 || x % 8) return PKV_ERR_INVALID;
+  if ((k_norm || q_norm) && !(std::isfinite(eps) && eps >= 0.f)) return PKV_ERR_INVALID;
+  if (Hq > 0) {
+    if (!q || !q_out) return PKV_ERR_INVALID;
+    for (int64_t x : {q_token_stride, q_head_stride, out_token_stride, out_head_stride})
+      if (x < 0 || x % 8) return PKV_ERR_INVALID;
+    if (!rows_disjoint(n, Hq, out_token_stride, out_head_stride, D)) return PKV_ERR_INVALID;
+    // in place, a row's output is its own input
+    if (q_out == q && ((n > 1 && out_token_stride != q_token_stride) || (Hq > 1 && out_head_stride != q_head_stride)))
+      return PKV_ERR_INVALID;
+  }
+  RotatedWriteArgs a;
+  a.lv = layer_view(p, layer);
+  a.fmt = p->cfg.format;
+  a.D = D;
+  a.group = p->cfg.group_size;
+  a.n = n;
+  a.rows = rows;
+  a.slots = slots;
+  a.k = (const uint16_t*)k;
+  a.k_tok = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v = (const uint16_t*)v;
+  a.v_tok = v_token_stride;
+  a.v_head = v_head_stride;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.n_pos = n_positions;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.k_norm = (const uint16_t*)k_norm;
+  a.q_norm = Hq > 0 ? (const uint16_t*)q_norm : nullptr;
+  a.eps = eps;
+  a.Hq = Hq;
+  a.q = (const uint16_t*)q;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.qo = (uint16_t*)q_out;
+  a.o_tok = out_token_stride;
+  a.o_head = out_head_stride;
+  a.signs = p->signs_dev;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_rotated_write(a), "write_rotated launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
+static bool tree_sizes_ok(const pkv_pool* p, int B, int n_q, int Hq) {
+  return B >= 0 && B <= kDraftMaxBatch && n_q >= 1 && n_q <= kDraftMaxQueries && Hq >= 1 && Hq <= kDraftMaxHeads &&
+         Hq % p->cfg.n_kv_heads == 0 && (int64_t)B * n_q * Hq <= kDraftMaxRows;
+}
+
+pkv_status pkv_tree_workspace_bytes(const pkv_pool* p, int B, int n_q, int Hq, size_t* bytes) {
+  if (!p || !bytes) return PKV_ERR_INVALID;
+  if (p->cfg.format == PKV_FMT_LATENT) return PKV_ERR_FORMAT;
+  if (!tree_sizes_ok(p, B, n_q, Hq)) return PKV_ERR_INVALID;
+  *bytes = tree_attn_workspace(p->cfg.head_dim, p->cfg.n_kv_heads, B, n_q, Hq, decode_grid(p));
+  return PKV_OK;
+}
+
+pkv_status pkv_paged_tree_attention(pkv_pool* p, int layer, int B, int n_q, int Hq, const void* q, const uint32_t* mask,
+                                    int64_t mask_stride, const int32_t* bt, int max_blocks, const int32_t* ctx,
+                                    int max_ctx, float scale, void* out, void* ws, size_t ws_bytes, void* stream) {
+  (void)max_ctx;
+  pkv_status st = draft_check(p, layer);
+  if (st != PKV_OK) return st;
+  float scale_log2;
+  if (!tree_sizes_ok(p, B, n_q, Hq) || max_blocks < 0 || max_blocks > kDraftMaxBlocks || !latent_scale(scale, &scale_log2))
+    return PKV_ERR_INVALID;
+  if (B == 0) return PKV_OK;
+  if (!q || !mask || (!bt && max_blocks > 0) || !ctx || !out || !ws) return PKV_ERR_INVALID;
+  if (mask_stride != 0 && mask_stride < (int64_t)n_q * ((n_q + 31) / 32)) return PKV_ERR_INVALID;
+  if (misaligned(q, 16) || misaligned(out, 16) || misaligned(mask, 4) || misaligned(ws, 256)) return PKV_ERR_INVALID;
+  TreeAttnArgs a;
+  a.fmt = p->cfg.format;
+  a.D = p->cfg.head_dim;
+  a.group = p->cfg.group_size;
+  a.ctas = decode_grid(p);
+  if (ws_bytes < tree_attn_workspace(a.D, p->cfg.n_kv_heads, B, n_q, Hq, a.ctas)) return PKV_ERR_INVALID;
+  a.lv = layer_view(p, layer);
+  a.B = B;
+  a.n_q = n_q;
+  a.Hq = Hq;
+  a.max_blocks = max_blocks;
+  a.q = (const uint16_t*)q;
+  a.mask = mask;
+  a.mask_stride = mask_stride;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.scale_log2 = scale_log2;
+  a.signs = p->signs_dev;
+  a.out = (uint16_t*)out;
+  a.ws = ws;
+  a.device = p->device;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_tree_attn(a), "paged_tree_attention launch");
+  p->last_stream = a.stream;
+  return PKV_OK;
+}
+
+pkv_status pkv_accept_drafts(pkv_pool* p, int B, int n_q, int max_path, const int32_t* path, const int32_t* path_lens,
+                             const int32_t* bt, int max_blocks, const int32_t* ctx, int32_t* new_lens, void* stream) {
+  if (!p || B < 0 || B > kDraftMaxBatch || n_q < 1 || n_q > kDraftMaxQueries || max_path < 0 || max_blocks < 0 ||
+      max_blocks > kDraftMaxBlocks)
+    return PKV_ERR_INVALID;
+  const int64_t ctas = (int64_t)B * p->cfg.n_layers * p->n_kinds;
+  if (ctas >= (int64_t)1 << 31) return PKV_ERR_INVALID;
+  int dev = -1;
+  PKV_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev != p->device) return PKV_ERR_INVALID;
+  if (B == 0) return PKV_OK;
+  if ((!path && max_path > 0) || !path_lens || (!bt && max_blocks > 0) || !ctx) return PKV_ERR_INVALID;
+  // the lengths are read while the new ones are written
+  if (new_lens && new_lens < ctx + B && ctx < new_lens + B) return PKV_ERR_INVALID;
+  if (new_lens && new_lens < path_lens + B && path_lens < new_lens + B) return PKV_ERR_INVALID;
+  AcceptArgs a;
+  a.table = p->table_dev;
+  a.n_layers = p->cfg.n_layers;
+  a.n_kinds = p->n_kinds;
+  for (int k = 0; k < 4; ++k) a.token_bytes[k] = p->row_bytes[k] * p->cfg.n_kv_heads;
+  a.slab_blocks = p->cfg.slab_blocks;
+  a.rows_capacity = (int64_t)p->groups.size() * p->cfg.slab_blocks;
+  a.B = B;
+  a.n_q = n_q;
+  a.max_path = max_path;
+  a.max_blocks = max_blocks;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.bt = bt;
+  a.ctx = ctx;
+  a.new_lens = new_lens;
+  a.err = p->err_dev;
+  a.stream = (cudaStream_t)stream;
+  PKV_CUDA(launch_accept(a), "accept_drafts launch");
   p->last_stream = a.stream;
   return PKV_OK;
 }

@@ -1,0 +1,427 @@
+// rotated_write.cu — write_rotated: normalise, turn and store the keys of new tokens with
+// their values, and turn the query heads by the same angles.
+//
+//   x' = x * rsqrt(mean(x^2) + eps) * w                    (skipped without a weight)
+//   (y_a, y_b) = (x'_a cos t - x'_b sin t, x'_a sin t + x'_b cos t)
+//
+// over the pairs (2j, 2j+1) or (j, j + rot/2) of a head's first `rot` values, t the j-th
+// angle of the token's position, read from a table.  Sums and products are FP32; queries
+// and the keys of a bf16 pool are rounded to bf16 once.
+//
+// Packed pools quantise on the way, without a rounding before: the key goes into the
+// Hadamard basis as it was turned.  Codes hang on the sums' last bits where a value lies
+// near a border, so the turned value is kept as an unevaluated sum of two FP32 (products
+// and sums with their exact remainders) and the butterflies run on two parts: the leading
+// 16 bits relative to the row's largest value, whose sums FP32 holds exactly, and the
+// rest.  That carries 40 bits relative to the largest value at twice the FP32 additions;
+// FP64 (2 lanes a cycle and SM) would take thirty times as long.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "drafts.cuh"
+#include "latent.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kLoads = 8;  // 16-byte loads a lane has in flight
+
+struct Params {
+  RotatedWriteArgs a;
+  int per_token;       // warps a token (rows of heads: keys, queries, values)
+  int64_t pack_units;  // packed: warps that quantise keys (and as many values), before the queries' warps
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  bf16x2_to_f32(v.x, x[0], x[1]);
+  bf16x2_to_f32(v.y, x[2], x[3]);
+  bf16x2_to_f32(v.z, x[4], x[5]);
+  bf16x2_to_f32(v.w, x[6], x[7]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(bf2(x[0], x[1]), bf2(x[2], x[3]), bf2(x[4], x[5]), bf2(x[6], x[7]));
+}
+
+__device__ __forceinline__ bool place_ok(const LayerView& lv, int32_t row, int32_t slot) {
+  return draft_row_ok(lv, row) && slot >= 0 && slot < kBlockTokens;
+}
+__device__ __forceinline__ void flag(const LayerView& lv, bool pos_ok, int32_t row) {
+  atomicOr(lv.err, !pos_ok ? (int32_t)ERR_POS : draft_row_ok(lv, row) ? ERR_SLOT : ERR_ROW);
+}
+
+// The angles of one lane's eight values (chunk c of the D / 8 that hold a head).
+template <bool IL>
+struct Angles {
+  float c[IL ? 4 : 8], s[IL ? 4 : 8];
+  __device__ __forceinline__ void load(const float* tab, int chunk, int rot) {
+    constexpr int N = IL ? 4 : 8;
+    const int half = rot / 2;
+    const int first = IL ? 4 * chunk : 8 * chunk < half ? 8 * chunk : 8 * chunk - half;
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(tab + first + e);
+      const float4 b = *reinterpret_cast<const float4*>(tab + half + first + e);
+      c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
+      s[e] = b.x, s[e + 1] = b.y, s[e + 2] = b.z, s[e + 3] = b.w;
+    }
+  }
+  // every lane of the warp takes part (shuffles); src: the lane that holds the partners
+  __device__ __forceinline__ void turn(float (&x)[8], int src, bool second) const {
+    if constexpr (IL) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        x[2 * e] = a * c[e] - b * s[e];
+        x[2 * e + 1] = a * s[e] + b * c[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float other = __shfl_sync(0xffffffffu, x[e], src);
+        x[e] = second ? other * s[e] + x[e] * c[e] : x[e] * c[e] - other * s[e];
+      }
+    }
+  }
+};
+
+// Rows of token i's heads, from row r0 on, 32 / (D / 8) of them a load: keys (stored),
+// queries, values (copied), in this order; `first`: the rows before r0 that this launch
+// leaves to others (a packed pool's keys), `rows`: one past the last.
+template <int D, bool IL>
+__device__ __forceinline__ void copy_rows(const RotatedWriteArgs& a, int i, int r0, int rows) {
+  constexpr int LPH = D / 8;     // lanes a head
+  constexpr int HPL = 32 / LPH;  // heads a load
+  const int lane = threadIdx.x & 31, c = lane % LPH, sub = lane / LPH;
+  const int hkv = a.lv.hkv, hq = a.Hq;
+  uint4 raw[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int r = r0 + u * HPL + sub;
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const uint16_t* src = r < hkv ? a.k + (int64_t)i * a.k_tok + r * a.k_head
+                            : r < hkv + hq ? a.q + (int64_t)i * a.q_tok + (r - hkv) * a.q_head
+                                           : a.v + (int64_t)i * a.v_tok + (r - hkv - hq) * a.v_head;
+      raw[u] = reinterpret_cast<const uint4*>(src)[c];
+    }
+  }
+  const int32_t pos = a.positions[i], row = a.rows[i], slot = a.slots[i];
+  const bool pos_ok = pos >= 0 && pos < a.n_pos, ok = place_ok(a.lv, row, slot) && pos_ok;
+  if (!ok && r0 == 0 && lane == 0) flag(a.lv, pos_ok, row);
+  if (!pos_ok) return;
+  uint4 *kd = nullptr, *vd = nullptr;
+  if (ok) {
+    kd = reinterpret_cast<uint4*>(draft_row(a.lv, PKV_KIND_K, row, slot, 0));
+    vd = reinterpret_cast<uint4*>(draft_row(a.lv, PKV_KIND_V, row, slot, 0));
+  }
+  const int half = a.rot / 16;  // chunks of half of the turned part
+  const bool turned = c < 2 * half, second = c >= half;
+  const int src = lane + (turned ? (second ? -half : half) : 0);
+  Angles<IL> ang;
+  if (turned) ang.load(a.cos_sin + (int64_t)pos * a.rot, c, a.rot);
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int r = r0 + u * HPL + sub;
+    const bool is_v = r >= hkv + hq;
+    float x[8];
+    unpack8(raw[u], x);
+    const uint16_t* w = r < hkv ? a.k_norm : is_v ? nullptr : a.q_norm;
+    if (a.k_norm || a.q_norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+#pragma unroll
+      for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (w) {
+        const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+        float g[8];
+        unpack8(reinterpret_cast<const uint4*>(w)[c], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * g[e];
+      }
+    }
+    const float keep[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+    ang.turn(x, src, second);
+    if (!turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = keep[e];
+    }
+    // untouched values keep their bits
+    const uint4 o = is_v || (!turned && !w) ? raw[u] : pack8(x);
+    if (r < rows) {
+      if (r < hkv) {
+        if (ok) kd[r * LPH + c] = o;
+      } else if (!is_v) {
+        reinterpret_cast<uint4*>(a.qo + (int64_t)i * a.o_tok + (r - hkv) * a.o_head)[c] = o;
+      } else if (ok) {
+        vd[(r - hkv - hq) * LPH + c] = o;
+      }
+    }
+  }
+}
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(256) rotated_write_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t u = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t i = u / (uint32_t)P.per_token;
+  if (i >= (uint32_t)P.a.n) return;
+  copy_rows<D, IL>(P.a, (int)i, (int)(u - i * P.per_token) * kLoads * (256 / D), 2 * P.a.lv.hkv + P.a.Hq);
+}
+
+// ---------------------------------------------------------------------------
+// Packed pools
+// ---------------------------------------------------------------------------
+constexpr int E = 16;  // values a lane
+
+__device__ __forceinline__ void load16(const uint16_t* src, float (&x)[E]) {
+  const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
+  float lo[8], hi[8];
+  unpack8(a, lo);
+  unpack8(b, hi);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = lo[e], x[8 + e] = hi[e];
+}
+
+// Codes and (scale, offset) of a row's groups, lane `c` of the row's D / 16.  IEEE single
+// precision, one rounding an operation.  The scale is the range times the rounded 1 / TOP: an
+// ulp from the quotient at most (the codes are the nearest for the scale that is stored).
+template <int BITS, int GS>
+__device__ __forceinline__ void quantise(const float (&x)[E], uint8_t* codes, uint8_t* meta, int c, bool store) {
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int e = 1; e < E; ++e) mn = fminf(mn, x[e]), mx = fmaxf(mx, x[e]);
+#pragma unroll
+  for (int off = 1; off < GS / E; off <<= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  }
+  constexpr int TOP = (1 << BITS) - 1;
+  const float scale = __fmul_rn(__fsub_rn(mx, mn), 1.0f / TOP);
+  uint32_t w[E * BITS / 32];
+#pragma unroll
+  for (int k = 0; k < E * BITS / 32; ++k) w[k] = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    int q = 0;
+    if (scale != 0.0f) {
+      q = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], mn), scale));
+      q = q < 0 ? 0 : (q > TOP ? TOP : q);
+    }
+    w[e * BITS / 32] |= (uint32_t)q << (e * BITS % 32);
+  }
+  if (!store) return;
+  if constexpr (BITS == 8)
+    reinterpret_cast<uint4*>(codes)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    reinterpret_cast<uint2*>(codes)[c] = make_uint2(w[0], w[1]);
+  if (c % (GS / E) == 0) reinterpret_cast<float2*>(meta)[c / (GS / E)] = make_float2(scale, mn);
+}
+
+// x += the exact product a b, x = (h, l)
+__device__ __forceinline__ void two_prod_add(float& h, float& l, float a, float b) {
+  const float p = __fmul_rn(a, b), pe = __fmaf_rn(a, b, -p);
+  const float s = __fadd_rn(h, p), t = __fsub_rn(s, h);
+  const float se = __fadd_rn(__fsub_rn(h, __fsub_rn(s, t)), __fsub_rn(p, t));
+  h = s;
+  l = __fadd_rn(l, __fadd_rn(se, pe));
+}
+
+template <int D>
+__device__ __forceinline__ void butterflies(float (&x)[E], int c) {
+#pragma unroll
+  for (int hs = 1; hs < E; hs <<= 1)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((e & hs) == 0) {
+        const float a = x[e], b = x[e + hs];
+        x[e] = a + b;
+        x[e + hs] = a - b;
+      }
+#pragma unroll
+  for (int m = 1; m < D / E; m <<= 1) {
+    const bool upper = (c & m) != 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float other = __shfl_xor_sync(0xffffffffu, x[e], m);
+      x[e] = upper ? other - x[e] : x[e] + other;
+    }
+  }
+}
+
+// A lane group's (token, head) row of keys: normalise, turn, into the Hadamard basis,
+// quantise.  Lanes past the last row take part in the shuffles with row 0's data.
+template <int D, bool IL, int BITS, int GS>
+__device__ __forceinline__ void pack_keys(const RotatedWriteArgs& a, int64_t r, bool live) {
+  constexpr int LPR = D / E;
+  const int lane = threadIdx.x & 31, c = lane % LPR;
+  const int i = (int)(r / a.lv.hkv), h = (int)(r - (int64_t)i * a.lv.hkv);
+  float x[E], l[E];
+  load16(a.k + (int64_t)i * a.k_tok + h * a.k_head + c * E, x);
+  const int32_t pos = a.positions[i], row = a.rows[i], slot = a.slots[i];
+  const bool pos_ok = pos >= 0 && pos < a.n_pos, ok = live && pos_ok && place_ok(a.lv, row, slot);
+  if (live && !ok && h == 0 && c == 0) flag(a.lv, pos_ok, row);
+  if (a.k_norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss += x[e] * x[e];
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+    float g[E];
+    load16(a.k_norm + c * E, g);
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = x[e] * rs * g[e];
+  }
+  const int half = a.rot / 2;
+  const bool turned = c * E < a.rot && pos_ok, second = c * E >= half;
+  const float* tab = a.cos_sin + (pos_ok ? (int64_t)pos * a.rot : 0);
+  if constexpr (IL) {
+#pragma unroll
+    for (int e = 0; e < E; e += 8) {
+      float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (turned) {
+        cs = *reinterpret_cast<const float4*>(tab + (c * E + e) / 2);
+        sn = *reinterpret_cast<const float4*>(tab + half + (c * E + e) / 2);
+      }
+      const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = x[e + 2 * j], v = x[e + 2 * j + 1];
+        float h0 = 0.f, l0 = 0.f, h1 = 0.f, l1 = 0.f;
+        two_prod_add(h0, l0, u, cc[j]);
+        two_prod_add(h0, l0, -v, ss[j]);
+        two_prod_add(h1, l1, u, ss[j]);
+        two_prod_add(h1, l1, v, cc[j]);
+        x[e + 2 * j] = h0, l[e + 2 * j] = l0;
+        x[e + 2 * j + 1] = h1, l[e + 2 * j + 1] = l1;
+      }
+    }
+  } else {
+    const int src = lane + (c * E < a.rot ? (second ? -half / E : half / E) : 0);
+    const int first = second ? c * E - half : c * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 4) {
+      float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (turned) {
+        cs = *reinterpret_cast<const float4*>(tab + first + e);
+        sn = *reinterpret_cast<const float4*>(tab + half + first + e);
+      }
+      const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float other = __shfl_sync(0xffffffffu, x[e + j], src);
+        float hh = 0.f, ll = 0.f;
+        two_prod_add(hh, ll, x[e + j], cc[j]);
+        two_prod_add(hh, ll, second ? other : -other, ss[j]);
+        x[e + j] = hh, l[e + j] = ll;
+      }
+    }
+  }
+  // the leading part: multiples of 2^(ex - 15), ex the exponent of the row's largest value
+  float mx = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+  for (int off = 1; off < LPR; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  const int ex = max(-118, min(118, (int)(__float_as_uint(mx) >> 23) - 127));
+  const float big = __uint_as_float((uint32_t)(127 + ex + 8) << 23 | 0x400000u);  // 1.5 2^(ex + 8)
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float sign = a.signs[c * E + e];
+    const float lead = __fsub_rn(__fadd_rn(x[e], big), big);
+    l[e] = sign * __fadd_rn(__fsub_rn(x[e], lead), l[e]);
+    x[e] = sign * lead;
+  }
+  butterflies<D>(x, c);
+  butterflies<D>(l, c);
+  // times 1 / sqrt(D), as a sum of two FP32
+  constexpr double inv = D == 64 ? 0.125 : D == 128 ? 0.08838834764831845 : 0.0625;
+  constexpr float i0 = (float)inv, i1 = (float)(inv - (double)(float)inv);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float p = __fmul_rn(x[e], i0), pe = __fmaf_rn(x[e], i0, -p);
+    x[e] = __fadd_rn(p, __fadd_rn(__fmaf_rn(x[e], i1, pe), __fmul_rn(l[e], i0)));
+  }
+  quantise<BITS, GS>(x, ok ? draft_row(a.lv, PKV_KIND_K, row, slot, h) : nullptr,
+                     ok ? draft_row(a.lv, PKV_KIND_KMETA, row, slot, h) : nullptr, c, ok);
+}
+
+template <int D, int BITS, int GS>
+__device__ __forceinline__ void pack_values(const RotatedWriteArgs& a, int64_t r, bool live) {
+  const int c = (threadIdx.x & 31) % (D / E);
+  const int i = (int)(r / a.lv.hkv), h = (int)(r - (int64_t)i * a.lv.hkv);
+  float x[E];
+  load16(a.v + (int64_t)i * a.v_tok + h * a.v_head + c * E, x);
+  const int32_t pos = a.positions[i], row = a.rows[i], slot = a.slots[i];
+  const bool ok = live && pos >= 0 && pos < a.n_pos && place_ok(a.lv, row, slot);
+  quantise<BITS, GS>(x, ok ? draft_row(a.lv, PKV_KIND_V, row, slot, h) : nullptr,
+                     ok ? draft_row(a.lv, PKV_KIND_VMETA, row, slot, h) : nullptr, c, ok);
+}
+
+template <int D, bool IL, int KBITS, int VBITS, int GS>
+__global__ void __launch_bounds__(256) rotated_pack_kernel(const __grid_constant__ Params P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int RPW = 32 / (D / E);  // rows a warp
+  int64_t u = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (u < 2 * P.pack_units) {
+    const bool values = u >= P.pack_units;
+    const int64_t r = (values ? u - P.pack_units : u) * RPW + (threadIdx.x & 31) / (D / E);
+    const bool live = r < (int64_t)P.a.n * P.a.lv.hkv;
+    if (values)
+      pack_values<D, VBITS, GS>(P.a, live ? r : 0, live);
+    else
+      pack_keys<D, IL, KBITS, GS>(P.a, live ? r : 0, live);
+    return;
+  }
+  u -= 2 * P.pack_units;
+  const int64_t i = u / P.per_token;
+  if (i >= P.a.n || P.a.Hq == 0) return;
+  copy_rows<D, IL>(P.a, (int)i, P.a.lv.hkv + (int)(u - i * P.per_token) * kLoads * (256 / D), P.a.lv.hkv + P.a.Hq);
+}
+
+template <int D, bool IL>
+cudaError_t launch_di(const RotatedWriteArgs& a) {
+  Params P;
+  P.a = a;
+  P.pack_units = 0;
+  constexpr int per_warp = kLoads * (256 / D);
+  const int rows = a.fmt == PKV_FMT_BF16 ? 2 * a.lv.hkv + a.Hq : a.Hq;
+  P.per_token = rows > 0 ? (rows + per_warp - 1) / per_warp : 1;
+  int64_t units = rows > 0 ? (int64_t)a.n * P.per_token : 0;
+  if (a.fmt != PKV_FMT_BF16) {
+    constexpr int RPW = 32 / (D / E);
+    P.pack_units = ((int64_t)a.n * a.lv.hkv + RPW - 1) / RPW;
+    units += 2 * P.pack_units;
+  }
+  // a step's few tokens spread over the SMs, one warp per CTA
+  const int threads = units < 2048 ? 32 : 256;
+  const dim3 grid((unsigned)((units * 32 + threads - 1) / threads));
+  static std::atomic<uint64_t> none{0};
+  void (*kern)(Params) = rotated_write_kernel<D, IL>;
+  if (a.fmt == PKV_FMT_K4V4)
+    kern = D >= 128 && a.group == kGroupWide ? rotated_pack_kernel<D, IL, 4, 4, (D >= 128 ? kGroupWide : kGroup)>
+                                             : rotated_pack_kernel<D, IL, 4, 4, kGroup>;
+  else if (a.fmt == PKV_FMT_K8V4)
+    kern = rotated_pack_kernel<D, IL, 8, 4, kGroup>;
+  else if (a.fmt == PKV_FMT_K8V8)
+    kern = rotated_pack_kernel<D, IL, 8, 8, kGroup>;
+  return tc_launch(kern, grid, threads, (size_t)0, a.stream, P, 0, &none);
+}
+
+}  // namespace
+
+int rotated_write_units(int hkv, int Hq) { return 2 * hkv + Hq; }  // of any head_dim, packed or not, at most
+
+cudaError_t launch_rotated_write(const RotatedWriteArgs& a) {
+  switch (a.D) {
+    case 64: return a.interleaved ? launch_di<64, true>(a) : launch_di<64, false>(a);
+    case 128: return a.interleaved ? launch_di<128, true>(a) : launch_di<128, false>(a);
+    default: return a.interleaved ? launch_di<256, true>(a) : launch_di<256, false>(a);
+  }
+}
+
+}  // namespace pkv
