@@ -1,0 +1,981 @@
+// tree_attn.cuh — attention of drafted token trees over the per-head pools, on the tensor
+// cores.
+//
+//   x[r, t] = scale q[r] . k_t,   o[r] = sum_t exp2(x[r, t] - m[r]) v_t / sum_t exp2(x[r, t] - m[r])
+//
+// r: a (query, head) row of one kv head; t: the tokens t < len - n_q, and the drafted tokens
+// (the last n_q) that the query's mask row names.  A token's key and value are read once for
+// all rows of its kv head: with R rows it costs 4 R D operations and the stored bytes (4 D in
+// bf16), so HBM bounds up to about R = 250 rows, the tensor cores beyond.
+//
+// Layout.  The rows are the MMA's M (a tile of 128), 64 tokens a tile its N:
+//   S [128 x 64] = Q [128 x D] K^T          Q and K in shared memory, K-major
+//   O [128 x D] += P [128 x 64] V           P over S in tensor memory (bf16), V MN-major
+// A thread of a softmax warpgroup owns a row: no reduction leaves the thread.  Two warpgroups
+// share the work by mode:
+//   kPair   more than 128 rows: a tile of rows each, all key tiles
+//   kTurns  up to 128 rows: the same rows, key tiles in turns, an O each, added at the end
+//   kSolo   head_dim 256 (whose O fills half of tensor memory): one of them takes all
+// S is double-buffered per warpgroup, so that the next product runs under the softmax.  The
+// reference m moves only when a logit passes it by more than 2^8: O is then rescaled.
+//
+// bf16 keys and values go from the pool to swizzled operand tiles by 16-byte asynchronous
+// copies, which fill tokens that nobody sees (past the length, unused drafts) with zeros: a
+// stale NaN reaches neither product.  Packed ones are expanded to operands by seven warps, whose
+// threads hold the next tile's codes in registers while they expand this one's (the tiles behind
+// it are on their way to L2): keys to fp16, each token's under the power of two that puts its
+// largest value near 2^13 (put back into the logits), values to bf16, whose range needs none.
+//
+// The key tiles of all units (sequence, kv head, 128 or 256 rows) are laid end to end and split
+// evenly in cost over the CTAs, one a SM.  A unit inside one CTA's share is written directly; a
+// split one leaves FP32 records that a second kernel merges in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "drafts.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace tree {
+
+enum Mode { kTurns = 0, kPair = 1, kSolo = 2 };
+
+constexpr int kTile = 64;               // tokens a tile
+constexpr int kRows = 128;              // rows a tile of rows
+// Warps 0..7: softmax; 8: MMAs; from 9 on: keys and values (feeders).
+constexpr int kSoftmaxThreads = 256;
+constexpr int kFeeder0 = 288;           // the first feeder thread
+constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the reference
+constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
+constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
+constexpr int kTokRing = 8;             // tiles whose keys' powers are held (see Small::tok)
+
+// Cost of a unit's start in the split over the CTAs, in quarter tiles: its queries are loaded
+// and its output or record written.
+constexpr int kSegCost = 16;
+constexpr int kCost = 4;
+
+template <int D, int MODE, bool PACKED>
+struct Plan {
+  // Packed: seven warps, so that the launch has 16 and a thread 128 registers.
+  static constexpr int kWarps = PACKED ? 7 : 4;
+  static constexpr int kFeeders = kWarps * 32;
+  static constexpr int kThreads = kFeeder0 + kFeeders;
+  static constexpr int kTileRows = MODE == kPair ? 2 * kRows : kRows;  // rows a unit
+  static constexpr int kQBytes = kTileRows * D * 2;
+  static constexpr int kSlot = kTile * D * 2;
+  static constexpr int kK = D == 256 ? 2 : PACKED ? 4 : D == 64 ? 8 : 5;
+  static constexpr int kV = D == 256 ? 2 : PACKED || D == 128 ? 4 : 8;
+  static constexpr int kLag = MODE == kTurns ? 2 : 1;  // tiles between a tile's S and its values
+  // Packed: pieces a feeder thread takes of a tile, at most (8-bit keys and values).
+  static constexpr int kPieces = PACKED ? (D / 4 + kWarps - 1) / kWarps : 0;
+  static constexpr int kSmall = 8 * 1024;
+  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kSlot + kSmall;
+  static_assert(kSmem <= kSmemLimit, "shared memory");
+  static_assert(!PACKED || kK + kLag + 1 <= kTokRing, "a tile's powers are read until its softmax is done");
+  static_assert(kV >= kLag, "the values of kLag tiles wait for their softmax while the next keys are awaited");
+};
+
+struct Params {
+  TreeAttnArgs a;
+  int G;         // query heads a kv head
+  int rows;      // n_q * G
+  int tile_rows; // rows a unit
+  int n_rt;      // units a (sequence, kv head)
+  int rec_rows;  // rows a record
+  int words;     // mask words a query
+  int kbits, vbits;
+  int2* meta;    // [B * hkv * n_rt]: first CTA of a split unit (-1: written directly), last CTA
+  float2* ml;    // [2 * grid][rec_rows]: reference and sum of a record's rows
+  float* acc;    // [2 * grid][rec_rows][D]
+};
+
+__device__ __forceinline__ int32_t length(const Params& P, int b) {
+  bool bad;
+  return draft_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
+}
+
+// A CTA's share of the tiles: a unit of n tiles costs kCost n + kSegCost, its tile k sits at
+// kSegCost + kCost k from its start, and CTA g holds the positions [g V, (g + 1) V).  V is at
+// least kCost, so the CTAs that hold a unit's tiles are consecutive.
+struct Segment {
+  int b, len, x;    // sequence, its length, unit within it: kv head * n_rt + group of rows
+  int k0, k1, n;    // this CTA's tiles of it, and all of them
+};
+
+struct Walk {
+  int b, x;
+  int64_t at;      // position of sequence b's first unit
+  int64_t lo, hi;  // positions of this CTA
+
+  // Warp-uniform values, known as such: copies and MMAs are issued with what follows from them.
+  __device__ __forceinline__ bool next(const Params& P, Segment& s) {
+    const int upb = P.a.lv.hkv * P.n_rt;
+    while (b < P.a.B) {
+      const int len = uniform(length(P, b));
+      const int n = (len + kTile - 1) / kTile;
+      const int64_t cost = n > 0 ? (int64_t)kCost * n + kSegCost : 0;
+      const int64_t first = at + x * cost + kSegCost;  // position of the unit's first tile
+      if (n > 0 && first >= hi) return false;
+      s.b = b, s.len = len, s.n = n, s.x = x;
+      if (n == 0 || ++x == upb) {
+        at += upb * cost;
+        x = 0;
+        ++b;
+      }
+      if (n == 0) continue;
+      const int64_t f = first >= lo ? 0 : (lo - first + kCost - 1) / kCost;
+      const int64_t e = (hi - first + kCost - 1) / kCost;
+      s.k0 = uniform((int)(f < n ? f : n));
+      s.k1 = uniform((int)(e < n ? e : n));
+      if (s.k1 > s.k0) return true;
+    }
+    return false;
+  }
+};
+
+// One warp: the CTA's positions and where its walk starts.
+__device__ __forceinline__ Walk start_walk(const Params& P) {
+  constexpr int kHeld = 128;  // sequences whose lengths are read once
+  const int lane = threadIdx.x & 31;
+  const int64_t upb = (int64_t)P.a.lv.hkv * P.n_rt;
+  auto cost = [&](int b) -> int64_t {
+    if (b >= P.a.B) return 0;
+    const int n = (length(P, b) + kTile - 1) / kTile;
+    return n > 0 ? upb * ((int64_t)kCost * n + kSegCost) : 0;
+  };
+  int64_t held[kHeld / 32], total = 0;
+#pragma unroll
+  for (int c = 0; c < kHeld / 32; ++c) {
+    held[c] = 32 * c < P.a.B ? cost(32 * c + lane) : 0;
+    total += held[c];
+  }
+  for (int b = kHeld + lane; b < P.a.B; b += 32) total += cost(b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  Walk w;
+  const int64_t v = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t V = v > kCost ? v : kCost;
+  w.lo = blockIdx.x * V;
+  w.hi = w.lo + V;
+  w.b = P.a.B;
+  w.x = 0;
+  w.at = total;
+  int64_t carry = 0;
+  // the first sequence that ends past the CTA's first position
+  auto found = [&](int base, int64_t c) {
+    int64_t inc = c;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, c > 0 && carry + inc > w.lo);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int64_t mine = __shfl_sync(0xffffffffu, c, l);
+      w.b = base + l;
+      w.at = carry + __shfl_sync(0xffffffffu, inc - c, l);
+      w.x = w.lo > w.at ? (int)((w.lo - w.at) / (mine / upb)) : 0;
+      return true;
+    }
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+    return false;
+  };
+#pragma unroll
+  for (int c = 0; c < kHeld / 32; ++c)
+    if (32 * c < P.a.B && found(32 * c, held[c])) return w;
+  for (int base = kHeld; base < P.a.B; base += 32)
+    if (found(base, cost(base + lane))) return w;
+  return w;
+}
+
+// Shared-memory state besides the operands.
+struct Small {
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // by slot
+  uint64_t s_full[2][2], p_full[2][2];                    // by warpgroup and buffer
+  uint64_t pv_done[2], q_full, q_empty, drain;
+  Walk walk;
+  uint32_t tmem;
+  int dead;                    // a wait gave up: every role runs on without waiting or issuing
+  float m[2][kRows], l[2][kRows];  // the warpgroups' references and sums of shared rows
+  float q_pow[2 * kRows];      // packed: the power of two that a row's query was divided by
+  // Packed: scale times the power of two that a token's key was divided by.  A tile's are
+  // overwritten kTokRing tiles later, when its softmax has long handed its P over.
+  float tok[kTokRing][kTile];
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0),
+               "l"(policy)
+               : "memory");
+}
+// This thread's copies so far count as one arrival once they have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Bits of the tokens j0 .. j0 + 31 (counted from the first drafted one): before it all are
+// set, from n_q on none.  word(w): the w-th word of a mask, 0 <= w < words.
+template <typename F>
+__device__ __forceinline__ uint32_t bits_at(int j0, int n_q, int words, F&& word) {
+  if (j0 >= n_q) return 0u;
+  if (j0 + 31 < 0) return 0xffffffffu;
+  const int w = j0 >> 5, s = j0 & 31;
+  const uint32_t a = w < 0 ? 0xffffffffu : word(w), b = w + 1 < words ? word(w + 1) : 0u;
+  uint32_t r = __funnelshift_r(a, b, s);
+  if (j0 + 32 > n_q) r &= (1u << (n_q - j0)) - 1u;
+  return r;
+}
+
+// A feeder warp's view of a segment: the blocks of its next tiles, and which of their tokens
+// some query sees (the others' slots may hold anything).
+struct Feed {
+  const uint8_t* base;  // lane l: block 2 ub + l: keys of its slab (null outside the pool)
+  int r;                // its row in the slab
+  uint32_t named;       // lane w: OR over the queries of mask word w
+
+  __device__ __forceinline__ void see(const Params& P, const Segment& s) {
+    const int lane = threadIdx.x & 31;
+    named = 0;
+    if (s.k1 * kTile <= s.len - P.a.n_q) return;  // no drafted token here
+    const uint32_t* mask = P.a.mask + s.b * P.a.mask_stride;
+    for (int w = 0; w < P.words; ++w) {
+      uint32_t v = 0;
+      for (int i = lane; i < P.a.n_q; i += 32) v |= mask[(int64_t)i * P.words + w];
+      v = __reduce_or_sync(0xffffffffu, v);
+      if (lane == w) named = v;
+    }
+  }
+  // blocks of the tiles from ub on (16 of them)
+  __device__ __forceinline__ void look_up(const Params& P, const Segment& s, int ub) {
+    const int j = 2 * ub + (int)(threadIdx.x & 31);
+    base = nullptr;
+    r = 0;
+    if (j < 2 * s.k1 && j * kBlockTokens < s.len) {
+      const int32_t row = P.a.bt[(int64_t)s.b * P.a.max_blocks + j];
+      if (draft_row_ok(P.a.lv, row)) {
+        const int32_t slab = row / P.a.lv.slab_blocks;
+        r = row - slab * P.a.lv.slab_blocks;
+        base = P.a.lv.tab.base[(size_t)slab * P.a.lv.tab.stride];
+      } else {
+        atomicOr(P.a.lv.err, ERR_ROW);
+      }
+    }
+  }
+  // Packed: asks for the head's rows of 32 blocks from block j0 on (16 tiles) to come to L2, of
+  // the tokens w, w + step, ... of each.
+  __device__ __forceinline__ static void prefetch(const Params& P, const Segment& s, int j0, int kvh, int w, int step) {
+    const int j = j0 + (int)(threadIdx.x & 31);
+    if (j >= 2 * s.k1 || j * kBlockTokens >= s.len) return;
+    const LayerView& lv = P.a.lv;
+    const int32_t row = P.a.bt[(int64_t)s.b * P.a.max_blocks + j];
+    if (!draft_row_ok(lv, row)) return;
+    const int32_t slab = row / lv.slab_blocks;
+    const uint8_t* at = lv.tab.base[(size_t)slab * lv.tab.stride];
+    const int64_t slab_rows = (int64_t)lv.slab_blocks * kBlockTokens * lv.hkv;
+    const int64_t first = (int64_t)(row - slab * lv.slab_blocks) * kBlockTokens * lv.hkv + kvh;
+    for (int k = 0; k < 4; ++k) {
+      const int bytes = lv.row_bytes[k];
+      for (int t = w; t < kBlockTokens; t += step)
+        for (int i = 0; i < bytes; i += 128) prefetch_l2(at + (first + (int64_t)t * lv.hkv) * bytes + i);
+      at += slab_rows * bytes;
+    }
+  }
+  // the 64 tokens of tile u that are read
+  __device__ __forceinline__ uint2 tokens(const Params& P, const Segment& s, int u) const {
+    if ((u + 1) * kTile <= s.len - P.a.n_q) return make_uint2(0xffffffffu, 0xffffffffu);
+    const int j0 = u * kTile - (s.len - P.a.n_q);
+    auto word = [&](int w) { return __shfl_sync(0xffffffffu, named, w); };
+    const uint32_t lo = bits_at(j0, P.a.n_q, P.words, word);
+    return make_uint2(lo, bits_at(j0 + 32, P.a.n_q, P.words, word));
+  }
+};
+
+// Offset of 16-byte piece c (of the row's D / 8) of row r in an operand of rows of 64 values
+// under the 128-byte swizzle; col: bytes of one 64-value column (all rows).
+__device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t col) {
+  return (uint32_t)(c >> 3) * col + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// Queries of a unit's rows into shared memory, a row a warp at a time; packed: into the keys'
+// basis, under a power of two in fp16.
+template <int D, bool PACKED>
+__device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, Small& sm, int row0, int nrow) {
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = s.x / P.n_rt;
+  float sign[E];
+  if constexpr (PACKED) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sign[e] = P.a.signs[lane * E + e] * (D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f);
+  }
+  constexpr int U = 4;  // rows in flight
+  for (int rb = warp; rb < nrow; rb += 8 * U) {
+    uint32_t w[U][E / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = row0 + min(rb + 8 * u, nrow - 1);
+      const int i = r / P.G, g = r - i * P.G;
+      const uint16_t* src = P.a.q + (((int64_t)s.b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D + lane * E;
+      if constexpr (E == 2)
+        w[u][0] = *reinterpret_cast<const uint32_t*>(src);
+      else if constexpr (E == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        w[u][0] = v.x, w[u][1] = v.y;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(src);
+        w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = rb + 8 * u;
+      if (r >= nrow) break;
+      if constexpr (PACKED) {
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          bf16x2_to_f32(w[u][e / 2], x[e], x[e + 1]);
+          x[e] *= sign[e], x[e + 1] *= sign[e + 1];
+        }
+#pragma unroll
+        for (int hs = 1; hs < E; hs <<= 1)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if ((e & hs) == 0) {
+              const float a = x[e], b = x[e + hs];
+              x[e] = a + b;
+              x[e + hs] = a - b;
+            }
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float other = __shfl_xor_sync(0xffffffffu, x[e], m);
+            x[e] = lane & m ? other - x[e] : x[e] + other;
+          }
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const int ex = max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+        const float f = pow2(-ex);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[u][e / 2] = fp16x2(x[e] * f, x[e + 1] * f);
+        if (lane == 0) sm.q_pow[r] = pow2(ex);
+      }
+      const int byte = lane * E * 2, tile = r / kRows, rr = r % kRows;
+      uint8_t* dst = qs + tile * (kRows * D * 2) + swizzled(rr, byte / 16, kRows * 128) + byte % 16;
+      if constexpr (E == 2)
+        *reinterpret_cast<uint32_t*>(dst) = w[u][0];
+      else if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[u][0], w[u][1]);
+      else
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+    }
+  }
+}
+
+// A packed tile's pieces (16 bytes of codes with their group's scale and offset) over the
+// feeder warps: unit g of 32 pieces goes to warp g % 7, keys first.  Within a unit the lanes
+// are laid out so that eight of them write operand pieces to eight different bank groups.
+template <int D>
+struct Piece {
+  int token, value;  // its token in the tile and first value
+  bool key;
+  __device__ __forceinline__ Piece(const Params& P, int g) {
+    const int lane = threadIdx.x & 31;
+    const int ku = D * P.kbits / 64;
+    key = g < ku;
+    const int bits = key ? P.kbits : P.vbits, hb = bits == 4 ? 2 : 4;  // pieces of 64 values
+    const int tpu = 32 / (hb * (D / 64));
+    token = (key ? g : g - ku) * tpu + lane / hb % tpu;
+    value = lane / (hb * tpu) * 64 + lane % hb * (64 / hb);
+  }
+};
+
+// Eight 4-bit codes to floats, in order.
+__device__ __forceinline__ void codes4(uint32_t w, float (&c)[8]) {
+  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[2 * i] = __uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7540 | i)) - 8388608.f;
+    c[2 * i + 1] = __uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7540 | i)) - 8388608.f;
+  }
+}
+__device__ __forceinline__ void codes8(uint32_t w, float (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | i)) - 8388608.f;
+}
+
+// Codes of a piece as operand pieces: s c + o, in fp16 (keys) or bf16.
+template <int BITS, bool KEY>
+__device__ __forceinline__ void expand(const uint4& code, float s, float o, uint8_t* slot, int token, int value) {
+  const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+  constexpr int N = BITS == 4 ? 4 : 2;  // operand pieces of eight values
+  const uint64_t ss = pair2(s, s), oo = pair2(o, o);
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    float c[8];
+    if constexpr (BITS == 4) {
+      codes4(w[q], c);
+    } else {
+      float a[4], b[4];
+      codes8(w[2 * q], a);
+      codes8(w[2 * q + 1], b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = a[i], c[4 + i] = b[i];
+    }
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x, y;
+      split2(fma2(pair2(c[2 * i], c[2 * i + 1]), ss, oo), x, y);
+      out[i] = KEY ? fp16x2(x, y) : bf2(x, y);
+    }
+    *reinterpret_cast<uint4*>(slot + swizzled(token, value / 8 + q, kTile * 128)) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+template <int D, int MODE, bool PACKED>
+__global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_kernel(const __grid_constant__ Params P) {
+  using L = Plan<D, MODE, PACKED>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* qs = smem;
+  uint8_t* ks = qs + L::kQBytes;
+  uint8_t* vs = ks + L::kK * L::kSlot;
+  Small& sm = *reinterpret_cast<Small*>(vs + L::kV * L::kSlot);
+  static_assert(sizeof(Small) <= L::kSmall, "small state");
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  volatile int* dead = &sm.dead;
+  int32_t* err = P.a.lv.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sm.k_full[i], L::kFeeders);
+      mbar_init(&sm.v_full[i], L::kFeeders);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[t][i], 1), mbar_init(&sm.p_full[t][i], 128);
+      mbar_init(&sm.pv_done[t], 1);
+    }
+    mbar_init(&sm.q_full, kSoftmaxThreads);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.drain, 1);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tc_alloc(&sm.tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 0) {
+    const Walk w = start_walk(P);
+    if (lane == 0) sm.walk = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(sm.tmem);
+  auto tm_s = [&](int t, int buf) { return tmem + (t * 2 + buf) * kTile; };
+  auto tm_o = [&](int t) { return tmem + 256 + t * D; };
+  Walk walk = {uniform(sm.walk.b), uniform(sm.walk.x), uniform(sm.walk.at), uniform(sm.walk.lo), uniform(sm.walk.hi)};
+  Segment seg;
+  // Which warpgroups work on tile `it` (counted over the CTA's segments) of a unit with nrow rows
+  auto works = [&](int t, int it, int nrow) {
+    return MODE == kTurns ? (it & 1) == t : MODE == kPair ? t == 0 || nrow > kRows : t == 0;
+  };
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int tr = (warp & 3) * 32 + lane;  // row of the tile
+    int it0 = 0, n_seg = 0;
+    int jobs[2] = {0, 0};                   // tiles that the warpgroups took, over all segments
+    while (walk.next(P, seg)) {
+      const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = min(L::kTileRows, P.rows - row0);
+      const int kvh = seg.x / P.n_rt;
+      if (n_seg > 0) wait_or_die(&sm.q_empty, (n_seg - 1) & 1, dead, err);
+      load_queries<D, PACKED>(P, seg, qs, sm, row0, nrow);
+      fence_async_shared();
+      mbar_arrive(&sm.q_full);
+      __syncwarp();
+      named_barrier_sync(1, kSoftmaxThreads);  // q_pow is written; the segment before is read
+      ++n_seg;
+      const int rr = MODE == kPair ? t * kRows + tr : tr;  // row of the unit
+      const bool mine = rr < nrow;
+      const bool idle = (MODE == kPair ? t * kRows : 0) + (warp & 3) * 32 >= nrow;  // a warp without rows
+      const int r = row0 + (mine ? rr : 0);
+      const float qp = PACKED && mine ? sm.q_pow[rr] : 1.f;
+      const uint64_t qp2 = pair2(qp, qp);
+      float m = kNoMax;
+      uint64_t l = 0;  // two partial sums
+      const int before = jobs[t];
+      int it = it0;
+      for (int u = seg.k0; u < seg.k1; ++u, ++it) {
+        if (!works(t, it, nrow)) continue;
+        const int job = jobs[t]++, buf = job & 1;
+        wait_or_die(&sm.s_full[t][buf], (job >> 1) & 1, dead, err);
+        if (!idle) {
+          tc_fence_after();
+          float x[kTile];
+          {
+            uint32_t a[2][32];
+            tc_ld_rows<32>(tm_s(t, buf) + lanes, a[0]);
+            tc_ld_rows<32>(tm_s(t, buf) + 32 + lanes, a[1]);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(a[c >> 5][c & 31]);
+          }
+#pragma unroll
+          for (int c = 0; c < kTile; c += 4) {
+            float4 f = make_float4(P.a.scale_log2, P.a.scale_log2, P.a.scale_log2, P.a.scale_log2);
+            if constexpr (PACKED) f = *reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][c]);
+            split2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), x[c], x[c + 1]);
+            split2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), x[c + 2], x[c + 3]);
+          }
+          if ((u + 1) * kTile > seg.len - P.a.n_q) {
+            const int j0 = u * kTile - (seg.len - P.a.n_q);
+            const uint32_t* mask = P.a.mask + seg.b * P.a.mask_stride + (int64_t)(r / P.G) * P.words;
+            auto word = [&](int w) { return mask[w]; };
+            const uint32_t b0 = bits_at(j0, P.a.n_q, P.words, word), b1 = bits_at(j0 + 32, P.a.n_q, P.words, word);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (!(b0 >> c & 1u)) x[c] = -INFINITY;
+              if (!(b1 >> c & 1u)) x[32 + c] = -INFINITY;
+            }
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int c = 4; c + 4 < kTile; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
+          // rows past the unit's hold anything: they must not move the references of this warp's others
+          const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * qp : -INFINITY;
+          if (__any_sync(0xffffffffu, top - m > kSlack)) {
+            const float mn = fmaxf(m, rintf(top));
+            const float f = ex2(m - mn);
+            m = mn;
+            l = mul2(l, pair2(f, f));
+            if (job > before) {
+              wait_or_die(&sm.pv_done[t], (job - 1) & 1, dead, err);
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tc_ld_rows<32>(tm_o(t) + 32 * q + lanes, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tc_st_rows<32>(tm_o(t) + 32 * q + lanes, o);
+              }
+            }
+          }
+          __syncwarp();
+          const uint64_t mm = pair2(-m, -m);
+          uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float e0, e1;
+              const uint64_t xx = pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
+              split2(PACKED ? fma2(xx, qp2, mm) : add2(xx, mm), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              uint64_t& s = c & 1 ? sum1 : sum0;
+              s = add2(s, pair2(e0, e1));
+              w[c] = bf2(e0, e1);
+            }
+            tc_st_rows<16>(tm_s(t, buf) + 16 * q + lanes, w);
+          }
+          l = add2(l, add2(sum0, sum1));
+          tc_wait_st();
+          tc_fence_before();
+        }
+        mbar_arrive(&sm.p_full[t][buf]);
+      }
+      // Tiles that each warpgroup took of this segment.
+      const int n = seg.k1 - seg.k0;
+      int took[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        took[k] = MODE == kTurns ? (n + (((it0 & 1) == k) ? 1 : 0)) / 2 : works(k, 0, nrow) ? n : 0;
+      jobs[t ^ 1] += took[t ^ 1];
+      it0 += n;
+      // Output of the segment: O / sum, or a record (reference, sum, O) to be merged.
+      const bool whole = seg.k0 == 0 && seg.k1 == seg.n;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.k0 > 0 ? 0 : 1);
+      if (threadIdx.x == 0) {
+        int2* meta = P.meta + (int64_t)seg.b * P.a.lv.hkv * P.n_rt + seg.x;
+        if (seg.k0 == 0) meta->x = whole ? -1 : (int)blockIdx.x;
+        if (seg.k1 == seg.n) meta->y = (int)blockIdx.x;
+      }
+      float l0, l1;
+      split2(l, l0, l1);
+      float sum = l0 + l1, f[2] = {1.f, 0.f};
+      // kTurns, kSolo: each warpgroup takes half of the columns of both O.
+      const bool shared_rows = MODE != kPair;
+      if (shared_rows) {
+        sm.m[t][tr] = m;
+        sm.l[t][tr] = sum;
+        __syncwarp();
+        named_barrier_sync(1, kSoftmaxThreads);
+        const float m0 = sm.m[0][tr], m1 = sm.m[1][tr];
+        m = fmaxf(m0, m1);
+        f[0] = ex2(m0 - m), f[1] = ex2(m1 - m);
+        sum = f[0] * sm.l[0][tr] + f[1] * sm.l[1][tr];
+      }
+      const int64_t rec = slot * P.rec_rows + rr;
+      if (!whole && mine && (!shared_rows || t == 0)) P.ml[rec] = make_float2(m, sum);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (took[k] > 0 && (shared_rows || k == t)) wait_or_die(&sm.pv_done[k], (jobs[k] - 1) & 1, dead, err);
+      tc_fence_after();
+      if (!idle) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int i = r / P.G, g = r - i * P.G;
+        uint16_t* out = P.a.out + (((int64_t)seg.b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D;
+        float* acc = P.acc + rec * D;
+        const int c0 = shared_rows ? t * (D / 64) : 0, c1 = shared_rows ? c0 + D / 64 : D / 32;
+#pragma unroll 1
+        for (int q = c0; q < c1; ++q) {
+          float o[32];
+          uint32_t a[32];
+          // The tensor-memory loads want the whole warp at once, which has just stored by rows.
+          __syncwarp();
+          if (shared_rows && took[0] == 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0.f;
+          } else {
+            tc_ld_rows<32>(tm_o(shared_rows ? 0 : t) + 32 * q + lanes, a);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __uint_as_float(a[c]) * f[0];
+          }
+          if (MODE == kTurns && took[1] > 0) {
+            tc_ld_rows<32>(tm_o(1) + 32 * q + lanes, a);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = fmaf(__uint_as_float(a[c]), f[1], o[c]);
+          }
+          if (mine && whole) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<uint4*>(out + 32 * q)[c] =
+                  make_uint4(bf2(o[8 * c] * inv, o[8 * c + 1] * inv), bf2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
+                             bf2(o[8 * c + 4] * inv, o[8 * c + 5] * inv), bf2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+          } else if (mine) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              reinterpret_cast<float4*>(acc + 32 * q)[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          }
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+    }
+  } else if (warp == 8) {
+    // -------------------------------------------------------------------- MMAs
+    constexpr uint32_t id_s = tc_idesc(kRows, kTile, false, false, PACKED);
+    constexpr uint32_t id_o = tc_idesc(kRows, D, false, true);
+    const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ks), 16, 1024);
+    const uint64_t d_v = tc_desc(smem_u32(vs), kTile * 128, 1024);
+    int it = 0, n_seg = 0, jobs[2] = {0, 0}, done[2] = {0, 0};
+    uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
+    bool alive = true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) { alive = alive && warp_wait(bar, parity, dead, err); };
+    while (alive && walk.next(P, seg)) {
+      const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = uniform(min(L::kTileRows, P.rows - row0));
+      const int first[2] = {done[0], done[1]};
+      const int n = uniform(seg.k1 - seg.k0), it0 = it;
+      ready(&sm.q_full, n_seg & 1);
+      ++n_seg;
+      // S of this tile for warpgroup t
+      auto logits = [&](int t) {
+        const int buf = jobs[t] & 1;
+        if (alive && elect_one()) {
+          const uint64_t q = d_q + ((MODE == kPair ? t * (kRows * D * 2) : 0) >> 4), k = d_k + ((kslot * L::kSlot) >> 4);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            tc_mma(tm_s(t, buf), q + (((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4),
+                   k + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4), id_s, c > 0);
+          tc_commit(&sm.s_full[t][buf]);
+        }
+        ++jobs[t];
+      };
+      // O += P V of warpgroup t's next tile
+      auto add_values = [&](int t) {
+        const int buf = done[t] & 1;
+        ready(&sm.p_full[t][buf], (done[t] >> 1) & 1);
+        tc_fence_after();
+        if (alive && elect_one()) {
+          const uint64_t v = d_v + ((vslot * L::kSlot) >> 4);
+#pragma unroll
+          for (int c = 0; c < kTile / 16; ++c)
+            tc_mma_ts(tm_o(t), tm_s(t, buf) + 8 * c, v + ((c * 2048) >> 4), id_o, done[t] > first[t] || c > 0);
+          tc_commit(&sm.pv_done[t]);
+        }
+        ++done[t];
+      };
+      for (int i = 0; alive && i < n + L::kLag; ++i) {
+        const bool values = i >= L::kLag;
+        if (i < n) {
+          ready(&sm.k_full[kslot], kround & 1);
+          fence_async_shared();  // the copies' writes, seen through the barrier, before the product's reads
+          tc_fence_after();
+          if (works(0, it0 + i, nrow)) logits(0);
+        }
+        if (values) {
+          ready(&sm.v_full[vslot], vround & 1);
+          fence_async_shared();
+          if (works(0, it0 + i - L::kLag, nrow)) add_values(0);
+        }
+        if (i < n) {
+          if (works(1, it0 + i, nrow)) logits(1);
+          if (alive && elect_one()) {
+            tc_commit(&sm.k_empty[kslot]);
+            if (i == n - 1) tc_commit(&sm.q_empty);
+          }
+          if (++kslot == L::kK) kslot = 0, ++kround;
+        }
+        if (values) {
+          if (works(1, it0 + i - L::kLag, nrow)) add_values(1);
+          if (alive && elect_one()) tc_commit(&sm.v_empty[vslot]);
+          if (++vslot == L::kV) vslot = 0, ++vround;
+        }
+      }
+      it += n;
+    }
+    __syncwarp();
+    if (elect_one()) tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
+    mbar_wait_bounded(&sm.drain, 0, err);
+  } else if constexpr (!PACKED) {
+    // ------------------------------------------------------------------ copies
+    constexpr int CPT = D / 8;                  // 16-byte pieces of a token's row
+    constexpr int TPP = L::kFeeders / CPT;      // tokens a pass
+    const int tid = threadIdx.x - kFeeder0;
+    const int c = tid % CPT, tk = tid / CPT;
+    const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const int64_t v_off = (int64_t)P.a.lv.slab_blocks * kBlockTokens * P.a.lv.hkv * (D * 2);  // a slab's values follow its keys
+    const int64_t token = (int64_t)P.a.lv.hkv * (D * 2);
+    uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
+    Feed feed;
+    while (walk.next(P, seg)) {
+      const int kvh = seg.x / P.n_rt;
+      feed.see(P, seg);
+      for (int ub = seg.k0; ub < seg.k1; ub += 16) {
+        feed.look_up(P, seg, ub);
+        const int ue = min(ub + 16, seg.k1);
+        for (int u = ub; u < ue; ++u) {
+          const uint2 live = feed.tokens(P, seg, u);
+          const uint8_t* blk[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            blk[k] = lane_ptr(feed.base, 2 * (u - ub) + k);
+            const int row = __shfl_sync(0xffffffffu, feed.r, 2 * (u - ub) + k);
+            if (blk[k]) blk[k] += (int64_t)row * kBlockTokens * token + (int64_t)kvh * (D * 2) + c * 16;
+          }
+          auto copy = [&](uint8_t* dst, int64_t off, uint64_t* full) {
+#pragma unroll
+            for (int p = 0; p < kTile / TPP; ++p) {
+              const int tok = p * TPP + tk;
+              const uint8_t* from = blk[p * TPP / 32];
+              const bool ok = from && ((p * TPP < 32 ? live.x : live.y) >> (tok & 31) & 1u);
+              cp_async16(smem_u32(dst) + swizzled(tok, c, kTile * 128),
+                         ok ? from + off + (tok & 31) * token : reinterpret_cast<const uint8_t*>(P.a.q), ok, policy);
+            }
+            cp_async_arrive(full);
+          };
+          if (kround > 0) wait_or_die(&sm.k_empty[kslot], (kround - 1) & 1, dead, err);
+          copy(ks + kslot * L::kSlot, 0, &sm.k_full[kslot]);
+          if (++kslot == L::kK) kslot = 0, ++kround;
+          if (vround > 0) wait_or_die(&sm.v_empty[vslot], (vround - 1) & 1, dead, err);
+          copy(vs + vslot * L::kSlot, v_off, &sm.v_full[vslot]);
+          if (++vslot == L::kV) vslot = 0, ++vround;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // --------------------------------------------------------------- expansion
+    const int w = warp - kFeeder0 / 32;
+    const int hkv = P.a.lv.hkv;
+    const int64_t slab_rows = (int64_t)P.a.lv.slab_blocks * kBlockTokens * hkv;
+    const int krow = P.a.lv.row_bytes[0], vrow = P.a.lv.row_bytes[1], mrow = P.a.lv.row_bytes[2];
+    const int64_t v_off = slab_rows * krow, km_off = v_off + slab_rows * vrow, vm_off = km_off + slab_rows * mrow;
+    const int units = D * (P.kbits + P.vbits) / 64;
+    const int pieces = w < units ? (units - w + L::kWarps - 1) / L::kWarps : 0;  // of this warp
+    // The loads run a tile ahead of the expansion, across segments: a walk of their own.
+    Walk lw = walk;
+    Segment ls = {};
+    Feed feed;
+    int lu = 0, lub = 0;  // next tile to load, first tile of the looked-up ones
+    const uint8_t *b0 = nullptr, *b1 = nullptr;  // the tile's blocks: the kv head's first key row
+    int64_t first0 = 0, first1 = 0;
+    uint2 live = make_uint2(0, 0);
+    uint4 code[L::kPieces];
+    float2 so[L::kPieces];
+    bool more = true;
+    // The next tile's blocks and tokens; a new segment where the last one ended.
+    auto ahead = [&] {
+      if (lu == ls.k1) {
+        more = more && lw.next(P, ls);
+        if (!more) return;
+        lu = lub = ls.k0;
+        feed.see(P, ls);
+        feed.look_up(P, ls, lub);
+        Feed::prefetch(P, ls, 2 * lub + 2, ls.x / P.n_rt, w, L::kWarps);
+      } else if (lu - lub == 16) {
+        lub = lu;
+        feed.look_up(P, ls, lub);
+      } else if (lu - lub == 8) {
+        Feed::prefetch(P, ls, 2 * lub + 34, ls.x / P.n_rt, w, L::kWarps);
+      }
+      live = feed.tokens(P, ls, lu);
+      const int at = 2 * (lu - lub);
+      b0 = lane_ptr(feed.base, at);
+      b1 = lane_ptr(feed.base, at + 1);
+      first0 = (int64_t)__shfl_sync(0xffffffffu, feed.r, at) * kBlockTokens * hkv + ls.x / P.n_rt;
+      first1 = (int64_t)__shfl_sync(0xffffffffu, feed.r, at + 1) * kBlockTokens * hkv + ls.x / P.n_rt;
+      ++lu;
+    };
+    auto load = [&](int p, uint4& c, float2& m) {
+      const Piece<D> pc(P, w + L::kWarps * p);
+      const bool second = pc.token >= 32;
+      const uint8_t* base = second ? b1 : b0;
+      const bool ok = base && ((second ? live.y : live.x) >> (pc.token & 31) & 1u);
+      const int64_t row = (second ? first1 : first0) + (int64_t)(pc.token & 31) * hkv;
+      const int bits = pc.key ? P.kbits : P.vbits;
+      c = make_uint4(0, 0, 0, 0);
+      m = make_float2(0.f, 0.f);
+      if (ok) {
+        c = *reinterpret_cast<const uint4*>(base + (pc.key ? 0 : v_off) + row * (pc.key ? krow : vrow) + pc.value * bits / 8);
+        m = *reinterpret_cast<const float2*>(base + (pc.key ? km_off : vm_off) + row * mrow + pc.value / P.a.group * 8);
+      }
+    };
+    ahead();
+    if (more) {
+#pragma unroll
+      for (int p = 0; p < L::kPieces; ++p)
+        if (p < pieces) load(p, code[p], so[p]);
+    }
+    uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
+    int taken = 0;
+    while (walk.next(P, seg)) {
+      for (int u = seg.k0; u < seg.k1; ++u, ++taken) {
+        ahead();
+        if (kround > 0) wait_or_die(&sm.k_empty[kslot], (kround - 1) & 1, dead, err);
+        uint8_t *kd = ks + kslot * L::kSlot, *vd = vs + vslot * L::kSlot;
+        bool keys = true;  // the pieces so far are keys
+        auto keys_done = [&] {
+          fence_async_shared();
+          mbar_arrive(&sm.k_full[kslot]);
+          if (vround > 0) wait_or_die(&sm.v_empty[vslot], (vround - 1) & 1, dead, err);
+          keys = false;
+        };
+#pragma unroll
+        for (int p = 0; p < L::kPieces; ++p) {
+          if (p < pieces) {
+            const Piece<D> pc(P, w + L::kWarps * p);
+            const uint4 c = code[p];
+            const float2 o = so[p];
+            if (more) load(p, code[p], so[p]);
+            if (pc.key) {
+              // the token's largest value, over the lanes that hold its pieces
+              const int hb = P.kbits == 4 ? 2 : 4, tpu = 32 / (hb * (D / 64));
+              float mx = fmaxf(fabsf(o.y), fabsf(fmaf(o.x, P.kbits == 4 ? 15.f : 255.f, o.y)));
+              for (int off = 1; off < hb; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              for (int off = hb * tpu; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+              const int ex = max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+              const float f = pow2(-ex);
+              if (pc.value == 0) sm.tok[taken % kTokRing][pc.token] = P.a.scale_log2 * pow2(ex);
+              if (P.kbits == 4)
+                expand<4, true>(c, o.x * f, o.y * f, kd, pc.token, pc.value);
+              else
+                expand<8, true>(c, o.x * f, o.y * f, kd, pc.token, pc.value);
+            } else {
+              if (keys) keys_done();
+              if (P.vbits == 4)
+                expand<4, false>(c, o.x, o.y, vd, pc.token, pc.value);
+              else
+                expand<8, false>(c, o.x, o.y, vd, pc.token, pc.value);
+            }
+          }
+        }
+        if (keys) keys_done();
+        fence_async_shared();
+        mbar_arrive(&sm.v_full[vslot]);
+        if (++kslot == L::kK) kslot = 0, ++kround;
+        if (++vslot == L::kV) vslot = 0, ++vround;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tc_dealloc(tmem, 512);
+}
+
+template <int D, int MODE, bool PACKED>
+cudaError_t launch(const Params& P) {
+  using L = Plan<D, MODE, PACKED>;
+  static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is set
+  return tc_launch(tree_attn_kernel<D, MODE, PACKED>, dim3((unsigned)P.a.ctas), L::kThreads, (size_t)L::kSmem, P.a.stream, P,
+                   P.a.device, &raised);
+}
+
+template <bool PACKED>
+cudaError_t launch_mode(const Params& P, int mode) {
+  if (P.a.D == 256) return launch<256, kSolo, PACKED>(P);
+  if (P.a.D == 128) return mode == kPair ? launch<128, kPair, PACKED>(P) : launch<128, kTurns, PACKED>(P);
+  return mode == kPair ? launch<64, kPair, PACKED>(P) : launch<64, kTurns, PACKED>(P);
+}
+
+}  // namespace tree
+
+// The attention kernel, defined in tree_bf16.cu and tree_packed.cu.
+cudaError_t launch_tree_bf16(const tree::Params& P, int mode);
+cudaError_t launch_tree_packed(const tree::Params& P, int mode);
+
+}  // namespace pkv
