@@ -131,13 +131,17 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a) {
   P.n_rt = g.n_rt;
   P.rec_rows = g.rec_rows;
   P.words = (a.n_q + 31) / 32;
-  const FormatBits fb = format_bits(a.fmt);
-  P.kbits = fb.k;
-  P.vbits = fb.v;
+  P.group_log = a.group == kGroupWide ? 6 : 5;
   P.meta = reinterpret_cast<int2*>(a.ws);
   P.ml = reinterpret_cast<float2*>((uint8_t*)a.ws + g.ml);
   P.acc = reinterpret_cast<float*>((uint8_t*)a.ws + g.acc);
-  const cudaError_t e = a.fmt == PKV_FMT_BF16 ? launch_tree_bf16(P, g.mode) : launch_tree_packed(P, g.mode);
+  cudaError_t e;
+  switch (a.fmt) {
+    case PKV_FMT_BF16: e = launch_tree_bf16(P, g.mode); break;
+    case PKV_FMT_K4V4: e = launch_tree_k4v4(P, g.mode); break;
+    case PKV_FMT_K8V4: e = launch_tree_k8v4(P, g.mode); break;
+    default: e = launch_tree_k8v8(P, g.mode); break;
+  }
   if (e != cudaSuccess) return e;
   return a.D == 64 ? tree::merge<64>(P) : a.D == 128 ? tree::merge<128>(P) : tree::merge<256>(P);
 }

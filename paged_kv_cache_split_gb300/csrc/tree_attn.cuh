@@ -21,10 +21,12 @@
 //
 // bf16 keys and values go from the pool to swizzled operand tiles by 16-byte asynchronous
 // copies, which fill tokens that nobody sees (past the length, unused drafts) with zeros: a
-// stale NaN reaches neither product.  Packed ones are expanded to operands by seven warps, whose
-// threads hold the next tile's codes in registers while they expand this one's (the tiles behind
-// it are on their way to L2): keys to fp16, each token's under the power of two that puts its
-// largest value near 2^13 (put back into the logits), values to bf16, whose range needs none.
+// stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by eight warps,
+// each token's keys and its values under the power of two that puts its largest near 2^13.  The
+// keys' power goes back into the logits.  The values' e_t goes into the probabilities' exponent,
+// P[t] = exp2(x[t] + e_t - m), so that O needs nothing (the reference follows x + e) and the sum
+// takes P[t] 2^-e_t: any magnitudes fit, and what fp16 drops of P is below 2^-25 of the largest
+// contribution to O.
 //
 // The key tiles of all units (sequence, kv head, 128 or 256 rows) are laid end to end and split
 // evenly in cost over the CTAs, one a SM.  A unit inside one CTA's share is written directly; a
@@ -44,24 +46,31 @@ enum Mode { kTurns = 0, kPair = 1, kSolo = 2 };
 
 constexpr int kTile = 64;               // tokens a tile
 constexpr int kRows = 128;              // rows a tile of rows
-// Warps 0..7: softmax; 8: MMAs; from 9 on: keys and values (feeders).
+// Warps 0..7: softmax; 8: MMAs; the last ones: keys and values (feeders).
 constexpr int kSoftmaxThreads = 256;
-constexpr int kFeeder0 = 288;           // the first feeder thread
 constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
 constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
 constexpr int kTokRing = 8;             // tiles whose keys' powers are held (see Small::tok)
+
+// Packed: the five warpgroups share the launch's registers, 2 x 128 + 48 + 2 x 88 = 5 x 96 (the
+// launcher checks that the kernel was built with 96).  Their paths do not rejoin: each ends in a
+// return.
+constexpr int kLaunchRegs = 96;
 
 // Cost of a unit's start in the split over the CTAs, in quarter tiles: its queries are loaded
 // and its output or record written.
 constexpr int kSegCost = 16;
 constexpr int kCost = 4;
 
-template <int D, int MODE, bool PACKED>
+template <int D, int MODE, int KB, int VB>
 struct Plan {
-  // Packed: seven warps, so that the launch has 16 and a thread 128 registers.
-  static constexpr int kWarps = PACKED ? 7 : 4;
+  static constexpr bool PACKED = KB < 16;
+  // Packed: two warpgroups of feeders, so that each warp has the same few pieces of every tile
+  // (warps 9..11 fill the MMA warp's warpgroup).
+  static constexpr int kWarps = PACKED ? 8 : 4;
   static constexpr int kFeeders = kWarps * 32;
+  static constexpr int kFeeder0 = PACKED ? 384 : 288;  // the first feeder thread
   static constexpr int kThreads = kFeeder0 + kFeeders;
   static constexpr int kTileRows = MODE == kPair ? 2 * kRows : kRows;  // rows a unit
   static constexpr int kQBytes = kTileRows * D * 2;
@@ -69,9 +78,7 @@ struct Plan {
   static constexpr int kK = D == 256 ? 2 : PACKED ? 4 : D == 64 ? 8 : 5;
   static constexpr int kV = D == 256 ? 2 : PACKED || D == 128 ? 4 : 8;
   static constexpr int kLag = MODE == kTurns ? 2 : 1;  // tiles between a tile's S and its values
-  // Packed: pieces a feeder thread takes of a tile, at most (8-bit keys and values).
-  static constexpr int kPieces = PACKED ? (D / 4 + kWarps - 1) / kWarps : 0;
-  static constexpr int kSmall = 8 * 1024;
+  static constexpr int kSmall = 12 * 1024;
   static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kSlot + kSmall;
   static_assert(kSmem <= kSmemLimit, "shared memory");
   static_assert(!PACKED || kK + kLag + 1 <= kTokRing, "a tile's powers are read until its softmax is done");
@@ -86,7 +93,7 @@ struct Params {
   int n_rt;      // units a (sequence, kv head)
   int rec_rows;  // rows a record
   int words;     // mask words a query
-  int kbits, vbits;
+  int group_log; // packed: log2 of the values a group
   int2* meta;    // [B * hkv * n_rt]: first CTA of a split unit (-1: written directly), last CTA
   float2* ml;    // [2 * grid][rec_rows]: reference and sum of a record's rows
   float* acc;    // [2 * grid][rec_rows][D]
@@ -196,15 +203,16 @@ __device__ __forceinline__ Walk start_walk(const Params& P) {
 struct Small {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // by slot
   uint64_t s_full[2][2], p_full[2][2];                    // by warpgroup and buffer
-  uint64_t pv_done[2], q_full, q_empty, drain;
+  uint64_t pv_done[2], q_full, q_empty, drain, done;
   Walk walk;
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
   float m[2][kRows], l[2][kRows];  // the warpgroups' references and sums of shared rows
   float q_pow[2 * kRows];      // packed: the power of two that a row's query was divided by
-  // Packed: scale times the power of two that a token's key was divided by.  A tile's are
-  // overwritten kTokRing tiles later, when its softmax has long handed its P over.
-  float tok[kTokRing][kTile];
+  // Packed, by token of a tile: scale times the power of two that its key was divided by; log2
+  // of the one its value was divided by, and the inverse of that.  A tile's are overwritten
+  // kTokRing tiles later, when its softmax has long handed its P over.
+  alignas(16) float tok[kTokRing][kTile], v_log[kTokRing][kTile], v_inv[kTokRing][kTile];
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t policy) {
@@ -329,11 +337,37 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t col) {
   return (uint32_t)(c >> 3) * col + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
 }
 
+// 4-bit codes are expanded two at a time, i and i + 4 of each eight values: an operand row holds
+// them in the order 0 4 1 5 2 6 3 7.  A warp's row of fp16 values (E a lane) into that order:
+template <int E>
+__device__ __forceinline__ void octets(uint32_t (&w)[E / 2]) {
+  const int lane = threadIdx.x & 31;
+  auto lows = [](uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); };
+  auto highs = [](uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); };
+  if constexpr (E == 2) {
+    const int j = lane & 3, from = (lane & ~3) + (j >> 1);
+    const uint32_t a = __shfl_sync(0xffffffffu, w[0], from), b = __shfl_sync(0xffffffffu, w[0], from + 2);
+    w[0] = j & 1 ? highs(a, b) : lows(a, b);
+  } else if constexpr (E == 4) {
+    const bool odd = lane & 1;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+    const uint32_t a = odd ? got : w[0], b = odd ? w[1] : got;
+    w[0] = lows(a, b);
+    w[1] = highs(a, b);
+  } else {
+    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+    w[0] = lows(a, c), w[1] = highs(a, c), w[2] = lows(b, d), w[3] = highs(b, d);
+  }
+}
+// Where column c of an operand made from BITS-bit codes lies among its values, and the inverse.
+__host__ __device__ constexpr int octet_column(int c) { return (c & ~7) | (c & 3) << 1 | (c & 4) >> 2; }
+
 // Queries of a unit's rows into shared memory, a row a warp at a time; packed: into the keys'
 // basis, under a power of two in fp16.
-template <int D, bool PACKED>
+template <int D, int KB>
 __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, Small& sm, int row0, int nrow) {
   constexpr int E = D / 32;
+  constexpr bool PACKED = KB < 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = s.x / P.n_rt;
   float sign[E];
@@ -396,6 +430,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
 #pragma unroll
         for (int e = 0; e < E; e += 2) w[u][e / 2] = fp16x2(x[e] * f, x[e + 1] * f);
         if (lane == 0) sm.q_pow[r] = pow2(ex);
+        if constexpr (KB == 4) octets<E>(w[u]);
       }
       const int byte = lane * E * 2, tile = r / kRows, rr = r % kRows;
       uint8_t* dst = qs + tile * (kRows * D * 2) + swizzled(rr, byte / 16, kRows * 128) + byte % 16;
@@ -409,70 +444,87 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
   }
 }
 
-// A packed tile's pieces (16 bytes of codes with their group's scale and offset) over the
-// feeder warps: unit g of 32 pieces goes to warp g % 7, keys first.  Within a unit the lanes
-// are laid out so that eight of them write operand pieces to eight different bank groups.
-template <int D>
-struct Piece {
-  int token, value;  // its token in the tile and first value
-  bool key;
-  __device__ __forceinline__ Piece(const Params& P, int g) {
+// A packed tile's pieces (16 bytes of codes with their group's scale and offset) of one kind,
+// in units of 32: `kTokens` tokens by D values.  The lanes are laid out so that eight of them
+// write operand pieces to eight different bank groups.
+template <int D, int BITS>
+struct Pieces {
+  static constexpr int kUnits = D * BITS / 64;      // units a tile
+  static constexpr int kCol = BITS == 4 ? 2 : 4;    // pieces of 64 values
+  static constexpr int kTokens = 32 / (kCol * (D / 64));
+  int token, value;          // this lane's token of the unit, its piece's first value
+  uint32_t code_at, meta_at;      // their bytes in a slab, from the unit's first token on
+  uint32_t code_row, meta_row;    // bytes from head to head
+  uint32_t code_step, meta_step;  // bytes from token to token
+  // `code_off`, `meta_off`: where the kind's two tensors lie in a slab (below 2^32 bytes)
+  __device__ __forceinline__ Pieces(int hkv, int row_bytes, int meta_bytes, uint32_t code_off, uint32_t meta_off, int group_log) {
     const int lane = threadIdx.x & 31;
-    const int ku = D * P.kbits / 64;
-    key = g < ku;
-    const int bits = key ? P.kbits : P.vbits, hb = bits == 4 ? 2 : 4;  // pieces of 64 values
-    const int tpu = 32 / (hb * (D / 64));
-    token = (key ? g : g - ku) * tpu + lane / hb % tpu;
-    value = lane / (hb * tpu) * 64 + lane % hb * (64 / hb);
+    token = lane / kCol % kTokens;
+    value = lane / (kCol * kTokens) * 64 + lane % kCol * (64 / kCol);
+    code_row = (uint32_t)row_bytes;
+    meta_row = (uint32_t)meta_bytes;
+    code_step = (uint32_t)(hkv * row_bytes);
+    meta_step = (uint32_t)(hkv * meta_bytes);
+    code_at = code_off + (uint32_t)token * code_step + (uint32_t)(value * BITS / 8);
+    meta_at = meta_off + (uint32_t)token * meta_step + (uint32_t)(value >> group_log) * 8u;
+  }
+  // unit g of a tile, one of whose blocks it lies in: `row` is that block's first row of the head
+  __device__ __forceinline__ void load(const uint8_t* slab, uint32_t row, int g, uint32_t live, uint4& c, float2& m) const {
+    const uint32_t t0 = (uint32_t)(g * kTokens) & 31u;
+    c = make_uint4(0, 0, 0, 0);
+    m = make_float2(0.f, 0.f);
+    if (live >> (t0 + token) & 1u) {
+      c = *reinterpret_cast<const uint4*>(slab + (row * code_row + t0 * code_step + code_at));
+      m = *reinterpret_cast<const float2*>(slab + (row * meta_row + t0 * meta_step + meta_at));
+    }
+  }
+  // log2 of the power of two that puts the token's largest magnitude near 2^13, from the scales and
+  // offsets of the lanes that hold its pieces
+  __device__ __forceinline__ static int power(const float2& m) {
+    float mx = fmaxf(fabsf(m.y), fabsf(fmaf(m.x, (float)((1 << BITS) - 1), m.y)));
+#pragma unroll
+    for (int off = 1; off < kCol; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll
+    for (int off = kCol * kTokens; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    return max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
   }
 };
 
-// Eight 4-bit codes to floats, in order.
-__device__ __forceinline__ void codes4(uint32_t w, float (&c)[8]) {
-  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[2 * i] = __uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7540 | i)) - 8388608.f;
-    c[2 * i + 1] = __uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7540 | i)) - 8388608.f;
-  }
-}
-__device__ __forceinline__ void codes8(uint32_t w, float (&c)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | i)) - 8388608.f;
-}
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// Codes of a piece as operand pieces: s c + o, in fp16 (keys) or bf16.
-template <int BITS, bool KEY>
+// Codes of a piece as operand pieces in fp16: s c + o, s and o rounded to fp16, one rounding
+// for the rest.  A code under a fitting exponent is 1024 + c (or 64 + c, four bits up), exactly.
+template <int BITS>
 __device__ __forceinline__ void expand(const uint4& code, float s, float o, uint8_t* slot, int token, int value) {
   const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+  const __half2 ss = __float2half2_rn(s), oo = __float2half2_rn(o);
+  const __half2 k1024 = half2_of(0x64006400u), k64 = half2_of(0x54005400u);
   constexpr int N = BITS == 4 ? 4 : 2;  // operand pieces of eight values
-  const uint64_t ss = pair2(s, s), oo = pair2(o, o);
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    float c[8];
-    if constexpr (BITS == 4) {
-      codes4(w[q], c);
-    } else {
-      float a[4], b[4];
-      codes8(w[2 * q], a);
-      codes8(w[2 * q + 1], b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = a[i], c[4 + i] = b[i];
-    }
     uint32_t out[4];
+    if constexpr (BITS == 4) {
+      // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+      const uint32_t lo = w[q], hi = w[q] >> 8;
+      out[0] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x000f000fu) | 0x64006400u), k1024), ss, oo));
+      out[1] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x00f000f0u) | 0x54005400u), k64), ss, oo));
+      out[2] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x000f000fu) | 0x64006400u), k1024), ss, oo));
+      out[3] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x00f000f0u) | 0x54005400u), k64), ss, oo));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x, y;
-      split2(fma2(pair2(c[2 * i], c[2 * i + 1]), ss, oo), x, y);
-      out[i] = KEY ? fp16x2(x, y) : bf2(x, y);
+      for (int i = 0; i < 4; ++i)
+        out[i] = bits_of(__hfma2(
+            __hsub2(half2_of(__byte_perm(w[2 * q + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), k1024), ss, oo));
     }
     *reinterpret_cast<uint4*>(slot + swizzled(token, value / 8 + q, kTile * 128)) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
-template <int D, int MODE, bool PACKED>
-__global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_kernel(const __grid_constant__ Params P) {
-  using L = Plan<D, MODE, PACKED>;
+template <int D, int MODE, int KB, int VB>
+__global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_kernel(const __grid_constant__ Params P) {
+  using L = Plan<D, MODE, KB, VB>;
+  constexpr bool PACKED = L::PACKED;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* qs = smem;
@@ -498,6 +550,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
     mbar_init(&sm.q_full, kSoftmaxThreads);
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.drain, 1);
+    mbar_init(&sm.done, kSoftmaxThreads);
     sm.dead = 0;
     fence_mbar_init();
   }
@@ -523,6 +576,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
+    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int tr = (warp & 3) * 32 + lane;  // row of the tile
@@ -532,7 +586,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
       const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = min(L::kTileRows, P.rows - row0);
       const int kvh = seg.x / P.n_rt;
       if (n_seg > 0) wait_or_die(&sm.q_empty, (n_seg - 1) & 1, dead, err);
-      load_queries<D, PACKED>(P, seg, qs, sm, row0, nrow);
+      load_queries<D, KB>(P, seg, qs, sm, row0, nrow);
       fence_async_shared();
       mbar_arrive(&sm.q_full);
       __syncwarp();
@@ -552,6 +606,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
         if (!works(t, it, nrow)) continue;
         const int job = jobs[t]++, buf = job & 1;
         wait_or_die(&sm.s_full[t][buf], (job >> 1) & 1, dead, err);
+        // the values' powers are written with them
+        if constexpr (PACKED) wait_or_die(&sm.v_full[it % L::kV], (it / L::kV) & 1, dead, err);
         if (!idle) {
           tc_fence_after();
           float x[kTile];
@@ -565,10 +621,16 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
           }
 #pragma unroll
           for (int c = 0; c < kTile; c += 4) {
-            float4 f = make_float4(P.a.scale_log2, P.a.scale_log2, P.a.scale_log2, P.a.scale_log2);
-            if constexpr (PACKED) f = *reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][c]);
-            split2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), x[c], x[c + 1]);
-            split2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), x[c + 2], x[c + 3]);
+            if constexpr (PACKED) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][c]);
+              const float4 e = *reinterpret_cast<const float4*>(&sm.v_log[it % kTokRing][c]);
+              split2(fma2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), qp2, pair2(e.x, e.y)), x[c], x[c + 1]);
+              split2(fma2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), qp2, pair2(e.z, e.w)), x[c + 2], x[c + 3]);
+            } else {
+              const uint64_t f = pair2(P.a.scale_log2, P.a.scale_log2);
+              split2(mul2(pair2(x[c], x[c + 1]), f), x[c], x[c + 1]);
+              split2(mul2(pair2(x[c + 2], x[c + 3]), f), x[c + 2], x[c + 3]);
+            }
           }
           if ((u + 1) * kTile > seg.len - P.a.n_q) {
             const int j0 = u * kTile - (seg.len - P.a.n_q);
@@ -589,7 +651,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
           // rows past the unit's hold anything: they must not move the references of this warp's others
-          const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * qp : -INFINITY;
+          const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) : -INFINITY;
           if (__any_sync(0xffffffffu, top - m > kSlack)) {
             const float mn = fmaxf(m, rintf(top));
             const float f = ex2(m - mn);
@@ -618,13 +680,18 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               float e0, e1;
-              const uint64_t xx = pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
-              split2(PACKED ? fma2(xx, qp2, mm) : add2(xx, mm), e0, e1);
+              split2(add2(pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]), mm), e0, e1);
               e0 = ex2(e0);
               e1 = ex2(e1);
               uint64_t& s = c & 1 ? sum1 : sum0;
-              s = add2(s, pair2(e0, e1));
-              w[c] = bf2(e0, e1);
+              if constexpr (PACKED) {
+                const float2 f = *reinterpret_cast<const float2*>(&sm.v_inv[it % kTokRing][32 * q + 2 * c]);
+                s = fma2(pair2(e0, e1), pair2(f.x, f.y), s);
+                w[c] = fp16x2(e0, e1);
+              } else {
+                s = add2(s, pair2(e0, e1));
+                w[c] = bf2(e0, e1);
+              }
             }
             tc_st_rows<16>(tm_s(t, buf) + 16 * q + lanes, w);
           }
@@ -698,6 +765,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = fmaf(__uint_as_float(a[c]), f[1], o[c]);
           }
+          if constexpr (VB == 4) {
+            float y[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) y[c] = o[octet_column(c)];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = y[c];
+          }
           if (mine && whole) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -714,10 +788,15 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
       __syncwarp();
       tc_fence_before();
     }
-  } else if (warp == 8) {
+    mbar_arrive(&sm.done);
+    return;
+  }
+  if (warp < L::kFeeder0 / 32) {
     // -------------------------------------------------------------------- MMAs
+    if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp > 8) return;
     constexpr uint32_t id_s = tc_idesc(kRows, kTile, false, false, PACKED);
-    constexpr uint32_t id_o = tc_idesc(kRows, D, false, true);
+    constexpr uint32_t id_o = tc_idesc(kRows, D, false, true, PACKED);
     const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ks), 16, 1024);
     const uint64_t d_v = tc_desc(smem_u32(vs), kTile * 128, 1024);
     int it = 0, n_seg = 0, jobs[2] = {0, 0}, done[2] = {0, 0};
@@ -789,11 +868,18 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
     __syncwarp();
     if (elect_one()) tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
     mbar_wait_bounded(&sm.drain, 0, err);
-  } else if constexpr (!PACKED) {
+    __syncwarp();
+    mbar_wait_bounded(&sm.done, 0, err);  // the softmax warps have read their last column
+    tc_fence_after();
+    __syncwarp();
+    tc_dealloc(tmem, 512);
+    return;
+  }
+  if constexpr (!PACKED) {
     // ------------------------------------------------------------------ copies
     constexpr int CPT = D / 8;                  // 16-byte pieces of a token's row
     constexpr int TPP = L::kFeeders / CPT;      // tokens a pass
-    const int tid = threadIdx.x - kFeeder0;
+    const int tid = threadIdx.x - L::kFeeder0;
     const int c = tid % CPT, tk = tid / CPT;
     const uint64_t policy = P.n_rt == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
     const int64_t v_off = (int64_t)P.a.lv.slab_blocks * kBlockTokens * P.a.lv.hkv * (D * 2);  // a slab's values follow its keys
@@ -838,144 +924,147 @@ __global__ void __launch_bounds__(Plan<D, MODE, PACKED>::kThreads, 1) tree_attn_
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // --------------------------------------------------------------- expansion
-    const int w = warp - kFeeder0 / 32;
-    const int hkv = P.a.lv.hkv;
-    const int64_t slab_rows = (int64_t)P.a.lv.slab_blocks * kBlockTokens * hkv;
-    const int krow = P.a.lv.row_bytes[0], vrow = P.a.lv.row_bytes[1], mrow = P.a.lv.row_bytes[2];
-    const int64_t v_off = slab_rows * krow, km_off = v_off + slab_rows * vrow, vm_off = km_off + slab_rows * mrow;
-    const int units = D * (P.kbits + P.vbits) / 64;
-    const int pieces = w < units ? (units - w + L::kWarps - 1) / L::kWarps : 0;  // of this warp
-    // The loads run a tile ahead of the expansion, across segments: a walk of their own.
-    Walk lw = walk;
-    Segment ls = {};
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const LayerView& lv = P.a.lv;
+    const uint32_t slab_rows = (uint32_t)(lv.slab_blocks * kBlockTokens * lv.hkv);
+    const uint32_t v_off = slab_rows * lv.row_bytes[0], km_off = v_off + slab_rows * lv.row_bytes[1],
+                   vm_off = km_off + slab_rows * lv.row_bytes[2];
+    using KP = Pieces<D, KB>;
+    using VP = Pieces<D, VB>;
+    const KP kp(lv.hkv, lv.row_bytes[0], lv.row_bytes[2], 0, km_off, P.group_log);
+    const VP vp(lv.hkv, lv.row_bytes[1], lv.row_bytes[2], v_off, vm_off, P.group_log);
+    // Unit j of the keys goes to warp j % 8, the values' units to the warps from there on.
+    constexpr int W = L::kWarps, KN = (KP::kUnits + W - 1) / W, VN = (VP::kUnits + W - 1) / W;
+    const int kw = warp - L::kFeeder0 / 32, vw = (kw - KP::kUnits % W + W) % W;
     Feed feed;
-    int lu = 0, lub = 0;  // next tile to load, first tile of the looked-up ones
-    const uint8_t *b0 = nullptr, *b1 = nullptr;  // the tile's blocks: the kv head's first key row
-    int64_t first0 = 0, first1 = 0;
+    int lu = 0, lub = 0;       // next tile to load, first tile of the looked-up ones
+    const uint8_t *slab0 = nullptr, *slab1 = nullptr;  // the tile's blocks' slabs, and their rows there
+    uint32_t row0 = 0, row1 = 0;
     uint2 live = make_uint2(0, 0);
-    uint4 code[L::kPieces];
-    float2 so[L::kPieces];
+    seg.k1 = 0;
     bool more = true;
     // The next tile's blocks and tokens; a new segment where the last one ended.
-    auto ahead = [&] {
-      if (lu == ls.k1) {
-        more = more && lw.next(P, ls);
+    auto next_tile = [&] {
+      if (lu == seg.k1) {
+        more = more && walk.next(P, seg);
         if (!more) return;
-        lu = lub = ls.k0;
-        feed.see(P, ls);
-        feed.look_up(P, ls, lub);
-        Feed::prefetch(P, ls, 2 * lub + 2, ls.x / P.n_rt, w, L::kWarps);
+        lu = lub = seg.k0;
+        feed.see(P, seg);
+        feed.look_up(P, seg, lub);
+        Feed::prefetch(P, seg, 2 * lub + 2, seg.x / P.n_rt, kw, W);
       } else if (lu - lub == 16) {
         lub = lu;
-        feed.look_up(P, ls, lub);
+        feed.look_up(P, seg, lub);
       } else if (lu - lub == 8) {
-        Feed::prefetch(P, ls, 2 * lub + 34, ls.x / P.n_rt, w, L::kWarps);
+        Feed::prefetch(P, seg, 2 * lub + 34, seg.x / P.n_rt, kw, W);
       }
-      live = feed.tokens(P, ls, lu);
-      const int at = 2 * (lu - lub);
-      b0 = lane_ptr(feed.base, at);
-      b1 = lane_ptr(feed.base, at + 1);
-      first0 = (int64_t)__shfl_sync(0xffffffffu, feed.r, at) * kBlockTokens * hkv + ls.x / P.n_rt;
-      first1 = (int64_t)__shfl_sync(0xffffffffu, feed.r, at + 1) * kBlockTokens * hkv + ls.x / P.n_rt;
+      live = feed.tokens(P, seg, lu);
+      const int at = 2 * (lu - lub), kvh = seg.x / P.n_rt;
+      slab0 = lane_ptr(feed.base, at);
+      slab1 = lane_ptr(feed.base, at + 1);
+      row0 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, at) * kBlockTokens * lv.hkv + kvh);
+      row1 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, at + 1) * kBlockTokens * lv.hkv + kvh);
+      if (!slab0) live.x = 0;
+      if (!slab1) live.y = 0;
       ++lu;
     };
-    auto load = [&](int p, uint4& c, float2& m) {
-      const Piece<D> pc(P, w + L::kWarps * p);
-      const bool second = pc.token >= 32;
-      const uint8_t* base = second ? b1 : b0;
-      const bool ok = base && ((second ? live.y : live.x) >> (pc.token & 31) & 1u);
-      const int64_t row = (second ? first1 : first0) + (int64_t)(pc.token & 31) * hkv;
-      const int bits = pc.key ? P.kbits : P.vbits;
-      c = make_uint4(0, 0, 0, 0);
-      m = make_float2(0.f, 0.f);
-      if (ok) {
-        c = *reinterpret_cast<const uint4*>(base + (pc.key ? 0 : v_off) + row * (pc.key ? krow : vrow) + pc.value * bits / 8);
-        m = *reinterpret_cast<const float2*>(base + (pc.key ? km_off : vm_off) + row * mrow + pc.value / P.a.group * 8);
-      }
+    // A tile's pieces are loaded while the tile before is expanded.
+    uint4 kc[KN], vc[VN];
+    float2 km[KN], vm[VN];
+    auto load_key = [&](int j) {
+      const int g = kw + W * j;
+      if (KP::kUnits % W && g >= KP::kUnits) return;
+      const bool k = g * KP::kTokens >= 32;
+      kp.load(k ? slab1 : slab0, k ? row1 : row0, g, k ? live.y : live.x, kc[j], km[j]);
     };
-    ahead();
-    if (more) {
+    auto load_value = [&](int j) {
+      const int g = vw + W * j;
+      if (VP::kUnits % W && g >= VP::kUnits) return;
+      const bool k = g * VP::kTokens >= 32;
+      vp.load(k ? slab1 : slab0, k ? row1 : row0, g, k ? live.y : live.x, vc[j], vm[j]);
+    };
+    next_tile();
+    bool have = more;
+    if (have) {
 #pragma unroll
-      for (int p = 0; p < L::kPieces; ++p)
-        if (p < pieces) load(p, code[p], so[p]);
+      for (int j = 0; j < KN; ++j) load_key(j);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) load_value(j);
     }
     uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
-    int taken = 0;
-    while (walk.next(P, seg)) {
-      for (int u = seg.k0; u < seg.k1; ++u, ++taken) {
-        ahead();
-        if (kround > 0) wait_or_die(&sm.k_empty[kslot], (kround - 1) & 1, dead, err);
-        uint8_t *kd = ks + kslot * L::kSlot, *vd = vs + vslot * L::kSlot;
-        bool keys = true;  // the pieces so far are keys
-        auto keys_done = [&] {
-          fence_async_shared();
-          mbar_arrive(&sm.k_full[kslot]);
-          if (vround > 0) wait_or_die(&sm.v_empty[vslot], (vround - 1) & 1, dead, err);
-          keys = false;
-        };
+    for (int it = 0; have; ++it) {
+      next_tile();
+      have = more;
+      if (kround > 0) wait_or_die(&sm.k_empty[kslot], (kround - 1) & 1, dead, err);
 #pragma unroll
-        for (int p = 0; p < L::kPieces; ++p) {
-          if (p < pieces) {
-            const Piece<D> pc(P, w + L::kWarps * p);
-            const uint4 c = code[p];
-            const float2 o = so[p];
-            if (more) load(p, code[p], so[p]);
-            if (pc.key) {
-              // the token's largest value, over the lanes that hold its pieces
-              const int hb = P.kbits == 4 ? 2 : 4, tpu = 32 / (hb * (D / 64));
-              float mx = fmaxf(fabsf(o.y), fabsf(fmaf(o.x, P.kbits == 4 ? 15.f : 255.f, o.y)));
-              for (int off = 1; off < hb; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-              for (int off = hb * tpu; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-              const int ex = max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
-              const float f = pow2(-ex);
-              if (pc.value == 0) sm.tok[taken % kTokRing][pc.token] = P.a.scale_log2 * pow2(ex);
-              if (P.kbits == 4)
-                expand<4, true>(c, o.x * f, o.y * f, kd, pc.token, pc.value);
-              else
-                expand<8, true>(c, o.x * f, o.y * f, kd, pc.token, pc.value);
-            } else {
-              if (keys) keys_done();
-              if (P.vbits == 4)
-                expand<4, false>(c, o.x, o.y, vd, pc.token, pc.value);
-              else
-                expand<8, false>(c, o.x, o.y, vd, pc.token, pc.value);
-            }
-          }
-        }
-        if (keys) keys_done();
-        fence_async_shared();
-        mbar_arrive(&sm.v_full[vslot]);
-        if (++kslot == L::kK) kslot = 0, ++kround;
-        if (++vslot == L::kV) vslot = 0, ++vround;
+      for (int j = 0; j < KN; ++j) {
+        const int g = kw + W * j;
+        if (KP::kUnits % W && g >= KP::kUnits) continue;
+        const uint4 c = kc[j];
+        const float2 m = km[j];
+        if (have) load_key(j);
+        const int ex = kp.power(m);
+        const float f = pow2(-ex);
+        const int token = g * KP::kTokens + kp.token;
+        if (kp.value == 0) sm.tok[it % kTokRing][token] = P.a.scale_log2 * pow2(ex);
+        expand<KB>(c, m.x * f, m.y * f, ks + kslot * L::kSlot, token, kp.value);
       }
+      fence_async_shared();
+      mbar_arrive(&sm.k_full[kslot]);
+      if (++kslot == L::kK) kslot = 0, ++kround;
+      if (vround > 0) wait_or_die(&sm.v_empty[vslot], (vround - 1) & 1, dead, err);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {
+        const int g = vw + W * j;
+        if (VP::kUnits % W && g >= VP::kUnits) continue;
+        const uint4 c = vc[j];
+        const float2 m = vm[j];
+        if (have) load_value(j);
+        const int ex = vp.power(m);
+        const float f = pow2(-ex);
+        const int token = g * VP::kTokens + vp.token;
+        if (vp.value == 0) {
+          sm.v_log[it % kTokRing][token] = (float)ex;
+          sm.v_inv[it % kTokRing][token] = f;
+        }
+        expand<VB>(c, m.x * f, m.y * f, vs + vslot * L::kSlot, token, vp.value);
+      }
+      fence_async_shared();
+      mbar_arrive(&sm.v_full[vslot]);
+      if (++vslot == L::kV) vslot = 0, ++vround;
     }
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 8) tc_dealloc(tmem, 512);
 }
 
-template <int D, int MODE, bool PACKED>
+template <int D, int MODE, int KB, int VB>
 cudaError_t launch(const Params& P) {
-  using L = Plan<D, MODE, PACKED>;
+  using L = Plan<D, MODE, KB, VB>;
+  if constexpr (L::PACKED) {
+    static const bool regs_ok = [] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, tree_attn_kernel<D, MODE, KB, VB>) == cudaSuccess && f.numRegs == kLaunchRegs;
+    }();
+    if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+  }
   static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is set
-  return tc_launch(tree_attn_kernel<D, MODE, PACKED>, dim3((unsigned)P.a.ctas), L::kThreads, (size_t)L::kSmem, P.a.stream, P,
+  return tc_launch(tree_attn_kernel<D, MODE, KB, VB>, dim3((unsigned)P.a.ctas), L::kThreads, (size_t)L::kSmem, P.a.stream, P,
                    P.a.device, &raised);
 }
 
-template <bool PACKED>
+// KB, VB: bits a key and a value (16: bf16).
+template <int KB, int VB>
 cudaError_t launch_mode(const Params& P, int mode) {
-  if (P.a.D == 256) return launch<256, kSolo, PACKED>(P);
-  if (P.a.D == 128) return mode == kPair ? launch<128, kPair, PACKED>(P) : launch<128, kTurns, PACKED>(P);
-  return mode == kPair ? launch<64, kPair, PACKED>(P) : launch<64, kTurns, PACKED>(P);
+  if (P.a.D == 256) return launch<256, kSolo, KB, VB>(P);
+  if (P.a.D == 128) return mode == kPair ? launch<128, kPair, KB, VB>(P) : launch<128, kTurns, KB, VB>(P);
+  return mode == kPair ? launch<64, kPair, KB, VB>(P) : launch<64, kTurns, KB, VB>(P);
 }
 
 }  // namespace tree
 
-// The attention kernel, defined in tree_bf16.cu and tree_packed.cu.
+// The attention kernel by format, defined in tree_*.cu.
 cudaError_t launch_tree_bf16(const tree::Params& P, int mode);
-cudaError_t launch_tree_packed(const tree::Params& P, int mode);
+cudaError_t launch_tree_k4v4(const tree::Params& P, int mode);
+cudaError_t launch_tree_k8v4(const tree::Params& P, int mode);
+cudaError_t launch_tree_k8v8(const tree::Params& P, int mode);
 
 }  // namespace pkv

@@ -3,6 +3,6 @@
 
 namespace pkv {
 
-cudaError_t launch_tree_bf16(const tree::Params& P, int mode) { return tree::launch_mode<false>(P, mode); }
+cudaError_t launch_tree_bf16(const tree::Params& P, int mode) { return tree::launch_mode<16, 16>(P, mode); }
 
 }  // namespace pkv

@@ -10,10 +10,14 @@ relative to the value, h = 2^-11 half an fp16 one):
   write, packed  the scale and offset are fp32 values of a row known to 2^-22 of its largest
                  value (2^-36 without the norm); a code is the nearest one of a quotient off by
                  the 2^-22 of top steps that the fp32 subtraction and division may lose;
-  tree           u |y| for the output, u sum p |v| for the probabilities' rounding, 2 d sum p
-                 |v| for the logits: d is D 2^-23 scale sum |q k| for the fp32 sums, and for
-                 packed pools 2 h scale sum |q k| for the two factors in fp16; their values add
-                 h sum p |v|, and what fp16 keeps of the smallest: 2^-24 of the largest.
+  tree           u |y| for the output, u sum p |v| for the probabilities' rounding (half of which
+                 goes to 16 bits at most), 2 d sum p |v| for the logits, d being D 2^-23 scale sum
+                 |q k| for the fp32 sums.  A packed value is c s + o with s and o rounded to fp16 and
+                 one rounding more: off by h (|c s| + |o| + |c s + o|) <= h (2 M + M + M) = 4 h M, M
+                 the largest magnitude of its group, as c s is at most the group's range.  So
+                 values add 4 h sum p M and keys 4 h scale sum |q| M to d, the queries' own rounding
+                 h scale sum |q| |k|; what fp16 drops altogether is 2^-24 of a token's largest, and
+                 of the largest contribution.
 The elementwise bounds are worst cases; a relative L2 bound holds the average: each
 rounding contributes at most u / sqrt(3) in the mean square, at most four of them with
 logits of unit size, so 2 u < 1e-2."""
@@ -390,16 +394,16 @@ class Case:
         self.pool.import_blocks(self.pool.config(), self.order, rec)
 
     def kv(self, b):
-        """[L, Hk, D] keys and values of sequence b in 64 bits, keys in the heads' own coordinates."""
+        """[L, Hk, D] keys and values of sequence b in 64 bits, and for a packed pool the largest
+        magnitude of each value's group; its keys are in the pool's basis."""
         L = self.lens[b]
         rows = self.table[b, :-(-L // 32)].contiguous()
         x = stored(self.pool, rows, self.layer)
         if self.fmt == "bf16":
-            k, v = (y.flatten(0, 1)[:L].double() for y in x)
-        else:
-            k = values(x[0], x[2]).flatten(0, 1)[:L] @ basis(self.D).t()
-            v = values(x[1], x[3]).flatten(0, 1)[:L]
-        return k, v
+            return [y.flatten(0, 1)[:L].double() for y in x] + [None, None]
+        k, v = (values(x[i], x[i + 2]).flatten(0, 1)[:L] for i in (0, 1))
+        return [k, v] + [y.abs().unflatten(-1, (x[2].shape[-2], -1)).amax(-1, keepdim=True).expand(
+            *y.shape[:-1], x[2].shape[-2], y.shape[-1] // x[2].shape[-2]).flatten(-2) for y in (k, v)]
 
 
 def random_tree(B, n_q, seed):
@@ -420,26 +424,30 @@ def reference(case, b, q, seen, scale):
     """(out, tolerance) of sequence b; q [n_q, Hq, D], seen [n_q, n_q]."""
     n_q, Hq, D = q.shape
     L, G = case.lens[b], Hq // case.Hk
-    k, v = case.kv(b)
+    k, v, km, vm = case.kv(b)
+    qd = q.double() if km is None else q.double() @ basis(D)
     vis = torch.ones(n_q, L, dtype=torch.bool, device="cuda")
     vis[:, L - n_q:] = seen
+    unseen = ~vis.any(0)
+    for x in (k, v, km, vm):
+        if x is not None:
+            x[unseen] = 0
     outs, tols = [], []
-    named = vis.any(0)
-    top = 0.0
     for h in range(Hq):
-        qh, kh, vh = q[:, h].double(), k[:, h // G].clone(), v[:, h // G].clone()
-        kh[~named], vh[~named] = 0, 0
+        qh, kh, vh = qd[:, h], k[:, h // G], v[:, h // G]
         x = (qh @ kh.t() * scale).masked_fill(~vis, -math.inf)
         p = torch.softmax(x, -1).nan_to_num(0.0)
         out, mag = p @ vh, p @ vh.abs()
-        size = (qh.abs() @ kh.abs().t() * abs(scale)).masked_fill(~vis, 0).amax(-1, keepdim=True)
-        if case.fmt != "bf16":
-            # in the basis: |q| |k| by norms, as the factors are rounded there
-            size = (qh.norm(dim=-1, keepdim=True) * kh.norm(dim=-1).amax() * abs(scale)).double()
-        d = D * 2.0 ** -23 * size + (0 if case.fmt == "bf16" else 2 * H16 * size)
-        hv = 0.0 if case.fmt == "bf16" else H16
+        size = qh.abs() @ kh.abs().t()
+        d = D * 2.0 ** -23 * size
+        extra = 0.0
+        if km is not None:
+            d = d + H16 * size + 4 * H16 * (qh.abs() @ km[:, h // G].t())
+            d = d + 2.0 ** -24 * D * qh.abs().amax(-1, keepdim=True) * km[:, h // G].amax(-1)
+            extra = 4 * H16 * (p @ vm[:, h // G]) + 2.0 ** -22 * (p * vm[:, h // G].amax(-1)).amax(-1, keepdim=True) * D
+        d = (abs(scale) * d).masked_fill(~vis, 0).amax(-1, keepdim=True)
         outs.append(out)
-        tols.append(U * out.abs() + (U + hv + 2 * d) * mag + (2.0 ** -24 if hv else 0.0) * vh.abs().max() + 1e-30)
+        tols.append(U * out.abs() + (U + 2 * d) * mag + extra + 1e-30)
     return torch.stack(outs, 1), torch.stack(tols, 1)
 
 
