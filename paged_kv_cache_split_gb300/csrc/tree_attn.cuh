@@ -46,11 +46,13 @@ enum Mode { kTurns = 0, kPair = 1, kSolo = 2 };
 
 constexpr int kTile = 64;               // tokens a tile
 constexpr int kRows = 128;              // rows a tile of rows
-// Warps 0..7: softmax; 8: MMAs; the last ones: keys and values (feeders).
+// Warps 0..7: softmax; 8: MMAs; 9 (packed): where the tiles lie (scout); the last ones: keys and
+// values (feeders).
 constexpr int kSoftmaxThreads = 256;
 constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
 constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
+constexpr int kAtRing = 8;              // packed: tiles that the scout runs ahead
 constexpr int kTokRing = 8;             // tiles whose keys' powers are held (see Small::tok)
 
 // Packed: the five warpgroups share the launch's registers, 2 x 128 + 48 + 2 x 88 = 5 x 96 (the
@@ -66,10 +68,13 @@ constexpr int kCost = 4;
 template <int D, int MODE, int KB, int VB>
 struct Plan {
   static constexpr bool PACKED = KB < 16;
-  // Packed: two warpgroups of feeders, so that each warp has the same few pieces of every tile
-  // (warps 9..11 fill the MMA warp's warpgroup).
+  // Packed: two warpgroups of feeders (warps 10 and 11 fill the MMA warp's).  They take tiles in
+  // turns, which halves what waits and barriers cost a tile, where a warp's pieces of the next
+  // tile, in registers, are few enough; else they share each tile.
   static constexpr int kWarps = PACKED ? 8 : 4;
   static constexpr int kFeeders = kWarps * 32;
+  static constexpr int kTeams = PACKED && D * (KB + VB) <= 1024 ? 2 : 1;
+  static constexpr int kTeam = kFeeders / kTeams;  // threads that bring a tile
   static constexpr int kFeeder0 = PACKED ? 384 : 288;  // the first feeder thread
   static constexpr int kThreads = kFeeder0 + kFeeders;
   static constexpr int kTileRows = MODE == kPair ? 2 * kRows : kRows;  // rows a unit
@@ -199,11 +204,20 @@ __device__ __forceinline__ Walk start_walk(const Params& P) {
   return w;
 }
 
+// Packed: where a tile lies, as the scout finds it.
+struct __align__(16) Place {
+  const uint8_t *slab0, *slab1;  // its blocks' slabs
+  uint32_t row0, row1;           // the kv head's first row in each; row0 = kNoTile: no tile is left
+  uint32_t live0, live1;         // tokens that are read
+};
+constexpr uint32_t kNoTile = 0xffffffffu;
+
 // Shared-memory state besides the operands.
 struct Small {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // by slot
   uint64_t s_full[2][2], p_full[2][2];                    // by warpgroup and buffer
   uint64_t pv_done[2], q_full, q_empty, drain, done;
+  uint64_t at_full[kAtRing], at_empty[kAtRing];           // packed: by tile
   Walk walk;
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
@@ -212,6 +226,7 @@ struct Small {
   // Packed, by token of a tile: scale times the power of two that its key was divided by; log2
   // of the one its value was divided by, and the inverse of that.  A tile's are overwritten
   // kTokRing tiles later, when its softmax has long handed its P over.
+  Place at[kAtRing];
   alignas(16) float tok[kTokRing][kTile], v_log[kTokRing][kTile], v_inv[kTokRing][kTile];
 };
 
@@ -302,22 +317,19 @@ struct Feed {
       }
     }
   }
-  // Packed: asks for the head's rows of 32 blocks from block j0 on (16 tiles) to come to L2, of
-  // the tokens w, w + step, ... of each.
-  __device__ __forceinline__ static void prefetch(const Params& P, const Segment& s, int j0, int kvh, int w, int step) {
-    const int j = j0 + (int)(threadIdx.x & 31);
-    if (j >= 2 * s.k1 || j * kBlockTokens >= s.len) return;
+  // Packed: asks for the rows of a kv head in lane l's block to come to L2 (lane: token).
+  __device__ __forceinline__ void prefetch(const Params& P, int l, int kvh) const {
+    const uint8_t* at = lane_ptr(base, l);
+    const int row = __shfl_sync(0xffffffffu, r, l);
+    if (!at) return;
     const LayerView& lv = P.a.lv;
-    const int32_t row = P.a.bt[(int64_t)s.b * P.a.max_blocks + j];
-    if (!draft_row_ok(lv, row)) return;
-    const int32_t slab = row / lv.slab_blocks;
-    const uint8_t* at = lv.tab.base[(size_t)slab * lv.tab.stride];
-    const int64_t slab_rows = (int64_t)lv.slab_blocks * kBlockTokens * lv.hkv;
-    const int64_t first = (int64_t)(row - slab * lv.slab_blocks) * kBlockTokens * lv.hkv + kvh;
+    const uint32_t slab_rows = (uint32_t)(lv.slab_blocks * kBlockTokens * lv.hkv);
+    const uint32_t mine = (uint32_t)((row * kBlockTokens + (int)(threadIdx.x & 31)) * lv.hkv + kvh);
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int bytes = lv.row_bytes[k];
-      for (int t = w; t < kBlockTokens; t += step)
-        for (int i = 0; i < bytes; i += 128) prefetch_l2(at + (first + (int64_t)t * lv.hkv) * bytes + i);
+      const uint32_t bytes = (uint32_t)lv.row_bytes[k];
+      prefetch_l2(at + mine * bytes);
+      if (bytes > 128) prefetch_l2(at + mine * bytes + 128);
       at += slab_rows * bytes;
     }
   }
@@ -538,8 +550,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&sm.k_full[i], L::kFeeders);
-      mbar_init(&sm.v_full[i], L::kFeeders);
+      mbar_init(&sm.k_full[i], L::kTeam);
+      mbar_init(&sm.v_full[i], L::kTeam);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_empty[i], 1);
     }
@@ -549,6 +561,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
     }
     mbar_init(&sm.q_full, kSoftmaxThreads);
     mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < kAtRing; ++i) mbar_init(&sm.at_full[i], 1), mbar_init(&sm.at_empty[i], L::kTeam / 32);
     mbar_init(&sm.drain, 1);
     mbar_init(&sm.done, kSoftmaxThreads);
     sm.dead = 0;
@@ -794,6 +807,52 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
   if (warp < L::kFeeder0 / 32) {
     // -------------------------------------------------------------------- MMAs
     if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if constexpr (PACKED) {
+      if (warp == 9) {
+        // The tiles' places, kAtRing tiles ahead of the feeders, and the rows kAhead tiles further
+        // on their way to L2.
+        constexpr int kAhead = 8;
+        Feed feed, next;  // 16 tiles each
+        int it = 0;
+        auto put = [&](const Place& p) {
+          const int slot = it % kAtRing;
+          if (it >= kAtRing) wait_or_die(&sm.at_empty[slot], (it / kAtRing - 1) & 1, dead, err);
+          if (lane == 0) {
+            sm.at[slot] = p;
+            mbar_arrive(&sm.at_full[slot]);
+          }
+          __syncwarp();
+          ++it;
+        };
+        while (walk.next(P, seg)) {
+          const int kvh = seg.x / P.n_rt;
+          feed.see(P, seg);
+          next.look_up(P, seg, seg.k0);
+          for (int u = seg.k0; u < seg.k1; ++u) {
+            const int i = (u - seg.k0) & 15;
+            if (i == 0) {
+              feed.base = next.base, feed.r = next.r;
+              next.look_up(P, seg, u + 16);
+            }
+            const uint2 live = feed.tokens(P, seg, u);
+            Place p;
+            p.slab0 = lane_ptr(feed.base, 2 * i);
+            p.slab1 = lane_ptr(feed.base, 2 * i + 1);
+            p.row0 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, 2 * i) * kBlockTokens * P.a.lv.hkv + kvh);
+            p.row1 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, 2 * i + 1) * kBlockTokens * P.a.lv.hkv + kvh);
+            p.live0 = live.x;
+            p.live1 = live.y;
+            put(p);
+            const Feed& far = i + kAhead < 16 ? feed : next;
+            far.prefetch(P, 2 * (i + kAhead) & 31, kvh);
+            far.prefetch(P, (2 * (i + kAhead) & 31) + 1, kvh);
+          }
+        }
+        // one end for each team
+        for (int k = 0; k < L::kTeams; ++k) put(Place{nullptr, nullptr, kNoTile, 0u, 0u, 0u});
+        return;
+      }
+    }
     if (warp > 8) return;
     constexpr uint32_t id_s = tc_idesc(kRows, kTile, false, false, PACKED);
     constexpr uint32_t id_o = tc_idesc(kRows, D, false, true, PACKED);
@@ -933,105 +992,82 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
     using VP = Pieces<D, VB>;
     const KP kp(lv.hkv, lv.row_bytes[0], lv.row_bytes[2], 0, km_off, P.group_log);
     const VP vp(lv.hkv, lv.row_bytes[1], lv.row_bytes[2], v_off, vm_off, P.group_log);
-    // Unit j of the keys goes to warp j % 8, the values' units to the warps from there on.
-    constexpr int W = L::kWarps, KN = (KP::kUnits + W - 1) / W, VN = (VP::kUnits + W - 1) / W;
-    const int kw = warp - L::kFeeder0 / 32, vw = (kw - KP::kUnits % W + W) % W;
-    Feed feed;
-    int lu = 0, lub = 0;       // next tile to load, first tile of the looked-up ones
-    const uint8_t *slab0 = nullptr, *slab1 = nullptr;  // the tile's blocks' slabs, and their rows there
-    uint32_t row0 = 0, row1 = 0;
-    uint2 live = make_uint2(0, 0);
-    seg.k1 = 0;
-    bool more = true;
-    // The next tile's blocks and tokens; a new segment where the last one ended.
-    auto next_tile = [&] {
-      if (lu == seg.k1) {
-        more = more && walk.next(P, seg);
-        if (!more) return;
-        lu = lub = seg.k0;
-        feed.see(P, seg);
-        feed.look_up(P, seg, lub);
-        Feed::prefetch(P, seg, 2 * lub + 2, seg.x / P.n_rt, kw, W);
-      } else if (lu - lub == 16) {
-        lub = lu;
-        feed.look_up(P, seg, lub);
-      } else if (lu - lub == 8) {
-        Feed::prefetch(P, seg, 2 * lub + 34, seg.x / P.n_rt, kw, W);
-      }
-      live = feed.tokens(P, seg, lu);
-      const int at = 2 * (lu - lub), kvh = seg.x / P.n_rt;
-      slab0 = lane_ptr(feed.base, at);
-      slab1 = lane_ptr(feed.base, at + 1);
-      row0 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, at) * kBlockTokens * lv.hkv + kvh);
-      row1 = (uint32_t)(__shfl_sync(0xffffffffu, feed.r, at + 1) * kBlockTokens * lv.hkv + kvh);
-      if (!slab0) live.x = 0;
-      if (!slab1) live.y = 0;
-      ++lu;
+    // Unit j of the keys goes to warp j % W of the team, the values' units to the warps from there on.
+    constexpr int W = L::kWarps / L::kTeams, KN = (KP::kUnits + W - 1) / W, VN = (VP::kUnits + W - 1) / W;
+    const int w = warp - L::kFeeder0 / 32, team = w / W;
+    const int kw = w % W, vw = (kw - KP::kUnits % W + W) % W;
+    Place at;
+    // The place of tile `it`; false: none is left.
+    auto next_place = [&](int it) {
+      wait_or_die(&sm.at_full[it % kAtRing], (it / kAtRing) & 1, dead, err);
+      at = sm.at[it % kAtRing];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.at_empty[it % kAtRing]);
+      if (!at.slab0) at.live0 = 0;
+      if (!at.slab1) at.live1 = 0;
+      return at.row0 != kNoTile && !__any_sync(0xffffffffu, *dead);
     };
-    // A tile's pieces are loaded while the tile before is expanded.
+    // A tile's pieces are loaded while the team's tile before is expanded.
     uint4 kc[KN], vc[VN];
     float2 km[KN], vm[VN];
     auto load_key = [&](int j) {
       const int g = kw + W * j;
       if (KP::kUnits % W && g >= KP::kUnits) return;
       const bool k = g * KP::kTokens >= 32;
-      kp.load(k ? slab1 : slab0, k ? row1 : row0, g, k ? live.y : live.x, kc[j], km[j]);
+      kp.load(k ? at.slab1 : at.slab0, k ? at.row1 : at.row0, g, k ? at.live1 : at.live0, kc[j], km[j]);
     };
     auto load_value = [&](int j) {
       const int g = vw + W * j;
       if (VP::kUnits % W && g >= VP::kUnits) return;
       const bool k = g * VP::kTokens >= 32;
-      vp.load(k ? slab1 : slab0, k ? row1 : row0, g, k ? live.y : live.x, vc[j], vm[j]);
+      vp.load(k ? at.slab1 : at.slab0, k ? at.row1 : at.row0, g, k ? at.live1 : at.live0, vc[j], vm[j]);
     };
-    next_tile();
-    bool have = more;
+    bool have = next_place(team);
     if (have) {
 #pragma unroll
       for (int j = 0; j < KN; ++j) load_key(j);
 #pragma unroll
       for (int j = 0; j < VN; ++j) load_value(j);
     }
-    uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
-    for (int it = 0; have; ++it) {
-      next_tile();
-      have = more;
-      if (kround > 0) wait_or_die(&sm.k_empty[kslot], (kround - 1) & 1, dead, err);
+    for (int it = team; have; it += L::kTeams) {
+      have = next_place(it + L::kTeams);
+      const int kslot = it % L::kK, vslot = it % L::kV;
+      if (it >= L::kK) wait_or_die(&sm.k_empty[kslot], (it / L::kK - 1) & 1, dead, err);
+      if (it >= L::kV) wait_or_die(&sm.v_empty[vslot], (it / L::kV - 1) & 1, dead, err);
+      int kx[KN], vx[VN];
+#pragma unroll
+      for (int j = 0; j < KN; ++j) kx[j] = kp.power(km[j]);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) vx[j] = vp.power(vm[j]);
 #pragma unroll
       for (int j = 0; j < KN; ++j) {
         const int g = kw + W * j;
         if (KP::kUnits % W && g >= KP::kUnits) continue;
         const uint4 c = kc[j];
-        const float2 m = km[j];
+        const float f = pow2(-kx[j]), s = km[j].x * f, o = km[j].y * f;
         if (have) load_key(j);
-        const int ex = kp.power(m);
-        const float f = pow2(-ex);
         const int token = g * KP::kTokens + kp.token;
-        if (kp.value == 0) sm.tok[it % kTokRing][token] = P.a.scale_log2 * pow2(ex);
-        expand<KB>(c, m.x * f, m.y * f, ks + kslot * L::kSlot, token, kp.value);
+        if (kp.value == 0) sm.tok[it % kTokRing][token] = P.a.scale_log2 * pow2(kx[j]);
+        expand<KB>(c, s, o, ks + kslot * L::kSlot, token, kp.value);
       }
       fence_async_shared();
       mbar_arrive(&sm.k_full[kslot]);
-      if (++kslot == L::kK) kslot = 0, ++kround;
-      if (vround > 0) wait_or_die(&sm.v_empty[vslot], (vround - 1) & 1, dead, err);
 #pragma unroll
       for (int j = 0; j < VN; ++j) {
         const int g = vw + W * j;
         if (VP::kUnits % W && g >= VP::kUnits) continue;
         const uint4 c = vc[j];
-        const float2 m = vm[j];
+        const float f = pow2(-vx[j]), s = vm[j].x * f, o = vm[j].y * f;
         if (have) load_value(j);
-        const int ex = vp.power(m);
-        const float f = pow2(-ex);
         const int token = g * VP::kTokens + vp.token;
         if (vp.value == 0) {
-          sm.v_log[it % kTokRing][token] = (float)ex;
+          sm.v_log[it % kTokRing][token] = (float)vx[j];
           sm.v_inv[it % kTokRing][token] = f;
         }
-        expand<VB>(c, m.x * f, m.y * f, vs + vslot * L::kSlot, token, vp.value);
+        expand<VB>(c, s, o, vs + vslot * L::kSlot, token, vp.value);
       }
       fence_async_shared();
       mbar_arrive(&sm.v_full[vslot]);
-      if (++vslot == L::kV) vslot = 0, ++vround;
     }
   }
 }
