@@ -46,8 +46,8 @@ enum Mode { kTurns = 0, kPair = 1, kSolo = 2 };
 
 constexpr int kTile = 64;               // tokens a tile
 constexpr int kRows = 128;              // rows a tile of rows
-// Warps 0..7: softmax; 8: MMAs; 9 (packed): where the tiles lie (scout); the last ones: keys and
-// values (feeders).
+// Warps 0..7: softmax; 8: the products with the keys; 9: those with the values; 10 (packed): where
+// the tiles lie (scout); the last ones: keys and values (feeders).
 constexpr int kSoftmaxThreads = 256;
 constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
@@ -68,26 +68,26 @@ constexpr int kCost = 4;
 template <int D, int MODE, int KB, int VB>
 struct Plan {
   static constexpr bool PACKED = KB < 16;
-  // Packed: two warpgroups of feeders (warps 10 and 11 fill the MMA warp's).  They take tiles in
+  // Packed: two warpgroups of feeders (warp 11 fills the MMA warps').  They take tiles in
   // turns, which halves what waits and barriers cost a tile, where a warp's pieces of the next
   // tile, in registers, are few enough; else they share each tile.
   static constexpr int kWarps = PACKED ? 8 : 4;
   static constexpr int kFeeders = kWarps * 32;
   static constexpr int kTeams = PACKED && D * (KB + VB) <= 1024 ? 2 : 1;
   static constexpr int kTeam = kFeeders / kTeams;  // threads that bring a tile
-  static constexpr int kFeeder0 = PACKED ? 384 : 288;  // the first feeder thread
+  static constexpr int kFeeder0 = PACKED ? 384 : 320;  // the first feeder thread
   static constexpr int kThreads = kFeeder0 + kFeeders;
   static constexpr int kTileRows = MODE == kPair ? 2 * kRows : kRows;  // rows a unit
   static constexpr int kQBytes = kTileRows * D * 2;
   static constexpr int kSlot = kTile * D * 2;
   static constexpr int kK = D == 256 ? 2 : PACKED ? 4 : D == 64 ? 8 : 5;
   static constexpr int kV = D == 256 ? 2 : PACKED || D == 128 ? 4 : 8;
-  static constexpr int kLag = MODE == kTurns ? 2 : 1;  // tiles between a tile's S and its values
   static constexpr int kSmall = 12 * 1024;
   static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kSlot + kSmall;
   static_assert(kSmem <= kSmemLimit, "shared memory");
-  static_assert(!PACKED || kK + kLag + 1 <= kTokRing, "a tile's powers are read until its softmax is done");
-  static_assert(kV >= kLag, "the values of kLag tiles wait for their softmax while the next keys are awaited");
+  // A tile's powers are overwritten kTokRing tiles later: its keys' slot was freed then by the S of
+  // the tile kTokRing - kK later, which waited for the values of the tile four before it at least.
+  static_assert(!PACKED || (kK + 4 <= kTokRing && kV <= kTokRing), "powers are read until the softmax is done");
 };
 
 struct Params {
@@ -216,7 +216,7 @@ constexpr uint32_t kNoTile = 0xffffffffu;
 struct Small {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];  // by slot
   uint64_t s_full[2][2], p_full[2][2];                    // by warpgroup and buffer
-  uint64_t pv_done[2], q_full, q_empty, drain, done;
+  uint64_t pv_done[2][2], q_full, q_empty, drain[2], done;
   uint64_t at_full[kAtRing], at_empty[kAtRing];           // packed: by tile
   Walk walk;
   uint32_t tmem;
@@ -315,22 +315,6 @@ struct Feed {
       } else {
         atomicOr(P.a.lv.err, ERR_ROW);
       }
-    }
-  }
-  // Packed: asks for the rows of a kv head in lane l's block to come to L2 (lane: token).
-  __device__ __forceinline__ void prefetch(const Params& P, int l, int kvh) const {
-    const uint8_t* at = lane_ptr(base, l);
-    const int row = __shfl_sync(0xffffffffu, r, l);
-    if (!at) return;
-    const LayerView& lv = P.a.lv;
-    const uint32_t slab_rows = (uint32_t)(lv.slab_blocks * kBlockTokens * lv.hkv);
-    const uint32_t mine = (uint32_t)((row * kBlockTokens + (int)(threadIdx.x & 31)) * lv.hkv + kvh);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t bytes = (uint32_t)lv.row_bytes[k];
-      prefetch_l2(at + mine * bytes);
-      if (bytes > 128) prefetch_l2(at + mine * bytes + 128);
-      at += slab_rows * bytes;
     }
   }
   // the 64 tokens of tile u that are read
@@ -556,13 +540,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       mbar_init(&sm.v_empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[t][i], 1), mbar_init(&sm.p_full[t][i], 128);
-      mbar_init(&sm.pv_done[t], 1);
+      for (int i = 0; i < 2; ++i)
+        mbar_init(&sm.s_full[t][i], 1), mbar_init(&sm.p_full[t][i], 128), mbar_init(&sm.pv_done[t][i], 1);
+      mbar_init(&sm.drain[t], 1);
     }
     mbar_init(&sm.q_full, kSoftmaxThreads);
     mbar_init(&sm.q_empty, 1);
     for (int i = 0; i < kAtRing; ++i) mbar_init(&sm.at_full[i], 1), mbar_init(&sm.at_empty[i], L::kTeam / 32);
-    mbar_init(&sm.drain, 1);
     mbar_init(&sm.done, kSoftmaxThreads);
     sm.dead = 0;
     fence_mbar_init();
@@ -671,7 +655,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
             m = mn;
             l = mul2(l, pair2(f, f));
             if (job > before) {
-              wait_or_die(&sm.pv_done[t], (job - 1) & 1, dead, err);
+              wait_or_die(&sm.pv_done[t][(job - 1) & 1], ((job - 1) >> 1) & 1, dead, err);
               tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
@@ -749,7 +733,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       if (!whole && mine && (!shared_rows || t == 0)) P.ml[rec] = make_float2(m, sum);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (took[k] > 0 && (shared_rows || k == t)) wait_or_die(&sm.pv_done[k], (jobs[k] - 1) & 1, dead, err);
+        if (took[k] > 0 && (shared_rows || k == t))
+          wait_or_die(&sm.pv_done[k][(jobs[k] - 1) & 1], ((jobs[k] - 1) >> 1) & 1, dead, err);
       tc_fence_after();
       if (!idle) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -808,10 +793,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
     // -------------------------------------------------------------------- MMAs
     if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if constexpr (PACKED) {
-      if (warp == 9) {
-        // The tiles' places, kAtRing tiles ahead of the feeders, and the rows kAhead tiles further
-        // on their way to L2.
-        constexpr int kAhead = 8;
+      if (warp == 10) {
+        // The tiles' places, kAtRing tiles ahead of the feeders.
         Feed feed, next;  // 16 tiles each
         int it = 0;
         auto put = [&](const Place& p) {
@@ -843,9 +826,6 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
             p.live0 = live.x;
             p.live1 = live.y;
             put(p);
-            const Feed& far = i + kAhead < 16 ? feed : next;
-            far.prefetch(P, 2 * (i + kAhead) & 31, kvh);
-            far.prefetch(P, (2 * (i + kAhead) & 31) + 1, kvh);
           }
         }
         // one end for each team
@@ -853,85 +833,91 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         return;
       }
     }
-    if (warp > 8) return;
-    constexpr uint32_t id_s = tc_idesc(kRows, kTile, false, false, PACKED);
-    constexpr uint32_t id_o = tc_idesc(kRows, D, false, true, PACKED);
-    const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ks), 16, 1024);
-    const uint64_t d_v = tc_desc(smem_u32(vs), kTile * 128, 1024);
-    int it = 0, n_seg = 0, jobs[2] = {0, 0}, done[2] = {0, 0};
-    uint32_t kslot = 0, kround = 0, vslot = 0, vround = 0;
+    if (warp > 9) return;
     bool alive = true;
     auto ready = [&](uint64_t* bar, uint32_t parity) { alive = alive && warp_wait(bar, parity, dead, err); };
-    while (alive && walk.next(P, seg)) {
-      const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = uniform(min(L::kTileRows, P.rows - row0));
-      const int first[2] = {done[0], done[1]};
-      const int n = uniform(seg.k1 - seg.k0), it0 = it;
-      ready(&sm.q_full, n_seg & 1);
-      ++n_seg;
-      // S of this tile for warpgroup t
-      auto logits = [&](int t) {
-        const int buf = jobs[t] & 1;
-        if (alive && elect_one()) {
-          const uint64_t q = d_q + ((MODE == kPair ? t * (kRows * D * 2) : 0) >> 4), k = d_k + ((kslot * L::kSlot) >> 4);
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            tc_mma(tm_s(t, buf), q + (((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4),
-                   k + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4), id_s, c > 0);
-          tc_commit(&sm.s_full[t][buf]);
-        }
-        ++jobs[t];
-      };
-      // O += P V of warpgroup t's next tile
-      auto add_values = [&](int t) {
-        const int buf = done[t] & 1;
-        ready(&sm.p_full[t][buf], (done[t] >> 1) & 1);
-        tc_fence_after();
-        if (alive && elect_one()) {
-          const uint64_t v = d_v + ((vslot * L::kSlot) >> 4);
-#pragma unroll
-          for (int c = 0; c < kTile / 16; ++c)
-            tc_mma_ts(tm_o(t), tm_s(t, buf) + 8 * c, v + ((c * 2048) >> 4), id_o, done[t] > first[t] || c > 0);
-          tc_commit(&sm.pv_done[t]);
-        }
-        ++done[t];
-      };
-      for (int i = 0; alive && i < n + L::kLag; ++i) {
-        const bool values = i >= L::kLag;
-        if (i < n) {
-          ready(&sm.k_full[kslot], kround & 1);
+    if (warp == 8) {
+      // -------------------------------------------------------------- S = Q K^T
+      constexpr uint32_t id_s = tc_idesc(kRows, kTile, false, false, PACKED);
+      const uint64_t d_q = tc_desc(smem_u32(qs), 16, 1024), d_k = tc_desc(smem_u32(ks), 16, 1024);
+      int it = 0, n_seg = 0, jobs[2] = {0, 0};
+      uint32_t slot = 0, round = 0;
+      while (alive && walk.next(P, seg)) {
+        const int nrow = uniform(min(L::kTileRows, P.rows - seg.x % P.n_rt * L::kTileRows));
+        const int n = uniform(seg.k1 - seg.k0);
+        ready(&sm.q_full, n_seg++ & 1);
+        for (int i = 0; alive && i < n; ++i, ++it) {
+          ready(&sm.k_full[slot], round & 1);
           fence_async_shared();  // the copies' writes, seen through the barrier, before the product's reads
-          tc_fence_after();
-          if (works(0, it0 + i, nrow)) logits(0);
-        }
-        if (values) {
-          ready(&sm.v_full[vslot], vround & 1);
-          fence_async_shared();
-          if (works(0, it0 + i - L::kLag, nrow)) add_values(0);
-        }
-        if (i < n) {
-          if (works(1, it0 + i, nrow)) logits(1);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!works(t, it, nrow)) continue;
+            const int buf = jobs[t] & 1;
+            // the P that lay here has met its values
+            if (jobs[t] >= 2) ready(&sm.pv_done[t][buf], ((jobs[t] >> 1) - 1) & 1);
+            tc_fence_after();
+            if (alive && elect_one()) {
+              const uint64_t q = d_q + ((MODE == kPair ? t * (kRows * D * 2) : 0) >> 4), k = d_k + ((slot * L::kSlot) >> 4);
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                tc_mma(tm_s(t, buf), q + (((c >> 2) * (kRows * 128) + (c & 3) * 32) >> 4),
+                       k + (((c >> 2) * (kTile * 128) + (c & 3) * 32) >> 4), id_s, c > 0);
+              tc_commit(&sm.s_full[t][buf]);
+            }
+            ++jobs[t];
+          }
           if (alive && elect_one()) {
-            tc_commit(&sm.k_empty[kslot]);
+            tc_commit(&sm.k_empty[slot]);
             if (i == n - 1) tc_commit(&sm.q_empty);
           }
-          if (++kslot == L::kK) kslot = 0, ++kround;
-        }
-        if (values) {
-          if (works(1, it0 + i - L::kLag, nrow)) add_values(1);
-          if (alive && elect_one()) tc_commit(&sm.v_empty[vslot]);
-          if (++vslot == L::kV) vslot = 0, ++vround;
+          if (++slot == L::kK) slot = 0, ++round;
         }
       }
-      it += n;
+      __syncwarp();
+      if (elect_one()) tc_commit(&sm.drain[0]);
+      // every MMA has completed, and the softmax warps have read their last column
+      mbar_wait_bounded(&sm.drain[0], 0, err);
+      __syncwarp();
+      mbar_wait_bounded(&sm.drain[1], 0, err);
+      __syncwarp();
+      mbar_wait_bounded(&sm.done, 0, err);
+      tc_fence_after();
+      __syncwarp();
+      tc_dealloc(tmem, 512);
+      return;
+    }
+    // ---------------------------------------------------------------- O += P V
+    constexpr uint32_t id_o = tc_idesc(kRows, D, false, true, PACKED);
+    const uint64_t d_v = tc_desc(smem_u32(vs), kTile * 128, 1024);
+    int it = 0, jobs[2] = {0, 0};
+    uint32_t slot = 0, round = 0;
+    while (alive && walk.next(P, seg)) {
+      const int nrow = uniform(min(L::kTileRows, P.rows - seg.x % P.n_rt * L::kTileRows));
+      const int n = uniform(seg.k1 - seg.k0), first[2] = {jobs[0], jobs[1]};
+      for (int i = 0; alive && i < n; ++i, ++it) {
+        ready(&sm.v_full[slot], round & 1);
+        fence_async_shared();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!works(t, it, nrow)) continue;
+          const int buf = jobs[t] & 1;
+          ready(&sm.p_full[t][buf], (jobs[t] >> 1) & 1);
+          tc_fence_after();
+          if (alive && elect_one()) {
+            const uint64_t v = d_v + ((slot * L::kSlot) >> 4);
+#pragma unroll
+            for (int c = 0; c < kTile / 16; ++c)
+              tc_mma_ts(tm_o(t), tm_s(t, buf) + 8 * c, v + ((c * 2048) >> 4), id_o, jobs[t] > first[t] || c > 0);
+            tc_commit(&sm.pv_done[t][buf]);
+          }
+          ++jobs[t];
+        }
+        if (alive && elect_one()) tc_commit(&sm.v_empty[slot]);
+        if (++slot == L::kV) slot = 0, ++round;
+      }
     }
     __syncwarp();
-    if (elect_one()) tc_commit(&sm.drain);  // every MMA has completed before the CTA ends
-    mbar_wait_bounded(&sm.drain, 0, err);
-    __syncwarp();
-    mbar_wait_bounded(&sm.done, 0, err);  // the softmax warps have read their last column
-    tc_fence_after();
-    __syncwarp();
-    tc_dealloc(tmem, 512);
+    if (elect_one()) tc_commit(&sm.drain[1]);
     return;
   }
   if constexpr (!PACKED) {
@@ -1045,10 +1031,10 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         if (KP::kUnits % W && g >= KP::kUnits) continue;
         const uint4 c = kc[j];
         const float f = pow2(-kx[j]), s = km[j].x * f, o = km[j].y * f;
-        if (have) load_key(j);
         const int token = g * KP::kTokens + kp.token;
         if (kp.value == 0) sm.tok[it % kTokRing][token] = P.a.scale_log2 * pow2(kx[j]);
         expand<KB>(c, s, o, ks + kslot * L::kSlot, token, kp.value);
+        if (have) load_key(j);
       }
       fence_async_shared();
       mbar_arrive(&sm.k_full[kslot]);
@@ -1058,13 +1044,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         if (VP::kUnits % W && g >= VP::kUnits) continue;
         const uint4 c = vc[j];
         const float f = pow2(-vx[j]), s = vm[j].x * f, o = vm[j].y * f;
-        if (have) load_value(j);
         const int token = g * VP::kTokens + vp.token;
         if (vp.value == 0) {
           sm.v_log[it % kTokRing][token] = (float)vx[j];
           sm.v_inv[it % kTokRing][token] = f;
         }
         expand<VB>(c, s, o, vs + vslot * L::kSlot, token, vp.value);
+        if (have) load_value(j);
       }
       fence_async_shared();
       mbar_arrive(&sm.v_full[vslot]);
