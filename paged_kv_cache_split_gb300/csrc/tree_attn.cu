@@ -6,83 +6,76 @@ namespace pkv {
 namespace tree {
 namespace {
 
-// Merge of a row's records, one warp per row, in order.  Also the zero rows of unused or bad
-// sequences.
+// Merge of the records of split units, in order: a warp takes eight columns of 32 rows, a lane a
+// row of them.  Also the zero rows of unused or bad sequences.
 template <int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ Params P) {
-  constexpr int V = D / 32;
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ Params P, int row_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int C = D / 8;  // groups of eight columns
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // (b, i, h)
-  if (row >= (int64_t)P.a.B * P.a.n_q * P.a.Hq) return;
-  const int h = (int)(row % P.a.Hq), i = (int)(row / P.a.Hq % P.a.n_q), b = (int)(row / P.a.Hq / P.a.n_q);
-  const int kvh = h / P.G, r = i * P.G + h % P.G;
-  const int64_t unit = ((int64_t)b * P.a.lv.hkv + kvh) * P.n_rt + r / P.tile_rows;
+  const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int c = (int)(item % C), rb = (int)(item / C % row_blocks);
+  const int64_t unit = item / C / row_blocks;  // (sequence, kv head, group of rows)
+  if (unit >= (int64_t)P.a.B * P.a.lv.hkv * P.n_rt) return;
+  const int rt = (int)(unit % P.n_rt), kvh = (int)(unit / P.n_rt % P.a.lv.hkv), b = (int)(unit / P.n_rt / P.a.lv.hkv);
   const int2 meta = P.meta[unit];  // (garbage where the length is 0)
   bool bad;
   const int32_t len = draft_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
-  uint16_t* out = P.a.out + row * D + lane * V;
-  float o[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = 0.f;
+  const int rr = rb * 32 + lane, r = rt * P.tile_rows + rr;
+  const bool mine = rr < P.tile_rows && r < P.rows;
+  float o[8] = {};
   float inv = 0.f;
   if (len == 0) {
-    if (bad && i == 0 && h == 0 && lane == 0) atomicOr(P.a.lv.err, ERR_CTX);
+    if (bad && kvh == 0 && rt == 0 && rb == 0 && c == 0 && lane == 0) atomicOr(P.a.lv.err, ERR_CTX);
   } else {
     if (meta.x < 0) return;
-    const int n = meta.y - meta.x + 1, rr = r % P.tile_rows;
-    // records: the first in its CTA's second slot, then the first slot of every later CTA
-    auto at = [&](int k) { return (2 * (int64_t)(meta.x + k) + (k == 0 ? 1 : 0)) * P.rec_rows + rr; };
-    constexpr int U = D == 256 ? 4 : 8;  // records in flight
-    float v[U][V];
-    float2 ml[U];
-    auto load = [&](int k0) {
+    if (mine) {
+      const int n = meta.y - meta.x + 1;
+      // records: the first in its CTA's second slot, then the first slot of every later CTA
+      auto slot = [&](int k) { return 2 * (int64_t)(meta.x + k) + (k == 0 ? 1 : 0); };
+      constexpr int U = 8;  // records in flight
+      float m = kNoMax, sum = 0.f;
+      for (int k0 = 0; k0 < n; k0 += U) {
+        float2 ml[U];
+        float4 v[U][2];
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (k0 + k < n) {
-          const int64_t a = at(k0 + k);
-          ml[k] = P.ml[a];
-          const float* src = P.acc + a * D + lane * V;
-          if constexpr (V == 2) {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            v[k][0] = x.x, v[k][1] = x.y;
-          } else {
-#pragma unroll
-            for (int e = 0; e < V; e += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src + e);
-              v[k][e] = x.x, v[k][e + 1] = x.y, v[k][e + 2] = x.z, v[k][e + 3] = x.w;
-            }
+        for (int k = 0; k < U; ++k) {
+          ml[k] = make_float2(kNoMax, 0.f);
+          v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k < n) {
+            const int64_t s = slot(k0 + k);
+            ml[k] = P.ml[s * P.rec_rows + rr];
+            const float4* acc = reinterpret_cast<const float4*>(P.acc) + (s * (D / 4) + 2 * c) * P.rec_rows + rr;
+            v[k][0] = acc[0];
+            v[k][1] = acc[P.rec_rows];
           }
         }
-    };
-    load(0);
-    float M = kNoMax;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, P.ml[at(k)].x);
+        float top = m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float sum = 0.f;
-    for (int k0 = 0; k0 < n; k0 += U) {
-      if (k0 > 0) load(k0);
+        for (int k = 0; k < U; ++k) top = fmaxf(top, ml[k].x);
+        const float f = ex2(m - top);
+        m = top;
+        sum *= f;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (k0 + k < n) {
-          const float w = ex2(ml[k].x - M);
+        for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float w = ex2(ml[k].x - m);
           sum = fmaf(w, ml[k].y, sum);
+          const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = fmaf(w, v[k][e], o[e]);
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(w, x[e], o[e]);
         }
+      }
+      inv = sum > 0.f ? 1.f / sum : 0.f;
     }
-    inv = sum > 0.f ? 1.f / sum : 0.f;
   }
-  if constexpr (V == 2) {
-    *reinterpret_cast<uint32_t*>(out) = bf2(o[0] * inv, o[1] * inv);
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(bf2(o[0] * inv, o[1] * inv), bf2(o[2] * inv, o[3] * inv));
-  } else {
-    *reinterpret_cast<uint4*>(out) = make_uint4(bf2(o[0] * inv, o[1] * inv), bf2(o[2] * inv, o[3] * inv),
-                                                bf2(o[4] * inv, o[5] * inv), bf2(o[6] * inv, o[7] * inv));
-  }
+  if (!mine) return;
+  const int i = r / P.G, g = r - i * P.G;
+  uint16_t* out = P.a.out + (((int64_t)b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D + 8 * c;
+  *reinterpret_cast<uint4*>(out) = make_uint4(bf2(o[0] * inv, o[1] * inv), bf2(o[2] * inv, o[3] * inv),
+                                              bf2(o[4] * inv, o[5] * inv), bf2(o[6] * inv, o[7] * inv));
 }
 
 // How a call is laid out: rows of a (sequence, kv head), 128 or 256 of them a unit.
@@ -107,11 +100,21 @@ Geometry geometry(int D, int hkv, int B, int n_q, int Hq, int ctas) {
   return g;
 }
 
+// Launched with programmatic dependence, as tc_launch does, with a second argument.
 template <int D>
 cudaError_t merge(const Params& P) {
-  static std::atomic<uint64_t> none{0};
-  const int64_t rows = (int64_t)P.a.B * P.a.n_q * P.a.Hq;
-  return tc_launch(tree_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)), 256, (size_t)0, P.a.stream, P, P.a.device, &none);
+  const int row_blocks = (P.rec_rows + 31) / 32;
+  const int64_t warps = (int64_t)P.a.B * P.a.lv.hkv * P.n_rt * row_blocks * (D / 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = P.a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, P, row_blocks);
 }
 
 }  // namespace

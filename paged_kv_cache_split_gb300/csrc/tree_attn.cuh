@@ -55,7 +55,7 @@ constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
 constexpr int kAtRing = 8;              // packed: tiles that the scout runs ahead
 constexpr int kTokRing = 8;             // tiles whose keys' powers are held (see Small::tok)
 
-// Packed: the five warpgroups share the launch's registers, 2 x 128 + 48 + 2 x 88 = 5 x 96 (the
+// Packed: the five warpgroups share the launch's registers, 2 x 136 + 40 + 2 x 80 <= 5 x 96 (the
 // launcher checks that the kernel was built with 96).  Their paths do not rejoin: each ends in a
 // return.
 constexpr int kLaunchRegs = 96;
@@ -71,7 +71,7 @@ struct Plan {
   // Packed: two warpgroups of feeders (warp 11 fills the MMA warps').  They take tiles in
   // turns, which halves what waits and barriers cost a tile, where a warp's pieces of the next
   // tile, in registers, are few enough; else they share each tile.
-  static constexpr int kWarps = PACKED ? 8 : 4;
+  static constexpr int kWarps = PACKED ? 8 : 2;  // (bf16: 12 warps in all, 168 registers a thread)
   static constexpr int kFeeders = kWarps * 32;
   static constexpr int kTeams = PACKED && D * (KB + VB) <= 1024 ? 2 : 1;
   static constexpr int kTeam = kFeeders / kTeams;  // threads that bring a tile
@@ -101,7 +101,7 @@ struct Params {
   int group_log; // packed: log2 of the values a group
   int2* meta;    // [B * hkv * n_rt]: first CTA of a split unit (-1: written directly), last CTA
   float2* ml;    // [2 * grid][rec_rows]: reference and sum of a record's rows
-  float* acc;    // [2 * grid][rec_rows][D]
+  float* acc;    // [2 * grid][D / 4][rec_rows][4]: lanes, which own rows, store and load whole lines
 };
 
 __device__ __forceinline__ int32_t length(const Params& P, int b) {
@@ -371,7 +371,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
 #pragma unroll
     for (int e = 0; e < E; ++e) sign[e] = P.a.signs[lane * E + e] * (D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f);
   }
-  constexpr int U = 4;  // rows in flight
+  constexpr int U = D == 256 ? 8 : 16;  // rows in flight
   for (int rb = warp; rb < nrow; rb += 8 * U) {
     uint32_t w[U][E / 2];
 #pragma unroll
@@ -573,12 +573,12 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int tr = (warp & 3) * 32 + lane;  // row of the tile
     int it0 = 0, n_seg = 0;
-    int jobs[2] = {0, 0};                   // tiles that the warpgroups took, over all segments
+    int jobs = 0, others = 0;               // tiles that this warpgroup and the other took, over all segments
     while (walk.next(P, seg)) {
       const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = min(L::kTileRows, P.rows - row0);
       const int kvh = seg.x / P.n_rt;
@@ -597,102 +597,121 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const uint64_t qp2 = pair2(qp, qp);
       float m = kNoMax;
       uint64_t l = 0;  // two partial sums
-      const int before = jobs[t];
+      const int before = jobs;
       int it = it0;
       for (int u = seg.k0; u < seg.k1; ++u, ++it) {
         if (!works(t, it, nrow)) continue;
-        const int job = jobs[t]++, buf = job & 1;
+        const int job = jobs++, buf = job & 1;
         wait_or_die(&sm.s_full[t][buf], (job >> 1) & 1, dead, err);
         // the values' powers are written with them
         if constexpr (PACKED) wait_or_die(&sm.v_full[it % L::kV], (it / L::kV) & 1, dead, err);
         if (!idle) {
           tc_fence_after();
-          float x[kTile];
-          {
-            uint32_t a[2][32];
-            tc_ld_rows<32>(tm_s(t, buf) + lanes, a[0]);
-            tc_ld_rows<32>(tm_s(t, buf) + 32 + lanes, a[1]);
-            tc_wait_ld();
+          // 32 tokens at a time: 64 logits would not fit the registers beside the rest.
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            float x[32];
+            {
+              uint32_t a[32];
+              tc_ld_rows<32>(tm_s(t, buf) + 32 * q + lanes, a);
+              tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) x[c] = __uint_as_float(a[c >> 5][c & 31]);
-          }
-#pragma unroll
-          for (int c = 0; c < kTile; c += 4) {
+              for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(a[c]);
+            }
             if constexpr (PACKED) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][c]);
-              const float4 e = *reinterpret_cast<const float4*>(&sm.v_log[it % kTokRing][c]);
-              split2(fma2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), qp2, pair2(e.x, e.y)), x[c], x[c + 1]);
-              split2(fma2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), qp2, pair2(e.z, e.w)), x[c + 2], x[c + 3]);
+              const float4* f4 = reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][32 * q]);
+              const float4* e4 = reinterpret_cast<const float4*>(&sm.v_log[it % kTokRing][32 * q]);
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 f = f4[c / 4], e = e4[c / 4];
+                split2(fma2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), qp2, pair2(e.x, e.y)), x[c], x[c + 1]);
+                split2(fma2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), qp2, pair2(e.z, e.w)), x[c + 2], x[c + 3]);
+              }
             } else {
               const uint64_t f = pair2(P.a.scale_log2, P.a.scale_log2);
-              split2(mul2(pair2(x[c], x[c + 1]), f), x[c], x[c + 1]);
-              split2(mul2(pair2(x[c + 2], x[c + 3]), f), x[c + 2], x[c + 3]);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) split2(mul2(pair2(x[c], x[c + 1]), f), x[c], x[c + 1]);
             }
-          }
-          if ((u + 1) * kTile > seg.len - P.a.n_q) {
-            const int j0 = u * kTile - (seg.len - P.a.n_q);
-            const uint32_t* mask = P.a.mask + seg.b * P.a.mask_stride + (int64_t)(r / P.G) * P.words;
-            auto word = [&](int w) { return mask[w]; };
-            const uint32_t b0 = bits_at(j0, P.a.n_q, P.words, word), b1 = bits_at(j0 + 32, P.a.n_q, P.words, word);
+            const int j0 = u * kTile + 32 * q - (seg.len - P.a.n_q);
+            if (j0 + 32 > 0) {
+              const uint32_t* mask = P.a.mask + seg.b * P.a.mask_stride + (int64_t)(r / P.G) * P.words;
+              const uint32_t bits = bits_at(j0, P.a.n_q, P.words, [&](int w) { return mask[w]; });
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (!(b0 >> c & 1u)) x[c] = -INFINITY;
-              if (!(b1 >> c & 1u)) x[32 + c] = -INFINITY;
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1u)) x[c] = -INFINITY;
             }
-          }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 4; c + 4 < kTile; c += 8)
+            for (int c = 4; c + 4 < 32; c += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kTile - 4 + e]);
-          // rows past the unit's hold anything: they must not move the references of this warp's others
-          const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) : -INFINITY;
-          if (__any_sync(0xffffffffu, top - m > kSlack)) {
-            const float mn = fmaxf(m, rintf(top));
-            const float f = ex2(m - mn);
-            m = mn;
-            l = mul2(l, pair2(f, f));
-            if (job > before) {
-              wait_or_die(&sm.pv_done[t][(job - 1) & 1], ((job - 1) >> 1) & 1, dead, err);
-              tc_fence_after();
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[28 + e]);
+            // rows past the unit's hold anything: they must not move the references of this warp's others
+            const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) : -INFINITY;
+            if (__any_sync(0xffffffffu, top - m > kSlack)) {
+              const float mn = fmaxf(m, rintf(top));
+              const float f = ex2(m - mn);
+              m = mn;
+              l = mul2(l, pair2(f, f));
+              if (job > before) {
+                wait_or_die(&sm.pv_done[t][(job - 1) & 1], ((job - 1) >> 1) & 1, dead, err);
+                tc_fence_after();
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tc_ld_rows<32>(tm_o(t) + 32 * q + lanes, o);
+                for (int k = 0; k < D / 32; ++k) {
+                  uint32_t o[32];
+                  tc_ld_rows<32>(tm_o(t) + 32 * k + lanes, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                  tc_st_rows<32>(tm_o(t) + 32 * k + lanes, o);
+                }
+              }
+              if (q > 0) {
+                // the tile's first half is written: f is a power of two, which P takes exactly
+                uint32_t w[16];
+                tc_wait_st();
+                tc_ld_rows<16>(tm_s(t, buf) + lanes, w);
                 tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                tc_st_rows<32>(tm_o(t) + 32 * q + lanes, o);
+                for (int c = 0; c < 16; ++c) {
+                  if constexpr (PACKED) {
+                    const float2 v = __half22float2(half2_of(w[c]));
+                    w[c] = fp16x2(v.x * f, v.y * f);
+                  } else {
+                    float v0, v1;
+                    bf16x2_to_f32(w[c], v0, v1);
+                    w[c] = bf2(v0 * f, v1 * f);
+                  }
+                }
+                tc_st_rows<16>(tm_s(t, buf) + lanes, w);
               }
             }
-          }
-          __syncwarp();
-          const uint64_t mm = pair2(-m, -m);
-          uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
+            __syncwarp();
+            const uint64_t mm = pair2(-m, -m);
+            const float4* i4 = reinterpret_cast<const float4*>(&sm.v_inv[it % kTokRing][32 * q]);
+            uint64_t sum0 = 0, sum1 = 0;
             uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float e0, e1;
-              split2(add2(pair2(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]), mm), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              uint64_t& s = c & 1 ? sum1 : sum0;
+            for (int c = 0; c < 16; c += 2) {
+              float e0, e1, e2, e3;
+              split2(add2(pair2(x[2 * c], x[2 * c + 1]), mm), e0, e1);
+              split2(add2(pair2(x[2 * c + 2], x[2 * c + 3]), mm), e2, e3);
+              e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
               if constexpr (PACKED) {
-                const float2 f = *reinterpret_cast<const float2*>(&sm.v_inv[it % kTokRing][32 * q + 2 * c]);
-                s = fma2(pair2(e0, e1), pair2(f.x, f.y), s);
-                w[c] = fp16x2(e0, e1);
+                const float4 f = i4[c / 2];
+                sum0 = fma2(pair2(e0, e1), pair2(f.x, f.y), sum0);
+                sum1 = fma2(pair2(e2, e3), pair2(f.z, f.w), sum1);
+                w[c] = fp16x2(e0, e1), w[c + 1] = fp16x2(e2, e3);
               } else {
-                s = add2(s, pair2(e0, e1));
-                w[c] = bf2(e0, e1);
+                sum0 = add2(sum0, pair2(e0, e1));
+                sum1 = add2(sum1, pair2(e2, e3));
+                w[c] = bf2(e0, e1), w[c + 1] = bf2(e2, e3);
               }
             }
             tc_st_rows<16>(tm_s(t, buf) + 16 * q + lanes, w);
+            l = add2(l, add2(sum0, sum1));
           }
-          l = add2(l, add2(sum0, sum1));
           tc_wait_st();
           tc_fence_before();
         }
@@ -700,11 +719,11 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       }
       // Tiles that each warpgroup took of this segment.
       const int n = seg.k1 - seg.k0;
-      int took[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        took[k] = MODE == kTurns ? (n + (((it0 & 1) == k) ? 1 : 0)) / 2 : works(k, 0, nrow) ? n : 0;
-      jobs[t ^ 1] += took[t ^ 1];
+      auto taken = [&](int k) {
+        return MODE == kTurns ? (n + (((it0 & 1) == k) ? 1 : 0)) / 2 : works(k, 0, nrow) ? n : 0;
+      };
+      const int took0 = taken(0), took1 = taken(1);
+      others += t ? took0 : took1;
       it0 += n;
       // Output of the segment: O / sum, or a record (reference, sum, O) to be merged.
       const bool whole = seg.k0 == 0 && seg.k1 == seg.n;
@@ -731,16 +750,16 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       }
       const int64_t rec = slot * P.rec_rows + rr;
       if (!whole && mine && (!shared_rows || t == 0)) P.ml[rec] = make_float2(m, sum);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (took[k] > 0 && (shared_rows || k == t))
-          wait_or_die(&sm.pv_done[k][(jobs[k] - 1) & 1], ((jobs[k] - 1) >> 1) & 1, dead, err);
+      // the last product of this warpgroup's O, and of the other's where both are read
+      auto settled = [&](int k, int last) { wait_or_die(&sm.pv_done[k][last & 1], (last >> 1) & 1, dead, err); };
+      if ((t ? took1 : took0) > 0) settled(t, jobs - 1);
+      if (shared_rows && (t ? took0 : took1) > 0) settled(t ^ 1, others - 1);
       tc_fence_after();
       if (!idle) {
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const int i = r / P.G, g = r - i * P.G;
         uint16_t* out = P.a.out + (((int64_t)seg.b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D;
-        float* acc = P.acc + rec * D;
+        float4* acc = reinterpret_cast<float4*>(P.acc) + slot * (D / 4) * P.rec_rows + rr;
         const int c0 = shared_rows ? t * (D / 64) : 0, c1 = shared_rows ? c0 + D / 64 : D / 32;
 #pragma unroll 1
         for (int q = c0; q < c1; ++q) {
@@ -748,7 +767,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
           uint32_t a[32];
           // The tensor-memory loads want the whole warp at once, which has just stored by rows.
           __syncwarp();
-          if (shared_rows && took[0] == 0) {
+          if (shared_rows && took0 == 0) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = 0.f;
           } else {
@@ -757,7 +776,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int c = 0; c < 32; ++c) o[c] = __uint_as_float(a[c]) * f[0];
           }
-          if (MODE == kTurns && took[1] > 0) {
+          if (MODE == kTurns && took1 > 0) {
             tc_ld_rows<32>(tm_o(1) + 32 * q + lanes, a);
             tc_wait_ld();
 #pragma unroll
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
           } else if (mine) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              reinterpret_cast<float4*>(acc + 32 * q)[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              acc[(int64_t)(8 * q + c) * P.rec_rows] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
       }
@@ -791,7 +810,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
   }
   if (warp < L::kFeeder0 / 32) {
     // -------------------------------------------------------------------- MMAs
-    if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if constexpr (PACKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if constexpr (PACKED) {
       if (warp == 10) {
         // The tiles' places, kAtRing tiles ahead of the feeders.
@@ -969,7 +988,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // --------------------------------------------------------------- expansion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const LayerView& lv = P.a.lv;
     const uint32_t slab_rows = (uint32_t)(lv.slab_blocks * kBlockTokens * lv.hkv);
     const uint32_t v_off = slab_rows * lv.row_bytes[0], km_off = v_off + slab_rows * lv.row_bytes[1],
