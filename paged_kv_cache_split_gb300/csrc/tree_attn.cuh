@@ -21,12 +21,12 @@
 //
 // bf16 keys and values go from the pool to swizzled operand tiles by 16-byte asynchronous
 // copies, which fill tokens that nobody sees (past the length, unused drafts) with zeros: a
-// stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by eight warps,
-// each token's keys and its values under the power of two that puts its largest near 2^13.  The
-// keys' power goes back into the logits.  The values' e_t goes into the probabilities' exponent,
-// P[t] = exp2(x[t] + e_t - m), so that O needs nothing (the reference follows x + e) and the sum
-// takes P[t] 2^-e_t: any magnitudes fit, and what fp16 drops of P is below 2^-25 of the largest
-// contribution to O.
+// stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by eight warps, a
+// tile's keys and its values each under the power of two that puts the largest near 2^13.  The
+// keys' power goes back into the logits.  The values' e goes into the probabilities' exponent,
+// P[t] = exp2(x[t] + e - m), so that O needs nothing (the reference follows x + e), and comes off
+// the tile's sum again.  Any magnitudes fit; within a tile, what is 2^-27 of the largest and less
+// loses bits.  (Powers by token took 48 loads a row and tile in the softmax: three times its time.)
 //
 // The key tiles of all units (sequence, kv head, 128 or 256 rows) are laid end to end and split
 // evenly in cost over the CTAs, one a SM.  A unit inside one CTA's share is written directly; a
@@ -53,7 +53,7 @@ constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the 
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
 constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
 constexpr int kAtRing = 8;              // packed: tiles that the scout runs ahead
-constexpr int kTokRing = 8;             // tiles whose keys' powers are held (see Small::tok)
+constexpr int kPowRing = 8;             // packed: tiles whose powers are held
 
 // Packed: the five warpgroups share the launch's registers, 2 x 136 + 40 + 2 x 80 <= 5 x 96 (the
 // launcher checks that the kernel was built with 96).  Their paths do not rejoin: each ends in a
@@ -85,9 +85,9 @@ struct Plan {
   static constexpr int kSmall = 12 * 1024;
   static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kSlot + kSmall;
   static_assert(kSmem <= kSmemLimit, "shared memory");
-  // A tile's powers are overwritten kTokRing tiles later: its keys' slot was freed then by the S of
-  // the tile kTokRing - kK later, which waited for the values of the tile four before it at least.
-  static_assert(!PACKED || (kK + 4 <= kTokRing && kV <= kTokRing), "powers are read until the softmax is done");
+  // A tile's powers are overwritten kPowRing tiles later: its keys' slot was freed then by the S of
+  // the tile kPowRing - kK later, which waited for the values of the tile four before it at least.
+  static_assert(!PACKED || kK + 4 <= kPowRing, "powers are read until the softmax is done");
 };
 
 struct Params {
@@ -223,11 +223,11 @@ struct Small {
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
   float m[2][kRows], l[2][kRows];  // the warpgroups' references and sums of shared rows
   float q_pow[2 * kRows];      // packed: the power of two that a row's query was divided by
-  // Packed, by token of a tile: scale times the power of two that its key was divided by; log2
-  // of the one its value was divided by, and the inverse of that.  A tile's are overwritten
-  // kTokRing tiles later, when its softmax has long handed its P over.
-  Place at[kAtRing];
-  alignas(16) float tok[kTokRing][kTile], v_log[kTokRing][kTile], v_inv[kTokRing][kTile];
+  // Packed, by tile: scale times the power of two that its keys were divided by, log2 of the one
+  // its values were divided by, and the inverse of that.
+  alignas(16) float4 pow[kPowRing];
+  Place at[kAtRing];           // packed
+  float2 widest[2][2][8];      // by team, parity of its tile and warp: largest key and value
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t policy) {
@@ -333,6 +333,11 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t col) {
   return (uint32_t)(c >> 3) * col + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
 }
 
+// log2 of the power of two that puts mx near 2^13
+__device__ __forceinline__ int power_of(float mx) {
+  return max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+}
+
 // 4-bit codes are expanded two at a time, i and i + 4 of each eight values: an operand row holds
 // them in the order 0 4 1 5 2 6 3 7.  A warp's row of fp16 values (E a lane) into that order:
 template <int E>
@@ -421,7 +426,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
         for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const int ex = max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+        const int ex = power_of(mx);
         const float f = pow2(-ex);
 #pragma unroll
         for (int e = 0; e < E; e += 2) w[u][e / 2] = fp16x2(x[e] * f, x[e + 1] * f);
@@ -474,15 +479,9 @@ struct Pieces {
       m = *reinterpret_cast<const float2*>(slab + (row * meta_row + t0 * meta_step + meta_at));
     }
   }
-  // log2 of the power of two that puts the token's largest magnitude near 2^13, from the scales and
-  // offsets of the lanes that hold its pieces
-  __device__ __forceinline__ static int power(const float2& m) {
-    float mx = fmaxf(fabsf(m.y), fabsf(fmaf(m.x, (float)((1 << BITS) - 1), m.y)));
-#pragma unroll
-    for (int off = 1; off < kCol; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-#pragma unroll
-    for (int off = kCol * kTokens; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    return max(-100, min(120, (int)(__float_as_uint(mx) >> 23) - 127 - 13));
+  // the largest magnitude of a piece
+  __device__ __forceinline__ static float widest(const float2& m) {
+    return fmaxf(fabsf(m.y), fabsf(fmaf(m.x, (float)((1 << BITS) - 1), m.y)));
   }
 };
 
@@ -594,7 +593,6 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const bool idle = (MODE == kPair ? t * kRows : 0) + (warp & 3) * 32 >= nrow;  // a warp without rows
       const int r = row0 + (mine ? rr : 0);
       const float qp = PACKED && mine ? sm.q_pow[rr] : 1.f;
-      const uint64_t qp2 = pair2(qp, qp);
       float m = kNoMax;
       uint64_t l = 0;  // two partial sums
       const int before = jobs;
@@ -603,10 +601,17 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         if (!works(t, it, nrow)) continue;
         const int job = jobs++, buf = job & 1;
         wait_or_die(&sm.s_full[t][buf], (job >> 1) & 1, dead, err);
-        // the values' powers are written with them
-        if constexpr (PACKED) wait_or_die(&sm.v_full[it % L::kV], (it / L::kV) & 1, dead, err);
         if (!idle) {
           tc_fence_after();
+          // Logits are in units of scale (times the row's and the tile's powers); packed: m is the
+          // reference of x + lift.
+          float sc = P.a.scale_log2, lift = 0.f, back = 1.f;
+          if constexpr (PACKED) {
+            const float4 f = sm.pow[it % kPowRing];
+            sc = f.x * qp, lift = f.y, back = f.z;
+          }
+          const uint64_t sc2 = pair2(sc, sc);
+          uint64_t sum = 0;
           // 32 tokens at a time: 64 logits would not fit the registers beside the rest.
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
@@ -618,20 +623,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
               for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(a[c]);
             }
-            if constexpr (PACKED) {
-              const float4* f4 = reinterpret_cast<const float4*>(&sm.tok[it % kTokRing][32 * q]);
-              const float4* e4 = reinterpret_cast<const float4*>(&sm.v_log[it % kTokRing][32 * q]);
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 f = f4[c / 4], e = e4[c / 4];
-                split2(fma2(mul2(pair2(x[c], x[c + 1]), pair2(f.x, f.y)), qp2, pair2(e.x, e.y)), x[c], x[c + 1]);
-                split2(fma2(mul2(pair2(x[c + 2], x[c + 3]), pair2(f.z, f.w)), qp2, pair2(e.z, e.w)), x[c + 2], x[c + 3]);
-              }
-            } else {
-              const uint64_t f = pair2(P.a.scale_log2, P.a.scale_log2);
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) split2(mul2(pair2(x[c], x[c + 1]), f), x[c], x[c + 1]);
-            }
+            for (int c = 0; c < 32; c += 2) split2(mul2(pair2(x[c], x[c + 1]), sc2), x[c], x[c + 1]);
             const int j0 = u * kTile + 32 * q - (seg.len - P.a.n_q);
             if (j0 + 32 > 0) {
               const uint32_t* mask = P.a.mask + seg.b * P.a.mask_stride + (int64_t)(r / P.G) * P.words;
@@ -648,12 +641,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[28 + e]);
             // rows past the unit's hold anything: they must not move the references of this warp's others
-            const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) : -INFINITY;
+            const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) + lift : -INFINITY;
             if (__any_sync(0xffffffffu, top - m > kSlack)) {
               const float mn = fmaxf(m, rintf(top));
               const float f = ex2(m - mn);
               m = mn;
               l = mul2(l, pair2(f, f));
+              sum = mul2(sum, pair2(f, f));
               if (job > before) {
                 wait_or_die(&sm.pv_done[t][(job - 1) & 1], ((job - 1) >> 1) & 1, dead, err);
                 tc_fence_after();
@@ -688,9 +682,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
               }
             }
             __syncwarp();
-            const uint64_t mm = pair2(-m, -m);
-            const float4* i4 = reinterpret_cast<const float4*>(&sm.v_inv[it % kTokRing][32 * q]);
-            uint64_t sum0 = 0, sum1 = 0;
+            const uint64_t mm = pair2(lift - m, lift - m);
+            uint64_t other = 0;
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
@@ -698,20 +691,15 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
               split2(add2(pair2(x[2 * c], x[2 * c + 1]), mm), e0, e1);
               split2(add2(pair2(x[2 * c + 2], x[2 * c + 3]), mm), e2, e3);
               e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
-              if constexpr (PACKED) {
-                const float4 f = i4[c / 2];
-                sum0 = fma2(pair2(e0, e1), pair2(f.x, f.y), sum0);
-                sum1 = fma2(pair2(e2, e3), pair2(f.z, f.w), sum1);
-                w[c] = fp16x2(e0, e1), w[c + 1] = fp16x2(e2, e3);
-              } else {
-                sum0 = add2(sum0, pair2(e0, e1));
-                sum1 = add2(sum1, pair2(e2, e3));
-                w[c] = bf2(e0, e1), w[c + 1] = bf2(e2, e3);
-              }
+              sum = add2(sum, pair2(e0, e1));
+              other = add2(other, pair2(e2, e3));
+              w[c] = PACKED ? fp16x2(e0, e1) : bf2(e0, e1);
+              w[c + 1] = PACKED ? fp16x2(e2, e3) : bf2(e2, e3);
             }
+            sum = add2(sum, other);
             tc_st_rows<16>(tm_s(t, buf) + 16 * q + lanes, w);
-            l = add2(l, add2(sum0, sum1));
           }
+          l = PACKED ? fma2(sum, pair2(back, back), l) : add2(l, sum);
           tc_wait_st();
           tc_fence_before();
         }
@@ -1039,40 +1027,49 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const int kslot = it % L::kK, vslot = it % L::kV;
       if (it >= L::kK) wait_or_die(&sm.k_empty[kslot], (it / L::kK - 1) & 1, dead, err);
       if (it >= L::kV) wait_or_die(&sm.v_empty[vslot], (it / L::kV - 1) & 1, dead, err);
-      int kx[KN], vx[VN];
+      // The tile's largest key and value: of the warp's pieces, then over the team's warps.
+      float kmax = 0.f, vmax = 0.f;
 #pragma unroll
-      for (int j = 0; j < KN; ++j) kx[j] = kp.power(km[j]);
+      for (int j = 0; j < KN; ++j)
+        if (KP::kUnits % W == 0 || kw + W * j < KP::kUnits) kmax = fmaxf(kmax, KP::widest(km[j]));
 #pragma unroll
-      for (int j = 0; j < VN; ++j) vx[j] = vp.power(vm[j]);
+      for (int j = 0; j < VN; ++j)
+        if (VP::kUnits % W == 0 || vw + W * j < VP::kUnits) vmax = fmaxf(vmax, VP::widest(vm[j]));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, off));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+      }
+      float2* all = sm.widest[team][it / L::kTeams & 1];
+      if (lane == 0) all[kw] = make_float2(kmax, vmax);
+      __syncwarp();
+      named_barrier_sync(2 + team, 32 * W);
+#pragma unroll
+      for (int i = 0; i < W; ++i) kmax = fmaxf(kmax, all[i].x), vmax = fmaxf(vmax, all[i].y);
+      const int kx = power_of(kmax), vx = power_of(vmax);
+      const float kf = pow2(-kx), vf = pow2(-vx);
+      if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_float4(P.a.scale_log2 * pow2(kx), (float)vx, vf, 0.f);
 #pragma unroll
       for (int j = 0; j < KN; ++j) {
         const int g = kw + W * j;
         if (KP::kUnits % W && g >= KP::kUnits) continue;
-        const uint4 c = kc[j];
-        const float f = pow2(-kx[j]), s = km[j].x * f, o = km[j].y * f;
-        const int token = g * KP::kTokens + kp.token;
-        if (kp.value == 0) sm.tok[it % kTokRing][token] = P.a.scale_log2 * pow2(kx[j]);
-        expand<KB>(c, s, o, ks + kslot * L::kSlot, token, kp.value);
-        if (have) load_key(j);
+        expand<KB>(kc[j], km[j].x * kf, km[j].y * kf, ks + kslot * L::kSlot, g * KP::kTokens + kp.token, kp.value);
       }
-      fence_async_shared();
+      // (the warps that issue the products order these writes before the products' reads)
       mbar_arrive(&sm.k_full[kslot]);
+#pragma unroll
+      for (int j = 0; j < KN; ++j)
+        if (have) load_key(j);
 #pragma unroll
       for (int j = 0; j < VN; ++j) {
         const int g = vw + W * j;
         if (VP::kUnits % W && g >= VP::kUnits) continue;
-        const uint4 c = vc[j];
-        const float f = pow2(-vx[j]), s = vm[j].x * f, o = vm[j].y * f;
-        const int token = g * VP::kTokens + vp.token;
-        if (vp.value == 0) {
-          sm.v_log[it % kTokRing][token] = (float)vx[j];
-          sm.v_inv[it % kTokRing][token] = f;
-        }
-        expand<VB>(c, s, o, vs + vslot * L::kSlot, token, vp.value);
-        if (have) load_value(j);
+        expand<VB>(vc[j], vm[j].x * vf, vm[j].y * vf, vs + vslot * L::kSlot, g * VP::kTokens + vp.token, vp.value);
       }
-      fence_async_shared();
       mbar_arrive(&sm.v_full[vslot]);
+#pragma unroll
+      for (int j = 0; j < VN; ++j)
+        if (have) load_value(j);
     }
   }
 }
