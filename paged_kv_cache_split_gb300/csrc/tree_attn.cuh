@@ -68,12 +68,14 @@ constexpr int kCost = 4;
 template <int D, int MODE, int KB, int VB>
 struct Plan {
   static constexpr bool PACKED = KB < 16;
-  // Packed: two warpgroups of feeders (warp 11 fills the MMA warps').  They take tiles in
-  // turns, which halves what waits and barriers cost a tile, where a warp's pieces of the next
-  // tile, in registers, are few enough; else they share each tile.
+  // Packed: two warpgroups of feeders (warp 11 fills the MMA warps'), in teams that take tiles in
+  // turns, so that one team's loads and waits lie under the others' work.  A warp then has (KB +
+  // VB) / 2 pieces of a tile, at most eight in registers, whatever D (two teams instead of one
+  // took 8 x 16384 tokens in K4/V4 from 188 to 155 us at D = 128, four instead of two from 134 to
+  // 126 us the other way; K8/V8 at D = 64 80 -> 74 us with four).
   static constexpr int kWarps = PACKED ? 8 : 2;  // (bf16: 12 warps in all, 168 registers a thread)
   static constexpr int kFeeders = kWarps * 32;
-  static constexpr int kTeams = PACKED && D * (KB + VB) <= 1024 ? 2 : 1;
+  static constexpr int kTeams = PACKED ? 256 / D : 1;
   static constexpr int kTeam = kFeeders / kTeams;  // threads that bring a tile
   static constexpr int kFeeder0 = PACKED ? 384 : 320;  // the first feeder thread
   static constexpr int kThreads = kFeeder0 + kFeeders;
@@ -227,7 +229,7 @@ struct Small {
   // its values were divided by, and the inverse of that.
   alignas(16) float4 pow[kPowRing];
   Place at[kAtRing];           // packed
-  float2 widest[2][2][8];      // by team, parity of its tile and warp: largest key and value
+  float2 widest[4][2][8];      // by team, parity of its tile and warp: largest key and value
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t policy) {
@@ -1000,7 +1002,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       if (!at.slab1) at.live1 = 0;
       return at.row0 != kNoTile && !__any_sync(0xffffffffu, *dead);
     };
-    // A tile's pieces are loaded while the team's tile before is expanded.
+    // (Loaded ahead, in registers, the pieces' arrival was waited for all the same: by the loads from
+    // shared memory that came in between.  More teams cover it.)
     uint4 kc[KN], vc[VN];
     float2 km[KN], vm[VN];
     auto load_key = [&](int j) {
@@ -1015,18 +1018,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const bool k = g * VP::kTokens >= 32;
       vp.load(k ? at.slab1 : at.slab0, k ? at.row1 : at.row0, g, k ? at.live1 : at.live0, vc[j], vm[j]);
     };
-    bool have = next_place(team);
-    if (have) {
+    for (int it = team; next_place(it); it += L::kTeams) {
+      const int kslot = it % L::kK, vslot = it % L::kV;
 #pragma unroll
       for (int j = 0; j < KN; ++j) load_key(j);
 #pragma unroll
       for (int j = 0; j < VN; ++j) load_value(j);
-    }
-    for (int it = team; have; it += L::kTeams) {
-      have = next_place(it + L::kTeams);
-      const int kslot = it % L::kK, vslot = it % L::kV;
       if (it >= L::kK) wait_or_die(&sm.k_empty[kslot], (it / L::kK - 1) & 1, dead, err);
-      if (it >= L::kV) wait_or_die(&sm.v_empty[vslot], (it / L::kV - 1) & 1, dead, err);
       // The tile's largest key and value: of the warp's pieces, then over the team's warps.
       float kmax = 0.f, vmax = 0.f;
 #pragma unroll
@@ -1057,9 +1055,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       }
       // (the warps that issue the products order these writes before the products' reads)
       mbar_arrive(&sm.k_full[kslot]);
-#pragma unroll
-      for (int j = 0; j < KN; ++j)
-        if (have) load_key(j);
+      if (it >= L::kV) wait_or_die(&sm.v_empty[vslot], (it / L::kV - 1) & 1, dead, err);
 #pragma unroll
       for (int j = 0; j < VN; ++j) {
         const int g = vw + W * j;
@@ -1067,9 +1063,6 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         expand<VB>(vc[j], vm[j].x * vf, vm[j].y * vf, vs + vslot * L::kSlot, g * VP::kTokens + vp.token, vp.value);
       }
       mbar_arrive(&sm.v_full[vslot]);
-#pragma unroll
-      for (int j = 0; j < VN; ++j)
-        if (have) load_value(j);
     }
   }
 }
