@@ -645,7 +645,11 @@ class Pool:
         one, kv = (n,), (n, Hk, D)
         kp, vp = _dev_strided(k, bf16, "k", kv), _dev_strided(v, bf16, "v", kv)
         # a dimension of one entry is never stepped over: its stride says nothing
-        kt, kh, vt, vh = (x.stride(d) if x.shape[d] > 1 else 0 for x in (k, v) for d in (0, 1))
+        (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
+        if n < 2:
+            kt = vt = 0
+        if Hk < 2:
+            kh = vh = 0
         Hq, qp, op = 0, None, None
         qt = qh = ot = oh = 0
         if q is not None:
@@ -656,7 +660,11 @@ class Pool:
             if q_out is None:
                 q_out = self._own(shape, bf16, q.device, stream)
             qp, op = _dev_strided(q, bf16, "q", shape), _dev_strided(q_out, bf16, "q_out", shape)
-            qt, qh, ot, oh = (x.stride(d) if x.shape[d] > 1 else 0 for x in (q, q_out) for d in (0, 1))
+            (qt, qh, _), (ot, oh, _) = q.stride(), q_out.stride()
+            if n < 2:
+                qt = ot = 0
+            if Hq < 2:
+                qh = oh = 0
         elif q_out is not None or q_norm is not None:
             raise ValueError("q_out or q_norm without q")
         self._same_device(rows, slots, k, v, positions, cos_sin, q, k_norm, q_norm, q_out)

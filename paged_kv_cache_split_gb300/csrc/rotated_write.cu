@@ -25,11 +25,12 @@
 namespace pkv {
 namespace {
 
-constexpr int kLoads = 8;  // 16-byte loads a lane has in flight
+constexpr int kLoads = 4;  // 16-byte loads a lane has in flight
 
 struct Params {
   RotatedWriteArgs a;
-  int per_token;       // warps a token (rows of heads: keys, queries, values)
+  int kv_units;        // warps that a token's keys take, and its values
+  int per_token;       // warps a token: keys, values and queries; packed: queries
   int64_t pack_units;  // packed: warps that quantise keys (and as many values), before the queries' warps
 };
 
@@ -85,90 +86,93 @@ struct Angles {
   }
 };
 
-// Rows of token i's heads, from row r0 on, 32 / (D / 8) of them a load: keys (stored),
-// queries, values (copied), in this order; `first`: the rows before r0 that this launch
-// leaves to others (a packed pool's keys), `rows`: one past the last.
-template <int D, bool IL>
-__device__ __forceinline__ void copy_rows(const RotatedWriteArgs& a, int i, int r0, int rows) {
+enum Kind { kKeys, kValues, kQueries };
+
+// Heads r0 .. of one kind of token i, 32 / (D / 8) of them a load.  NORM: k_norm or q_norm is given.
+template <int D, bool IL, bool NORM>
+__device__ __forceinline__ void copy_heads(const RotatedWriteArgs& a, int i, Kind kind, int r0) {
   constexpr int LPH = D / 8;     // lanes a head
   constexpr int HPL = 32 / LPH;  // heads a load
   const int lane = threadIdx.x & 31, c = lane % LPH, sub = lane / LPH;
-  const int hkv = a.lv.hkv, hq = a.Hq;
+  const int heads = kind == kQueries ? a.Hq : a.lv.hkv;
+  const int64_t step = kind == kKeys ? a.k_head : kind == kValues ? a.v_head : a.q_head;
+  const uint16_t* src = kind == kKeys     ? a.k + (int64_t)i * a.k_tok
+                        : kind == kValues ? a.v + (int64_t)i * a.v_tok
+                                          : a.q + (int64_t)i * a.q_tok;
   uint4 raw[kLoads];
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     const int r = r0 + u * HPL + sub;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const uint16_t* src = r < hkv ? a.k + (int64_t)i * a.k_tok + r * a.k_head
-                            : r < hkv + hq ? a.q + (int64_t)i * a.q_tok + (r - hkv) * a.q_head
-                                           : a.v + (int64_t)i * a.v_tok + (r - hkv - hq) * a.v_head;
-      raw[u] = reinterpret_cast<const uint4*>(src)[c];
-    }
+    raw[u] = r < heads ? reinterpret_cast<const uint4*>(src + r * step)[c] : make_uint4(0, 0, 0, 0);
   }
-  const int32_t pos = a.positions[i], row = a.rows[i], slot = a.slots[i];
-  const bool pos_ok = pos >= 0 && pos < a.n_pos, ok = place_ok(a.lv, row, slot) && pos_ok;
-  if (!ok && r0 == 0 && lane == 0) flag(a.lv, pos_ok, row);
-  if (!pos_ok) return;
-  uint4 *kd = nullptr, *vd = nullptr;
-  if (ok) {
-    kd = reinterpret_cast<uint4*>(draft_row(a.lv, PKV_KIND_K, row, slot, 0));
-    vd = reinterpret_cast<uint4*>(draft_row(a.lv, PKV_KIND_V, row, slot, 0));
+  const int32_t pos = a.positions[i];
+  const bool pos_ok = pos >= 0 && pos < a.n_pos;
+  uint4* dst;
+  int64_t dst_step;  // in 16-byte pieces
+  if (kind == kQueries) {
+    if (!pos_ok) return;  // flagged with the keys
+    dst = reinterpret_cast<uint4*>(a.qo + (int64_t)i * a.o_tok);
+    dst_step = a.o_head / 8;
+  } else {
+    const int32_t row = a.rows[i], slot = a.slots[i];
+    if (!pos_ok || !place_ok(a.lv, row, slot)) {
+      if (kind == kKeys && r0 == 0 && lane == 0) flag(a.lv, pos_ok, row);
+      return;
+    }
+    dst = reinterpret_cast<uint4*>(draft_row(a.lv, kind == kKeys ? PKV_KIND_K : PKV_KIND_V, row, slot, 0));
+    dst_step = LPH;
+  }
+  if (kind == kValues) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int r = r0 + u * HPL + sub;
+      if (r < heads) dst[r * dst_step + c] = raw[u];
+    }
+    return;
   }
   const int half = a.rot / 16;  // chunks of half of the turned part
   const bool turned = c < 2 * half, second = c >= half;
-  const int src = lane + (turned ? (second ? -half : half) : 0);
+  const int from = lane + (turned ? (second ? -half : half) : 0);
   Angles<IL> ang;
-  if (turned) ang.load(a.cos_sin + (int64_t)pos * a.rot, c, a.rot);
+  // (chunks that are not turned take the first angles and drop the result)
+  ang.load(a.cos_sin + (int64_t)pos * a.rot, turned ? c : 0, a.rot);
+  const uint16_t* w = kind == kKeys ? a.k_norm : a.q_norm;
+  float g[8];
+  if (NORM && w) unpack8(reinterpret_cast<const uint4*>(w)[c], g);
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     const int r = r0 + u * HPL + sub;
-    const bool is_v = r >= hkv + hq;
     float x[8];
     unpack8(raw[u], x);
-    const uint16_t* w = r < hkv ? a.k_norm : is_v ? nullptr : a.q_norm;
-    if (a.k_norm || a.q_norm) {
+    uint4 o = raw[u];  // untouched values keep their bits
+    if (NORM && w) {
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
       for (int off = 1; off < LPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (w) {
-        const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
-        float g[8];
-        unpack8(reinterpret_cast<const uint4*>(w)[c], g);
+      const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * g[e];
-      }
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * g[e];
+      if (a.rot < D) o = pack8(x);
     }
-    const float keep[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-    ang.turn(x, src, second);
-    if (!turned) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = keep[e];
-    }
-    // untouched values keep their bits
-    const uint4 o = is_v || (!turned && !w) ? raw[u] : pack8(x);
-    if (r < rows) {
-      if (r < hkv) {
-        if (ok) kd[r * LPH + c] = o;
-      } else if (!is_v) {
-        reinterpret_cast<uint4*>(a.qo + (int64_t)i * a.o_tok + (r - hkv) * a.o_head)[c] = o;
-      } else if (ok) {
-        vd[(r - hkv - hq) * LPH + c] = o;
-      }
-    }
+    ang.turn(x, from, second);
+    if (turned) o = pack8(x);
+    if (r < heads) dst[r * dst_step + c] = o;
   }
 }
 
-template <int D, bool IL>
-__global__ void __launch_bounds__(256) rotated_write_kernel(const __grid_constant__ Params P) {
+template <int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(256, !IL && NORM ? 3 : 4) rotated_write_kernel(const __grid_constant__ Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t u = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const uint32_t i = u / (uint32_t)P.per_token;
   if (i >= (uint32_t)P.a.n) return;
-  copy_rows<D, IL>(P.a, (int)i, (int)(u - i * P.per_token) * kLoads * (256 / D), 2 * P.a.lv.hkv + P.a.Hq);
+  int part = (int)(u - i * P.per_token);
+  const Kind kind = part < P.kv_units ? kKeys : part < 2 * P.kv_units ? kValues : kQueries;
+  part -= kind == kKeys ? 0 : kind == kValues ? P.kv_units : 2 * P.kv_units;
+  copy_heads<D, IL, NORM>(P.a, (int)i, kind, part * kLoads * (256 / D));
 }
 
 // ---------------------------------------------------------------------------
@@ -203,13 +207,17 @@ __device__ __forceinline__ void quantise(const float (&x)[E], uint8_t* codes, ui
   uint32_t w[E * BITS / 32];
 #pragma unroll
   for (int k = 0; k < E * BITS / 32; ++k) w[k] = 0;
+  // The code is that of the IEEE quotient.  A product with the reciprocal is off by less than
+  // 2^-21 TOP steps: where it lies further than that from a border, it gives the same code.
+  const float inv = scale > 1e-37f && scale < 1e37f ? __frcp_rn(scale) : 0.f;  // (0: divides)
+  constexpr float kClear = 0.5f - TOP * 4.76837158e-7f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    int q = 0;
-    if (scale != 0.0f) {
-      q = __float2int_rn(__fdiv_rn(__fsub_rn(x[e], mn), scale));
-      q = q < 0 ? 0 : (q > TOP ? TOP : q);
-    }
+    const float d = __fsub_rn(x[e], mn);
+    const float t = __fmul_rn(d, inv);
+    float code = rintf(t);
+    if (inv == 0.f || !(fabsf(__fsub_rn(t, code)) < kClear)) code = scale != 0.f ? rintf(__fdiv_rn(d, scale)) : 0.f;
+    const int q = min(max((int)code, 0), TOP);
     w[e * BITS / 32] |= (uint32_t)q << (e * BITS % 32);
   }
   if (!store) return;
@@ -220,7 +228,12 @@ __device__ __forceinline__ void quantise(const float (&x)[E], uint8_t* codes, ui
   if (c % (GS / E) == 0) reinterpret_cast<float2*>(meta)[c / (GS / E)] = make_float2(scale, mn);
 }
 
-// x += the exact product a b, x = (h, l)
+// x = the exact product a b, x = (h, l)
+__device__ __forceinline__ void two_prod(float& h, float& l, float a, float b) {
+  h = __fmul_rn(a, b);
+  l = __fmaf_rn(a, b, -h);
+}
+// x += the exact product a b
 __device__ __forceinline__ void two_prod_add(float& h, float& l, float a, float b) {
   const float p = __fmul_rn(a, b), pe = __fmaf_rn(a, b, -p);
   const float s = __fadd_rn(h, p), t = __fsub_rn(s, h);
@@ -290,10 +303,10 @@ __device__ __forceinline__ void pack_keys(const RotatedWriteArgs& a, int64_t r, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float u = x[e + 2 * j], v = x[e + 2 * j + 1];
-        float h0 = 0.f, l0 = 0.f, h1 = 0.f, l1 = 0.f;
-        two_prod_add(h0, l0, u, cc[j]);
+        float h0, l0, h1, l1;
+        two_prod(h0, l0, u, cc[j]);
         two_prod_add(h0, l0, -v, ss[j]);
-        two_prod_add(h1, l1, u, ss[j]);
+        two_prod(h1, l1, u, ss[j]);
         two_prod_add(h1, l1, v, cc[j]);
         x[e + 2 * j] = h0, l[e + 2 * j] = l0;
         x[e + 2 * j + 1] = h1, l[e + 2 * j + 1] = l1;
@@ -313,8 +326,8 @@ __device__ __forceinline__ void pack_keys(const RotatedWriteArgs& a, int64_t r, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float other = __shfl_sync(0xffffffffu, x[e + j], src);
-        float hh = 0.f, ll = 0.f;
-        two_prod_add(hh, ll, x[e + j], cc[j]);
+        float hh, ll;
+        two_prod(hh, ll, x[e + j], cc[j]);
         two_prod_add(hh, ll, second ? other : -other, ss[j]);
         x[e + j] = hh, l[e + j] = ll;
       }
@@ -380,35 +393,41 @@ __global__ void __launch_bounds__(256) rotated_pack_kernel(const __grid_constant
   u -= 2 * P.pack_units;
   const int64_t i = u / P.per_token;
   if (i >= P.a.n || P.a.Hq == 0) return;
-  copy_rows<D, IL>(P.a, (int)i, P.a.lv.hkv + (int)(u - i * P.per_token) * kLoads * (256 / D), P.a.lv.hkv + P.a.Hq);
+  copy_heads<D, IL, true>(P.a, (int)i, kQueries, (int)(u - i * P.per_token) * kLoads * (256 / D));
 }
 
 template <int D, bool IL>
 cudaError_t launch_di(const RotatedWriteArgs& a) {
   Params P;
   P.a = a;
-  P.pack_units = 0;
   constexpr int per_warp = kLoads * (256 / D);
-  const int rows = a.fmt == PKV_FMT_BF16 ? 2 * a.lv.hkv + a.Hq : a.Hq;
-  P.per_token = rows > 0 ? (rows + per_warp - 1) / per_warp : 1;
-  int64_t units = rows > 0 ? (int64_t)a.n * P.per_token : 0;
-  if (a.fmt != PKV_FMT_BF16) {
+  const int q_units = (a.Hq + per_warp - 1) / per_warp;
+  int64_t units;
+  void (*kern)(Params);
+  if (a.fmt == PKV_FMT_BF16) {
+    P.pack_units = 0;
+    P.kv_units = (a.lv.hkv + per_warp - 1) / per_warp;
+    P.per_token = 2 * P.kv_units + q_units;
+    units = (int64_t)a.n * P.per_token;
+    kern = a.k_norm || a.q_norm ? rotated_write_kernel<D, IL, true> : rotated_write_kernel<D, IL, false>;
+  } else {
     constexpr int RPW = 32 / (D / E);
     P.pack_units = ((int64_t)a.n * a.lv.hkv + RPW - 1) / RPW;
-    units += 2 * P.pack_units;
+    P.kv_units = 0;
+    P.per_token = q_units > 0 ? q_units : 1;
+    units = 2 * P.pack_units + (int64_t)a.n * q_units;
+    if (a.fmt == PKV_FMT_K4V4)
+      kern = D >= 128 && a.group == kGroupWide ? rotated_pack_kernel<D, IL, 4, 4, (D >= 128 ? kGroupWide : kGroup)>
+                                               : rotated_pack_kernel<D, IL, 4, 4, kGroup>;
+    else if (a.fmt == PKV_FMT_K8V4)
+      kern = rotated_pack_kernel<D, IL, 8, 4, kGroup>;
+    else
+      kern = rotated_pack_kernel<D, IL, 8, 8, kGroup>;
   }
   // a step's few tokens spread over the SMs, one warp per CTA
   const int threads = units < 2048 ? 32 : 256;
   const dim3 grid((unsigned)((units * 32 + threads - 1) / threads));
   static std::atomic<uint64_t> none{0};
-  void (*kern)(Params) = rotated_write_kernel<D, IL>;
-  if (a.fmt == PKV_FMT_K4V4)
-    kern = D >= 128 && a.group == kGroupWide ? rotated_pack_kernel<D, IL, 4, 4, (D >= 128 ? kGroupWide : kGroup)>
-                                             : rotated_pack_kernel<D, IL, 4, 4, kGroup>;
-  else if (a.fmt == PKV_FMT_K8V4)
-    kern = rotated_pack_kernel<D, IL, 8, 4, kGroup>;
-  else if (a.fmt == PKV_FMT_K8V8)
-    kern = rotated_pack_kernel<D, IL, 8, 8, kGroup>;
   return tc_launch(kern, grid, threads, (size_t)0, a.stream, P, 0, &none);
 }
 
