@@ -6,13 +6,16 @@ namespace pkv {
 namespace tree {
 namespace {
 
-// Merge of the records of split units, in order: a warp takes eight columns of 32 rows, a lane a
-// row of them.  Also the zero rows of unused or bad sequences.
-template <int D>
+// Merge of the records of split units, in order: a warp takes 4 V columns of 32 rows, a lane a
+// row of them.  Also the zero rows of unused or bad sequences.  U records are in flight: few
+// units over many CTAs leave many records each, whose latency counts (U = 16, V = 1: 8 units with
+// 19 records 26.9 us a call against 28.6), many units many warps (U = 8, V = 2: 128 units of 128
+// rows 185 us against 191).
+template <int D, int U, int V>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ Params P, int row_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int C = D / 8;  // groups of eight columns
+  constexpr int C = D / (4 * V);  // groups of columns
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int c = (int)(item % C), rb = (int)(item / C % row_blocks);
@@ -24,7 +27,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const int32_t len = draft_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
   const int rr = rb * 32 + lane, r = rt * P.tile_rows + rr;
   const bool mine = rr < P.tile_rows && r < P.rows;
-  float o[8] = {};
+  float o[4 * V] = {};
   float inv = 0.f;
   if (len == 0) {
     if (bad && kvh == 0 && rt == 0 && rb == 0 && c == 0 && lane == 0) atomicOr(P.a.lv.err, ERR_CTX);
@@ -34,21 +37,21 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
       const int n = meta.y - meta.x + 1;
       // records: the first in its CTA's second slot, then the first slot of every later CTA
       auto slot = [&](int k) { return 2 * (int64_t)(meta.x + k) + (k == 0 ? 1 : 0); };
-      constexpr int U = 8;  // records in flight
       float m = kNoMax, sum = 0.f;
       for (int k0 = 0; k0 < n; k0 += U) {
         float2 ml[U];
-        float4 v[U][2];
+        float4 v[U][V];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           ml[k] = make_float2(kNoMax, 0.f);
-          v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (k0 + k < n) {
             const int64_t s = slot(k0 + k);
             ml[k] = P.ml[s * P.rec_rows + rr];
-            const float4* acc = reinterpret_cast<const float4*>(P.acc) + (s * (D / 4) + 2 * c) * P.rec_rows + rr;
-            v[k][0] = acc[0];
-            v[k][1] = acc[P.rec_rows];
+            const float4* acc = reinterpret_cast<const float4*>(P.acc) + (s * (D / 4) + V * c) * P.rec_rows + rr;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][e] = acc[e * P.rec_rows];
           }
         }
         float top = m;
@@ -58,14 +61,18 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
         m = top;
         sum *= f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= f;
+        for (int e = 0; e < 4 * V; ++e) o[e] *= f;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           const float w = ex2(ml[k].x - m);
           sum = fmaf(w, ml[k].y, sum);
-          const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(w, x[e], o[e]);
+          for (int e = 0; e < V; ++e) {
+            o[4 * e] = fmaf(w, v[k][e].x, o[4 * e]);
+            o[4 * e + 1] = fmaf(w, v[k][e].y, o[4 * e + 1]);
+            o[4 * e + 2] = fmaf(w, v[k][e].z, o[4 * e + 2]);
+            o[4 * e + 3] = fmaf(w, v[k][e].w, o[4 * e + 3]);
+          }
         }
       }
       inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -73,9 +80,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   }
   if (!mine) return;
   const int i = r / P.G, g = r - i * P.G;
-  uint16_t* out = P.a.out + (((int64_t)b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D + 8 * c;
-  *reinterpret_cast<uint4*>(out) = make_uint4(bf2(o[0] * inv, o[1] * inv), bf2(o[2] * inv, o[3] * inv),
-                                              bf2(o[4] * inv, o[5] * inv), bf2(o[6] * inv, o[7] * inv));
+  uint16_t* out = P.a.out + (((int64_t)b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D + 4 * V * c;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    reinterpret_cast<uint2*>(out)[e] =
+        make_uint2(bf2(o[4 * e] * inv, o[4 * e + 1] * inv), bf2(o[4 * e + 2] * inv, o[4 * e + 3] * inv));
 }
 
 // How a call is laid out: rows of a (sequence, kv head), 128 or 256 of them a unit.
@@ -104,7 +113,9 @@ Geometry geometry(int D, int hkv, int B, int n_q, int Hq, int ctas) {
 template <int D>
 cudaError_t merge(const Params& P) {
   const int row_blocks = (P.rec_rows + 31) / 32;
-  const int64_t warps = (int64_t)P.a.B * P.a.lv.hkv * P.n_rt * row_blocks * (D / 8);
+  const int64_t units = (int64_t)P.a.B * P.a.lv.hkv * P.n_rt;
+  const bool many = P.a.ctas >= 4 * units;  // records a unit
+  const int64_t warps = units * row_blocks * (many ? D / 4 : D / 8);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
   cfg.blockDim = dim3(256);
@@ -114,7 +125,7 @@ cudaError_t merge(const Params& P) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, P, row_blocks);
+  return cudaLaunchKernelEx(&cfg, many ? tree_merge_kernel<D, 16, 1> : tree_merge_kernel<D, 8, 2>, P, row_blocks);
 }
 
 }  // namespace

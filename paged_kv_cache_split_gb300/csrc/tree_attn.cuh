@@ -61,8 +61,9 @@ constexpr int kPowRing = 8;             // packed: tiles whose powers are held
 constexpr int kLaunchRegs = 96;
 
 // Cost of a unit's start in the split over the CTAs, in quarter tiles: its queries are loaded
-// and its output or record written.
-constexpr int kSegCost = 16;
+// and its output or record written.  (4, 7, 10 tiles: 4 x 16384, 64 drafts 58.1, 56.1, 56.6 us;
+// the same with heads of 64 38.1, 37.1, 37.9; K8/V8 8 x 16384, 24 drafts 75.1, 74.4, 74.0.)
+constexpr int kSegCost = 28;
 constexpr int kCost = 4;
 
 template <int D, int MODE, int KB, int VB>
