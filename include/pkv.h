@@ -535,7 +535,8 @@ pkv_status pkv_latent_prefill_attention(pkv_pool* pool, int layer, int B, int n_
  * drafts than the batch's n_q still has n_q places; the unused ones are named by no mask.
  * Outputs and workspaces overlap no input, but for write_rotated's q_out, and a workspace
  * belongs to one call at a time (two streams or graphs take one each).  These calls require
- * the pool's device to be the current one (PKV_ERR_INVALID otherwise).  The pages describe
+ * the pool's device to be the current one (PKV_ERR_INVALID otherwise).  pkv_price_request
+ * prices such a step but for its workspace, which is pkv_tree_workspace_bytes.  The pages describe
  * none of them: they are written from the formulas given here.
  * --------------------------------------------------------------------------- */
 
@@ -597,8 +598,12 @@ pkv_status pkv_tree_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq
  * Slots past a sequence's length, and drafted tokens that no query of the sequence sees, are
  * never read into a result, whatever they hold; a drafted token whose value holds a NaN or an
  * infinity may reach queries that do not see it, once one does.  max_ctx is accepted for
- * interface stability.  Probabilities enter the second product in 16 bits; sums and softmax
- * state are fp32.  Deterministic.  Limits: B <= 4096, n_q <= 1024, Hq <= 1024 and a multiple of
+ * interface stability.  Probabilities enter the second product in 16 bits (bf16, for packed
+ * pools fp16); sums and softmax state are fp32.  A packed pool's keys, values and rotated
+ * queries are expanded to fp16 (c s + o with s and o rounded to fp16), keys and values under a
+ * power of two for each 64 tokens (positions 64 j to 64 j + 63), so that any magnitude fits but
+ * what is below 2^-27 of the largest of its 64 loses bits; the logits times log2(e) are expected
+ * to be finite in fp32.  Deterministic.  Limits: B <= 4096, n_q <= 1024, Hq <= 1024 and a multiple of
  * n_kv_heads, B * n_q * Hq <= 2^24, max_blocks <= 2^20, |scale| log2(e) finite in fp32, pointers
  * 16-byte aligned.  PKV_ERR_FORMAT on a latent pool.  B = 0 returns PKV_OK.  Asynchronous. */
 pkv_status pkv_paged_tree_attention(pkv_pool* pool, int layer, int B, int n_q, int Hq, const void* q_bf16,

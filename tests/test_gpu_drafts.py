@@ -10,14 +10,16 @@ relative to the value, h = 2^-11 half an fp16 one):
   write, packed  the scale and offset are fp32 values of a row known to 2^-22 of its largest
                  value (2^-36 without the norm); a code is the nearest one of a quotient off by
                  the 2^-22 of top steps that the fp32 subtraction and division may lose;
-  tree           u |y| for the output, u sum p |v| for the probabilities' rounding (half of which
-                 goes to 16 bits at most), 2 d sum p |v| for the logits, d being D 2^-23 scale sum
-                 |q k| for the fp32 sums.  A packed value is c s + o with s and o rounded to fp16 and
-                 one rounding more: off by h (|c s| + |o| + |c s + o|) <= h (2 M + M + M) = 4 h M, M
-                 the largest magnitude of its group, as c s is at most the group's range.  So
-                 values add 4 h sum p M and keys 4 h scale sum |q| M to d, the queries' own rounding
-                 h scale sum |q| |k|; what fp16 drops altogether is 2^-24 of a token's largest, and
-                 of the largest contribution.
+  tree           u |y| for the output, u sum p |v| for the probabilities' rounding to 16 bits
+                 (bf16: u; fp16, packed pools: less), 2 d sum p |v| for the logits, d being D 2^-23
+                 scale sum |q k| for the fp32 sums.  A packed value is c s + o with s and o rounded to
+                 fp16 and one rounding more: off by h (|c s| + |o| + |c s + o|) <= h (2 M + M + M) =
+                 4 h M, M the largest magnitude of its group, as c s is at most the group's range.  So
+                 values add 4 h sum p M and keys 4 h scale sum |q| M to d, the queries' own rounding h
+                 scale sum |q| |k|.  The operands lie under a power of two by tile (64 tokens) whose
+                 largest is 2^13 to 2^14: fp16 drops at most 2^-25 of it, 2^-38 of the tile's largest
+                 magnitude T a value (keys: 2^-38 scale D |q| T; values: 2^-38 T), and at most 2^-25
+                 of P, whose largest is 2^-1 at least: L 2^-24 of the largest p T over L tokens.
 The elementwise bounds are worst cases; a relative L2 bound holds the average: each
 rounding contributes at most u / sqrt(3) in the mean square, at most four of them with
 logits of unit size, so 2 u < 1e-2."""
@@ -420,6 +422,13 @@ def bits_of(mask, n_q):
     return (mask.long()[..., j // 32] >> j % 32 & 1).bool()
 
 
+def tile_largest(x):
+    """[L]: the largest of x [L, D] in each token's tile of 64."""
+    m = x.amax(-1)
+    m = torch.nn.functional.pad(m, (0, -m.shape[0] % 64)).view(-1, 64).amax(-1)
+    return m.repeat_interleave(64)[:x.shape[0]]
+
+
 def reference(case, b, q, seen, scale):
     """(out, tolerance) of sequence b; q [n_q, Hq, D], seen [n_q, n_q]."""
     n_q, Hq, D = q.shape
@@ -443,8 +452,9 @@ def reference(case, b, q, seen, scale):
         extra = 0.0
         if km is not None:
             d = d + H16 * size + 4 * H16 * (qh.abs() @ km[:, h // G].t())
-            d = d + 2.0 ** -24 * D * qh.abs().amax(-1, keepdim=True) * km[:, h // G].amax(-1)
-            extra = 4 * H16 * (p @ vm[:, h // G]) + 2.0 ** -22 * (p * vm[:, h // G].amax(-1)).amax(-1, keepdim=True) * D
+            tk, tv = (tile_largest(y[:, h // G]) for y in (km, vm))
+            d = d + 2.0 ** -38 * D * qh.abs().amax(-1, keepdim=True) * tk
+            extra = 4 * H16 * (p @ vm[:, h // G]) + 2.0 ** -38 * tv.max() + L * 2.0 ** -24 * (p * tv).amax(-1, keepdim=True)
         d = (abs(scale) * d).masked_fill(~vis, 0).amax(-1, keepdim=True)
         outs.append(out)
         tols.append(U * out.abs() + (U + 2 * d) * mag + extra + 1e-30)
