@@ -596,9 +596,9 @@ pkv_status pkv_tree_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq
  * max_blocks * 32 or one in (0, n_q) sets the device error word (bit 2) and gives zero rows; a
  * block-table row outside the pool sets bit 1 (the sequence's result is then undefined).
  * Slots past a sequence's length, and drafted tokens that no query of the sequence sees, are
- * never read into a result, whatever they hold; a drafted token whose value holds a NaN or an
- * infinity may reach queries that do not see it, once one does.  max_ctx is accepted for
- * interface stability.  Probabilities enter the second product in 16 bits (bf16, for packed
+ * never read into a result, whatever they hold; a drafted token whose value (packed: key or
+ * value, scales and offsets among them) holds a NaN or an infinity may reach queries that do not
+ * see it, once one does.  max_ctx is accepted for interface stability.  Probabilities enter the second product in 16 bits (bf16, for packed
  * pools fp16); sums and softmax state are fp32.  A packed pool's keys, values and rotated
  * queries are expanded to fp16 (c s + o with s and o rounded to fp16), keys and values under a
  * power of two for each 64 tokens (positions 64 j to 64 j + 63), so that any magnitude fits but

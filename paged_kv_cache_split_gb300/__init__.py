@@ -303,7 +303,7 @@ class Pool:
         _check(st, "pool_create")
         self._h = h
         self._ws = {}
-        self._ws_bytes = {}  # workspace sizes of the latent calls by their arguments
+        self._ws_bytes = {}  # workspace sizes of the latent and tree calls by their arguments
         self._latent_dims = (head_dim, int(group_size)) if self.format == "latent" else None
         self._device = _torch().cuda.current_device()
         s = self.stats()

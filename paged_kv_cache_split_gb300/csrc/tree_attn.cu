@@ -144,6 +144,8 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& a) {
   P.tile_rows = g.tile_rows;
   P.n_rt = g.n_rt;
   P.rec_rows = g.rec_rows;
+  P.cols = a.ctas >= a.lv.hkv ? a.lv.hkv : 1;
+  P.col_ctas = a.ctas / P.cols;
   P.words = (a.n_q + 31) / 32;
   P.group_log = a.group == kGroupWide ? 6 : 5;
   P.meta = reinterpret_cast<int2*>(a.ws);

@@ -28,9 +28,12 @@
 // the tile's sum again.  Any magnitudes fit; within a tile, what is 2^-27 of the largest and less
 // loses bits.  (Powers by token took 48 loads a row and tile in the softmax: three times its time.)
 //
-// The key tiles of all units (sequence, kv head, 128 or 256 rows) are laid end to end and split
-// evenly in cost over the CTAs, one a SM.  A unit inside one CTA's share is written directly; a
-// split one leaves FP32 records that a second kernel merges in order.
+// Every kv head has a column of CTAs, one CTA a SM.  The key tiles of a head's units (sequence, 128 or
+// 256 rows) are laid end to end and split evenly in cost over its column, so that the columns pass
+// the same tokens at about the same time: a packed head's row of a token is 16 to 128 bytes of
+// lines that the other heads share (8 x 16384 tokens in K4/V4: 477 MB read from DRAM with one
+// column for all heads, 204 MB, what is stored, with one each).  A unit inside one CTA's share is
+// written directly; a split one leaves FP32 records that a second kernel merges in order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -100,6 +103,8 @@ struct Params {
   int tile_rows; // rows a unit
   int n_rt;      // units a (sequence, kv head)
   int rec_rows;  // rows a record
+  int cols;      // columns of CTAs: a kv head's each, or one for all (fewer CTAs than heads)
+  int col_ctas;  // CTAs a column
   int words;     // mask words a query
   int group_log; // packed: log2 of the values a group
   int2* meta;    // [B * hkv * n_rt]: first CTA of a split unit (-1: written directly), last CTA
@@ -112,9 +117,9 @@ __device__ __forceinline__ int32_t length(const Params& P, int b) {
   return draft_ctx(P.a.ctx[b], (int64_t)P.a.max_blocks * kBlockTokens, P.a.n_q, &bad);
 }
 
-// A CTA's share of the tiles: a unit of n tiles costs kCost n + kSegCost, its tile k sits at
-// kSegCost + kCost k from its start, and CTA g holds the positions [g V, (g + 1) V).  V is at
-// least kCost, so the CTAs that hold a unit's tiles are consecutive.
+// A CTA's share of its column's tiles: a unit of n tiles costs kCost n + kSegCost, its tile k sits
+// at kSegCost + kCost k from its start, and the column's CTA g holds the positions [g V, (g + 1) V).
+// V is at least kCost, so the CTAs that hold a unit's tiles are consecutive.
 struct Segment {
   int b, len, x;    // sequence, its length, unit within it: kv head * n_rt + group of rows
   int k0, k1, n;    // this CTA's tiles of it, and all of them
@@ -122,19 +127,20 @@ struct Segment {
 
 struct Walk {
   int b, x;
+  int x0;          // the column's first unit of a sequence
   int64_t at;      // position of sequence b's first unit
   int64_t lo, hi;  // positions of this CTA
 
   // Warp-uniform values, known as such: copies and MMAs are issued with what follows from them.
   __device__ __forceinline__ bool next(const Params& P, Segment& s) {
-    const int upb = P.a.lv.hkv * P.n_rt;
+    const int upb = P.a.lv.hkv / P.cols * P.n_rt;
     while (b < P.a.B) {
       const int len = uniform(length(P, b));
       const int n = (len + kTile - 1) / kTile;
       const int64_t cost = n > 0 ? (int64_t)kCost * n + kSegCost : 0;
       const int64_t first = at + x * cost + kSegCost;  // position of the unit's first tile
       if (n > 0 && first >= hi) return false;
-      s.b = b, s.len = len, s.n = n, s.x = x;
+      s.b = b, s.len = len, s.n = n, s.x = x0 + x;
       if (n == 0 || ++x == upb) {
         at += upb * cost;
         x = 0;
@@ -155,7 +161,8 @@ struct Walk {
 __device__ __forceinline__ Walk start_walk(const Params& P) {
   constexpr int kHeld = 128;  // sequences whose lengths are read once
   const int lane = threadIdx.x & 31;
-  const int64_t upb = (int64_t)P.a.lv.hkv * P.n_rt;
+  const int64_t upb = (int64_t)(P.a.lv.hkv / P.cols) * P.n_rt;
+  const int col = (int)blockIdx.x / P.col_ctas, g = (int)blockIdx.x % P.col_ctas;
   auto cost = [&](int b) -> int64_t {
     if (b >= P.a.B) return 0;
     const int n = (length(P, b) + kTile - 1) / kTile;
@@ -171,12 +178,13 @@ __device__ __forceinline__ Walk start_walk(const Params& P) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   Walk w;
-  const int64_t v = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t v = (total + P.col_ctas - 1) / P.col_ctas;
   const int64_t V = v > kCost ? v : kCost;
-  w.lo = blockIdx.x * V;
+  w.lo = g * V;
   w.hi = w.lo + V;
   w.b = P.a.B;
   w.x = 0;
+  w.x0 = (int)(col * upb);
   w.at = total;
   int64_t carry = 0;
   // the first sequence that ends past the CTA's first position
@@ -566,7 +574,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
   const uint32_t tmem = uniform(sm.tmem);
   auto tm_s = [&](int t, int buf) { return tmem + (t * 2 + buf) * kTile; };
   auto tm_o = [&](int t) { return tmem + 256 + t * D; };
-  Walk walk = {uniform(sm.walk.b), uniform(sm.walk.x), uniform(sm.walk.at), uniform(sm.walk.lo), uniform(sm.walk.hi)};
+  Walk walk = {uniform(sm.walk.b), uniform(sm.walk.x), uniform(sm.walk.x0), uniform(sm.walk.at), uniform(sm.walk.lo), uniform(sm.walk.hi)};
   Segment seg;
   // Which warpgroups work on tile `it` (counted over the CTA's segments) of a unit with nrow rows
   auto works = [&](int t, int it, int nrow) {
@@ -1079,7 +1087,7 @@ cudaError_t launch(const Params& P) {
     if (!regs_ok) return cudaErrorInvalidDeviceFunction;
   }
   static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is set
-  return tc_launch(tree_attn_kernel<D, MODE, KB, VB>, dim3((unsigned)P.a.ctas), L::kThreads, (size_t)L::kSmem, P.a.stream, P,
+  return tc_launch(tree_attn_kernel<D, MODE, KB, VB>, dim3((unsigned)(P.cols * P.col_ctas)), L::kThreads, (size_t)L::kSmem, P.a.stream, P,
                    P.a.device, &raised);
 }
 
