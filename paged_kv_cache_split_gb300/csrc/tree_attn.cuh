@@ -21,7 +21,7 @@
 //
 // bf16 keys and values go from the pool to swizzled operand tiles by 16-byte asynchronous
 // copies, which fill tokens that nobody sees (past the length, unused drafts) with zeros: a
-// stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by eight warps, a
+// stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by twelve warps, a
 // tile's keys and its values each under the power of two that puts the largest near 2^13.  The
 // keys' power goes back into the logits.  The values' e goes into the probabilities' exponent,
 // P[t] = exp2(x[t] + e - m), so that O needs nothing (the reference follows x + e), and comes off
@@ -56,12 +56,12 @@ constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the 
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
 constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
 constexpr int kAtRing = 8;              // packed: tiles that the scout runs ahead
-constexpr int kPowRing = 8;             // packed: tiles whose powers are held
+constexpr int kPowRing = 12;            // packed: tiles whose powers are held
 
-// Packed: the five warpgroups share the launch's registers, 2 x 136 + 40 + 2 x 80 <= 5 x 96 (the
-// launcher checks that the kernel was built with 96).  Their paths do not rejoin: each ends in a
-// return.
-constexpr int kLaunchRegs = 96;
+// Packed: the six warpgroups share the launch's registers, 2 x 112 + 40 + 3 x 72 = 6 x 80 (the
+// launcher checks that the kernel was built with 80).  Their paths do not rejoin: each ends in a
+// return.  (120 and 64 for softmax and feeders, or 128 and 56, are no faster.)
+constexpr int kLaunchRegs = 80;
 
 // Cost of a unit's start in the split over the CTAs, in quarter tiles: its queries are loaded
 // and its output or record written.  (4, 7, 10 tiles: 4 x 16384, 64 drafts 58.1, 56.1, 56.6 us;
@@ -72,22 +72,22 @@ constexpr int kCost = 4;
 template <int D, int MODE, int KB, int VB>
 struct Plan {
   static constexpr bool PACKED = KB < 16;
-  // Packed: two warpgroups of feeders (warp 11 fills the MMA warps'), in teams that take tiles in
+  // Packed: three warpgroups of feeders (warp 11 fills the MMA warps'), in teams that take tiles in
   // turns, so that one team's loads and waits lie under the others' work.  A warp then has (KB +
-  // VB) / 2 pieces of a tile, at most eight in registers, whatever D (two teams instead of one
-  // took 8 x 16384 tokens in K4/V4 from 188 to 155 us at D = 128, four instead of two from 134 to
-  // 126 us the other way; K8/V8 at D = 64 80 -> 74 us with four).
-  static constexpr int kWarps = PACKED ? 8 : 2;  // (bf16: 12 warps in all, 168 registers a thread)
+  // VB) / 2 pieces of a tile in registers (D = 256, one team: a third less), eight at most.  Two
+  // teams instead of one took 8 x 16384 tokens in K4/V4 from 188 to 155 us; three warpgroups
+  // instead of two from 123 to 108, 16 x 6000 in K8/V8 with heads of 64 from 79 to 72.
+  static constexpr int kWarps = PACKED ? 12 : 2;  // (bf16: 12 warps in all, 168 registers a thread)
   static constexpr int kFeeders = kWarps * 32;
-  static constexpr int kTeams = PACKED ? 256 / D : 1;
+  static constexpr int kTeams = !PACKED || D == 256 ? 1 : 384 / D;
   static constexpr int kTeam = kFeeders / kTeams;  // threads that bring a tile
   static constexpr int kFeeder0 = PACKED ? 384 : 320;  // the first feeder thread
   static constexpr int kThreads = kFeeder0 + kFeeders;
   static constexpr int kTileRows = MODE == kPair ? 2 * kRows : kRows;  // rows a unit
   static constexpr int kQBytes = kTileRows * D * 2;
   static constexpr int kSlot = kTile * D * 2;
-  static constexpr int kK = D == 256 ? 2 : PACKED ? 4 : D == 64 ? 8 : 5;
-  static constexpr int kV = D == 256 ? 2 : PACKED || D == 128 ? 4 : 8;
+  static constexpr int kK = D == 256 ? 2 : D == 64 ? 8 : PACKED ? 4 : 5;
+  static constexpr int kV = D == 256 ? 2 : D == 128 ? 4 : 8;
   static constexpr int kSmall = 12 * 1024;
   static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kSlot + kSmall;
   static_assert(kSmem <= kSmemLimit, "shared memory");
@@ -238,7 +238,7 @@ struct Small {
   // its values were divided by, and the inverse of that.
   alignas(16) float4 pow[kPowRing];
   Place at[kAtRing];           // packed
-  float2 widest[4][2][8];      // by team, parity of its tile and warp: largest key and value
+  float2 widest[6][2][12];      // by team, parity of its tile and warp: largest key and value
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t policy) {
@@ -387,7 +387,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
 #pragma unroll
     for (int e = 0; e < E; ++e) sign[e] = P.a.signs[lane * E + e] * (D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f);
   }
-  constexpr int U = D == 256 ? 8 : 16;  // rows in flight
+  constexpr int U = D == 256 || PACKED ? 8 : 16;  // rows in flight
   for (int rb = warp; rb < nrow; rb += 8 * U) {
     uint32_t w[U][E / 2];
 #pragma unroll
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    if constexpr (PACKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int tr = (warp & 3) * 32 + lane;  // row of the tile
@@ -987,7 +987,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // --------------------------------------------------------------- expansion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const LayerView& lv = P.a.lv;
     const uint32_t slab_rows = (uint32_t)(lv.slab_blocks * kBlockTokens * lv.hkv);
     const uint32_t v_off = slab_rows * lv.row_bytes[0], km_off = v_off + slab_rows * lv.row_bytes[1],
