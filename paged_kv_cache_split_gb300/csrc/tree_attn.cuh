@@ -30,8 +30,8 @@
 //
 // Every kv head has a column of CTAs, one CTA a SM.  The key tiles of a head's units (sequence, 128 or
 // 256 rows) are laid end to end and split evenly in cost over its column, so that the columns pass
-// the same tokens at about the same time: a packed head's row of a token is 16 to 128 bytes of
-// lines that the other heads share (8 x 16384 tokens in K4/V4: 477 MB read from DRAM with one
+// the same tokens at about the same time: a packed head's row of a token is often less than a
+// line, which the other heads share (8 x 16384 tokens in K4/V4: 477 MB read from DRAM with one
 // column for all heads, 204 MB, what is stored, with one each).  A unit inside one CTA's share is
 // written directly; a split one leaves FP32 records that a second kernel merges in order.
 #pragma once
@@ -94,6 +94,9 @@ struct Plan {
   // A tile's powers are overwritten kPowRing tiles later: its keys' slot was freed then by the S of
   // the tile kPowRing - kK later, which waited for the values of the tile four before it at least.
   static_assert(!PACKED || kK + 4 <= kPowRing, "powers are read until the softmax is done");
+  // A slot's barrier is waited on by parity: a team that comes to tile t knows by its last one, t -
+  // kTeams, that the slot's use before the last, t - 2 kK, is over, so that the parity is not stale.
+  static_assert(kTeams <= kK && kTeams <= kV && kTeams <= kAtRing, "a team a ring ahead");
 };
 
 struct Params {
