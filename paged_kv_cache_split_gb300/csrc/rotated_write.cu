@@ -15,6 +15,11 @@
 // 16 bits relative to the row's largest value, whose sums FP32 holds exactly, and the
 // rest.  That carries 40 bits relative to the largest value at twice the FP32 additions;
 // FP64 (2 lanes a cycle and SM) would take thirty times as long.
+//
+// Measured on one GB300: 16384 tokens of 8 kv and 32 query heads of 128, half of each turned, norms, bf16
+// 71 us, 5.7 TB/s (HBM); 5001 tokens, heads of 64, 11.1 us, 5.7 TB/s; 8 tokens 3.1 us (latency); 1512 tokens into a
+// K4/V4 pool 11.0 us, 16384 107 us: 3 and 3.1 times the bytes' time, the butterflies' and quantiser's
+// instructions (issue 64% active).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
