@@ -38,8 +38,9 @@
 // Measured on one GB300, with the merge, in a stream of calls: 16 trees of 64 drafts behind 16384 tokens
 // (bf16, 16 of 8 heads of 128) 183 to 187 us, 5.8 to 5.9 TB/s: HBM.  4 of the same 57 us: of it 4.5 are the start
 // (walk, block rows, queries), 6 the last tiles and the merge.  8 trees of 24 behind 16384 in K4/V4 108 us,
-// 1.9 TB/s: the feeders' loads and expansion (85 us without either of them), then the chain S, softmax, O
-// of a tile (64 us without the softmax).  1 tree of 8 behind 1000: 11.8 us, latency.
+// 1.9 TB/s: the feeders' loads and expansion (85 us without either of them, 75 without both), then the
+// hand-over of a tile from copies to S, softmax and O (64 us without the softmax's work besides).  1 tree of 8
+// behind 1000: 11.8 us, latency.
 #pragma once
 
 #include <cuda_bf16.h>
