@@ -36,11 +36,11 @@
 // written directly; a split one leaves FP32 records that a second kernel merges in order.
 //
 // Measured on one GB300, with the merge, in a stream of calls: 16 trees of 64 drafts behind 16384 tokens
-// (bf16, 16 of 8 heads of 128) 183 to 187 us, 5.8 to 5.9 TB/s: HBM.  4 of the same 57 us: of it 4.5 are the start
-// (walk, block rows, queries), 6 the last tiles and the merge.  8 trees of 24 behind 16384 in K4/V4 108 us,
-// 1.9 TB/s: the feeders' loads and expansion (85 us without either of them, 75 without both), then the
-// hand-over of a tile from copies to S, softmax and O (64 us without the softmax's work besides).  1 tree of 8
-// behind 1000: 11.8 us, latency.
+// (bf16, 16 of 8 heads of 128) 183 to 187 us, 5.8 to 5.9 TB/s: HBM.  16 trees of 13, 32 of 8 heads of 64, behind 2048,
+// 4096, 8192 tokens: 25.5, 38.2, 62.0 us: 5.6 TB/s from length to length, and 14 us for what does not hang on it: the
+// start (walk, block rows, queries), the last tiles, the records and their merge.  8 trees of 24 behind 2048, 8192, 16384
+// in K4/V4: 29.8, 65.1, 107.9 us, 0.8 us a tile and CTA: the feeders' loads and expansion (16384: 85 us
+// without either of them, 75 without both).  1 tree of 8 behind 1000: 11.8 us, latency.
 #pragma once
 
 #include <cuda_bf16.h>
