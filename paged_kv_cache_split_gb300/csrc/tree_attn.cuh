@@ -243,7 +243,9 @@ struct Small {
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
   float m[2][kRows], l[2][kRows];  // the warpgroups' references and sums of shared rows
-  float q_pow[2 * kRows];      // packed: the power of two that a row's query was divided by
+  // Packed: the power of two that a row's query was divided by, for every other segment: a
+  // warpgroup may load the next segment's queries before the other has read this one's powers.
+  float q_pow[2][2 * kRows];
   // Packed, by tile: scale times the power of two that its keys were divided by, log2 of the one
   // its values were divided by, and the inverse of that.
   alignas(16) float4 pow[kPowRing];
@@ -387,7 +389,7 @@ __host__ __device__ constexpr int octet_column(int c) { return (c & ~7) | (c & 3
 // Queries of a unit's rows into shared memory, a row a warp at a time; packed: into the keys'
 // basis, under a power of two in fp16.
 template <int D, int KB>
-__device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, Small& sm, int row0, int nrow) {
+__device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, float* q_pow, int row0, int nrow) {
   constexpr int E = D / 32;
   constexpr bool PACKED = KB < 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -451,7 +453,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
         const float f = pow2(-ex);
 #pragma unroll
         for (int e = 0; e < E; e += 2) w[u][e / 2] = fp16x2(x[e] * f, x[e + 1] * f);
-        if (lane == 0) sm.q_pow[r] = pow2(ex);
+        if (lane == 0) q_pow[r] = pow2(ex);
         if constexpr (KB == 4) octets<E>(w[u]);
       }
       const int byte = lane * E * 2, tile = r / kRows, rr = r % kRows;
@@ -603,17 +605,18 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = min(L::kTileRows, P.rows - row0);
       const int kvh = seg.x / P.n_rt;
       if (n_seg > 0) wait_or_die(&sm.q_empty, (n_seg - 1) & 1, dead, err);
-      load_queries<D, KB>(P, seg, qs, sm, row0, nrow);
+      float* q_pow = sm.q_pow[n_seg & 1];  // (read for the last time before the barrier of the segment in between)
+      load_queries<D, KB>(P, seg, qs, q_pow, row0, nrow);
       fence_async_shared();
       mbar_arrive(&sm.q_full);
       __syncwarp();
-      named_barrier_sync(1, kSoftmaxThreads);  // q_pow is written; the segment before is read
+      named_barrier_sync(1, kSoftmaxThreads);  // q_pow is written; where both O are read by both, that is done
       ++n_seg;
       const int rr = MODE == kPair ? t * kRows + tr : tr;  // row of the unit
       const bool mine = rr < nrow;
       const bool idle = (MODE == kPair ? t * kRows : 0) + (warp & 3) * 32 >= nrow;  // a warp without rows
       const int r = row0 + (mine ? rr : 0);
-      const float qp = PACKED && mine ? sm.q_pow[rr] : 1.f;
+      const float qp = PACKED && mine ? q_pow[rr] : 1.f;
       float m = kNoMax;
       uint64_t l = 0;  // two partial sums
       const int before = jobs;

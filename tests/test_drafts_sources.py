@@ -46,3 +46,16 @@ def test_whole_warps_meet_the_tensor_memory_loads():
         synced = max(before.rfind(x) for x in ("__syncwarp()", "wait_or_die(", "tc_wait_ld()", "tc_wait_st()"))
         lanes = max(before.rfind(x) for x in ("if (mine", "if (lane", "threadIdx.x == 0"))
         assert synced > lanes, body[m.start() - 200:m.end()]
+
+
+def test_the_powers_of_two_segments_queries_lie_apart():
+    """With more than 128 rows a warpgroup's part of a segment of few tiles hangs on nothing that the
+    other does: it may load the next segment's queries before the other has read the powers of this
+    one.  Two copies in turns are enough: a barrier lies in every segment."""
+    text = sources()["tree_attn.cuh"]
+    assert re.search(r"float q_pow\[2\]\[2 \* kRows\];", text)
+    uses = re.findall(r"sm\.q_pow\b[^;,]*", text)
+    assert uses and all(u.startswith("sm.q_pow[n_seg & 1]") for u in uses), uses
+    body = text[text.index("load_queries<D, KB>(P"):]
+    body = body[:body.index("q_pow[rr]")]
+    assert body.index("named_barrier_sync(1, kSoftmaxThreads)") < body.index("++n_seg")
