@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
                   for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
                   tc_st_rows<32>(tm_o(t) + 32 * k + lanes, o);
                 }
+                tc_wait_st();  // the tile's other half may load these columns again
               }
               if (q > 0) {
                 // the tile's first half is written: f is a power of two, which P takes exactly

@@ -59,3 +59,22 @@ def test_the_powers_of_two_segments_queries_lie_apart():
     body = text[text.index("load_queries<D, KB>(P"):]
     body = body[:body.index("q_pow[rr]")]
     assert body.index("named_barrier_sync(1, kSoftmaxThreads)") < body.index("++n_seg")
+
+
+def block(text, head):
+    """The braces that follow the first `head` in text, and what lies between them."""
+    at = text.index("{", text.index(head))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+    raise AssertionError(head)
+
+
+def test_a_rescaled_output_is_stored_before_it_is_loaded_again():
+    """Both halves of a tile may rescale O.  Stores to tensor memory are not ordered before later
+    loads of the same columns without a wait for them, so the rescaling itself ends in one."""
+    body = block(sources()["tree_attn.cuh"], "if (job > before)")
+    assert "tc_ld_rows<32>(tm_o(t)" in body
+    assert "tc_wait_st()" in body[body.index("tc_st_rows<32>(tm_o(t)"):]
