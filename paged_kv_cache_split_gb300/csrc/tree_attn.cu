@@ -6,11 +6,15 @@ namespace pkv {
 namespace tree {
 namespace {
 
-// Merge of the records of split units, in order: a warp takes 4 V columns of 32 rows, a lane a
-// row of them.  Also the zero rows of unused or bad sequences.  U records are in flight: few
-// units over many CTAs leave many records each, whose latency counts (U = 16, V = 1: 8 units with
-// 19 records 26.9 us a call against 28.6), many units many warps (U = 8, V = 2: 128 units of 128
-// rows 185 us against 191).
+// A sum is below 2^kSlack times 2^25 tokens: under this the weights sum to less than 1, so that the
+// values' weighted sum is no larger than they are.
+constexpr float kWeight = 5.8207660913467407e-11f;  // 2^-34
+
+// Merge of the records of split units, in order: a record's output counts by exp2(m) times its sum.  A
+// warp takes 4 V columns of 32 rows, a lane a row of them.  Also the zero rows of unused or bad
+// sequences.  U records are in flight: few units over many CTAs leave many records each, whose latency
+// counts (U = 16, V = 1: 8 units with 19 records 26.9 us a call against 28.6), many units many warps
+// (U = 8, V = 2: 128 units of 128 rows 185 us against 191).
 template <int D, int U, int V>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ Params P, int row_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -64,8 +68,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
         for (int e = 0; e < 4 * V; ++e) o[e] *= f;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const float w = ex2(ml[k].x - m);
-          sum = fmaf(w, ml[k].y, sum);
+          const float w = ex2(ml[k].x - m) * ml[k].y * kWeight;
+          sum += w;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             o[4 * e] = fmaf(w, v[k][e].x, o[4 * e]);

@@ -24,9 +24,13 @@
 // stale NaN reaches neither product.  Packed ones are expanded to fp16 operands by twelve warps, a
 // tile's keys and its values each under the power of two that puts the largest near 2^13.  The
 // keys' power goes back into the logits.  The values' e goes into the probabilities' exponent,
-// P[t] = exp2(x[t] + e - m), so that O needs nothing (the reference follows x + e), and comes off
-// the tile's sum again.  Any magnitudes fit; within a tile, what is 2^-27 of the largest and less
-// loses bits.  (Powers by token took 48 loads a row and tile in the softmax: three times its time.)
+//   P[t] = exp2(x[t] - m + c),   c = max(e - u, -64),
+// so that O needs nothing: u, an integer, is O's power of two beside 2^m and follows x + e - m as m follows
+// x.  The sum is of the x alone: it takes a tile's P times 2^-c.  (A P that the 64 raises is below
+// 2^-56 all the same and 0 in fp16, while its share of the sum stays what it is.)  A reference from 2^22 on comes
+// off first, which is exact where x is near it; below, c - m is.  Any magnitudes fit; within a tile,
+// what is 2^-27 of the largest and less loses bits.  (Powers by token took 48 loads a row and tile in the softmax:
+// three times its time.)
 //
 // Every kv head has a column of CTAs, one CTA a SM.  The key tiles of a head's units (sequence, 128 or
 // 256 rows) are laid end to end and split evenly in cost over its column, so that the columns pass
@@ -61,6 +65,8 @@ constexpr int kRows = 128;              // rows a tile of rows
 constexpr int kSoftmaxThreads = 256;
 constexpr float kSlack = 8.0f;          // log2 of how far a logit may pass the reference
 constexpr float kNoMax = -3.402823466e38f;  // the reference before any visible token: no logit is below it
+constexpr float kExact = 4194304.0f;    // 2^22: whole numbers up to twice that are exact in fp32, with c's 2^8 among them
+constexpr float kLeast = -64.0f;        // packed: no probability is lifted by less (2^(kSlack - 64) is 0 in fp16)
 constexpr int kSmemLimit = 232448;      // 227 KB opt-in shared memory per block
 constexpr int kAtRing = 8;              // packed: tiles that the scout runs ahead
 constexpr int kPowRing = 12;            // packed: tiles whose powers are held
@@ -119,7 +125,7 @@ struct Params {
   int group_log; // packed: log2 of the values a group
   int2* meta;    // [B * hkv * n_rt]: first CTA of a split unit (-1: written directly), last CTA
   float2* ml;    // [2 * grid][rec_rows]: reference and sum of a record's rows
-  float* acc;    // [2 * grid][D / 4][rec_rows][4]: lanes, which own rows, store and load whole lines
+  float* acc;    // [2 * grid][D / 4][rec_rows][4], over the sums: lanes, which own rows, store and load whole lines
 };
 
 __device__ __forceinline__ int32_t length(const Params& P, int b) {
@@ -242,13 +248,13 @@ struct Small {
   Walk walk;
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
-  float m[2][kRows], l[2][kRows];  // the warpgroups' references and sums of shared rows
+  float m[2][kRows], u[2][kRows], l[2][kRows];  // the warpgroups' references, O's powers and sums of shared rows
   // Packed: the power of two that a row's query was divided by, for every other segment: a
   // warpgroup may load the next segment's queries before the other has read this one's powers.
   float q_pow[2][2 * kRows];
-  // Packed, by tile: scale times the power of two that its keys were divided by, log2 of the one
-  // its values were divided by, and the inverse of that.
-  alignas(16) float4 pow[kPowRing];
+  // Packed, by tile: scale times the power of two that its keys were divided by, and log2 of the
+  // one its values were divided by.
+  alignas(8) float2 pow[kPowRing];
   Place at[kAtRing];           // packed
   float2 widest[6][2][12];      // by team, parity of its tile and warp: largest key and value
 };
@@ -617,8 +623,9 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const bool idle = (MODE == kPair ? t * kRows : 0) + (warp & 3) * 32 >= nrow;  // a warp without rows
       const int r = row0 + (mine ? rr : 0);
       const float qp = PACKED && mine ? q_pow[rr] : 1.f;
-      float m = kNoMax;
-      uint64_t l = 0;  // two partial sums
+      float m = kNoMax, up = 0.f;  // O is in units of 2^(m + up)
+      float slack = kSlack;  // (packed: none for a reference from kExact on)
+      uint64_t l = 0;  // two partial sums, in units of 2^m
       const int before = jobs;
       int it = it0;
       for (int u = seg.k0; u < seg.k1; ++u, ++it) {
@@ -627,15 +634,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         wait_or_die(&sm.s_full[t][buf], (job >> 1) & 1, dead, err);
         if (!idle) {
           tc_fence_after();
-          // Logits are in units of scale (times the row's and the tile's powers); packed: m is the
-          // reference of x + lift.
-          float sc = P.a.scale_log2, lift = 0.f, back = 1.f;
+          // Logits are in units of scale (times the row's and the tile's powers).
+          float sc = P.a.scale_log2, lift = 0.f;
           if constexpr (PACKED) {
-            const float4 f = sm.pow[it % kPowRing];
-            sc = f.x * qp, lift = f.y, back = f.z;
+            const float2 f = sm.pow[it % kPowRing];
+            sc = f.x * qp, lift = f.y;
           }
           const uint64_t sc2 = pair2(sc, sc);
-          uint64_t sum = 0;
           // 32 tokens at a time: 64 logits would not fit the registers beside the rest.
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
@@ -665,13 +670,26 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[28 + e]);
             // rows past the unit's hold anything: they must not move the references of this warp's others
-            const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) + lift : -INFINITY;
-            if (__any_sync(0xffffffffu, top - m > kSlack)) {
-              const float mn = fmaxf(m, rintf(top));
-              const float f = ex2(m - mn);
-              m = mn;
+            const float top = mine ? fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) : -INFINITY;
+            float from = m;
+            if (__any_sync(0xffffffffu, top - m > slack || (PACKED && top - m + lift - up > kSlack))) {
+              const float mn = fmaxf(m, rintf(top)), fell = m - mn;
+              float f = ex2(fell);
               l = mul2(l, pair2(f, f));
-              sum = mul2(sum, pair2(f, f));
+              if constexpr (PACKED) {
+                const float was = up + fell;
+                up = fmaxf(was, rintf(top - mn + lift));
+                f = ex2(was - up);
+              }
+              from = m = mn;
+              if constexpr (PACKED) {
+                // A reference that c - m would round comes off first (and from now on in every half).
+                const bool far = fabsf(m) >= kExact && m != kNoMax;
+                slack = far ? -INFINITY : kSlack;
+                from = far ? 0.f : m;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) split2(add2(pair2(x[i], x[i + 1]), pair2(from - m, from - m)), x[i], x[i + 1]);
+              }
               if (job > before) {
                 wait_or_die(&sm.pv_done[t][(job - 1) & 1], ((job - 1) >> 1) & 1, dead, err);
                 tc_fence_after();
@@ -707,24 +725,30 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
               }
             }
             __syncwarp();
-            const uint64_t mm = pair2(lift - m, lift - m);
-            uint64_t other = 0;
+            const float c = PACKED ? fmaxf(lift - up, kLeast) : 0.f;
+            const uint64_t mm = pair2(c - from, c - from);
+            uint64_t sum = 0, other = 0;
             uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
+            for (int i = 0; i < 16; i += 2) {
               float e0, e1, e2, e3;
-              split2(add2(pair2(x[2 * c], x[2 * c + 1]), mm), e0, e1);
-              split2(add2(pair2(x[2 * c + 2], x[2 * c + 3]), mm), e2, e3);
+              split2(add2(pair2(x[2 * i], x[2 * i + 1]), mm), e0, e1);
+              split2(add2(pair2(x[2 * i + 2], x[2 * i + 3]), mm), e2, e3);
               e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
               sum = add2(sum, pair2(e0, e1));
               other = add2(other, pair2(e2, e3));
-              w[c] = PACKED ? fp16x2(e0, e1) : bf2(e0, e1);
-              w[c + 1] = PACKED ? fp16x2(e2, e3) : bf2(e2, e3);
+              w[i] = PACKED ? fp16x2(e0, e1) : bf2(e0, e1);
+              w[i + 1] = PACKED ? fp16x2(e2, e3) : bf2(e2, e3);
             }
             sum = add2(sum, other);
+            if constexpr (PACKED) {
+              const float back = ex2(-c);
+              l = fma2(sum, pair2(back, back), l);
+            } else {
+              l = add2(l, sum);
+            }
             tc_st_rows<16>(tm_s(t, buf) + 16 * q + lanes, w);
           }
-          l = PACKED ? fma2(sum, pair2(back, back), l) : add2(l, sum);
           tc_wait_st();
           tc_fence_before();
         }
@@ -738,7 +762,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const int took0 = taken(0), took1 = taken(1);
       others += t ? took0 : took1;
       it0 += n;
-      // Output of the segment: O / sum, or a record (reference, sum, O) to be merged.
+      // Output of the segment: O / sum, or that in a record with the reference and the sum, to be merged.
       const bool whole = seg.k0 == 0 && seg.k1 == seg.n;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (seg.k0 > 0 ? 0 : 1);
       if (threadIdx.x == 0) {
@@ -754,12 +778,18 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       if (shared_rows) {
         sm.m[t][tr] = m;
         sm.l[t][tr] = sum;
+        if constexpr (PACKED) sm.u[t][tr] = up;
         __syncwarp();
         named_barrier_sync(1, kSoftmaxThreads);
         const float m0 = sm.m[0][tr], m1 = sm.m[1][tr];
         m = fmaxf(m0, m1);
         f[0] = ex2(m0 - m), f[1] = ex2(m1 - m);
         sum = f[0] * sm.l[0][tr] + f[1] * sm.l[1][tr];
+        if constexpr (PACKED) {
+          const float u0 = sm.u[0][tr] + (m0 - m), u1 = sm.u[1][tr] + (m1 - m);
+          up = fmaxf(u0, u1);
+          f[0] = ex2(u0 - up), f[1] = ex2(u1 - up);
+        }
       }
       const int64_t rec = slot * P.rec_rows + rr;
       if (!whole && mine && (!shared_rows || t == 0)) P.ml[rec] = make_float2(m, sum);
@@ -769,7 +799,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       if (shared_rows && (t ? took0 : took1) > 0) settled(t ^ 1, others - 1);
       tc_fence_after();
       if (!idle) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum > 0.f ? (PACKED ? ex2(up) : 1.f) / sum : 0.f;
+        f[0] *= inv, f[1] *= inv;
         const int i = r / P.G, g = r - i * P.G;
         uint16_t* out = P.a.out + (((int64_t)seg.b * P.a.n_q + i) * P.a.Hq + kvh * P.G + g) * D;
         float4* acc = reinterpret_cast<float4*>(P.acc) + slot * (D / 4) * P.rec_rows + rr;
@@ -806,8 +837,8 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               reinterpret_cast<uint4*>(out + 32 * q)[c] =
-                  make_uint4(bf2(o[8 * c] * inv, o[8 * c + 1] * inv), bf2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                             bf2(o[8 * c + 4] * inv, o[8 * c + 5] * inv), bf2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+                  make_uint4(bf2(o[8 * c], o[8 * c + 1]), bf2(o[8 * c + 2], o[8 * c + 3]), bf2(o[8 * c + 4], o[8 * c + 5]),
+                             bf2(o[8 * c + 6], o[8 * c + 7]));
           } else if (mine) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -1069,7 +1100,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       for (int i = 0; i < W; ++i) kmax = fmaxf(kmax, all[i].x), vmax = fmaxf(vmax, all[i].y);
       const int kx = power_of(kmax), vx = power_of(vmax);
       const float kf = pow2(-kx), vf = pow2(-vx);
-      if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_float4(P.a.scale_log2 * pow2(kx), (float)vx, vf, 0.f);
+      if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_float2(P.a.scale_log2 * pow2(kx), (float)vx);
 #pragma unroll
       for (int j = 0; j < KN; ++j) {
         const int g = kw + W * j;

@@ -37,3 +37,59 @@ def test_both_halves_of_a_tile_move_the_reference(fmt, D, n_q, Hq, ctas):
     q = way[torch.arange(n_q * Hq, device="cuda") % 7].view(1, n_q, Hq, 1).expand(1, n_q, Hq, D).bfloat16().contiguous()
     run_tree(case, n_q, Hq, seed=n_q, q=q, l2=False)
     assert case.pool.check_errors() == 0
+
+
+def by_tile(powers, zero=()):
+    """Values of each tile of 64 tokens times 2 to the powers, in turns; tiles of `zero` hold none."""
+    def f(k, v):
+        tile = torch.arange(k.shape[0], device="cuda") // 2
+        p = torch.tensor(powers, dtype=torch.float64, device="cuda")[tile % len(powers)]
+        m = torch.where(torch.isin(tile % len(powers), torch.tensor(list(zero), device="cuda")), 0.0, 2.0 ** p)
+        return k, (v.double() * m[:, None, None, None]).float()
+    return f
+
+
+PACKED = [("k4v4", 64), ("k4v4", 128), ("k8v4", 128), ("k8v8", 256), ("k8v8", 64)]
+
+
+@pytest.mark.parametrize("fmt,D", PACKED + [("bf16", 128)])
+@pytest.mark.parametrize("powers,zero", [((0, 40), (0,)), ((60, -60), ()), ((100, 0, -100, 30), ()), ((118, 0), (1,)),
+                                         ((0, 0, 100), (0, 1))])
+@pytest.mark.parametrize("n_q,ctas", [(8, 1), (8, 3), (8, 40), (70, 2)])
+def test_tiles_of_very_different_values(fmt, D, powers, zero, n_q, ctas):
+    """The values' sizes say nothing about a token's weight: tiles of nothing, or of tiny values, keep
+    their share of the softmax beside tiles of huge ones, within a CTA and over several."""
+    if fmt == "bf16" and max(powers) > 110:
+        pytest.skip("O in fp32 does not hold sums of such values")
+    case = Case(fmt, D, 1, [n_q + 700, max(64, n_q), n_q + 129], seed=n_q, shape_kv=by_tile(powers, zero))
+    case.pool.decode_set_ctas(ctas)
+    run_tree(case, n_q, 2, seed=n_q, l2=False)
+    assert case.pool.check_errors() == 0
+
+
+@pytest.mark.parametrize("fmt,D", PACKED)
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 20, -2.0 ** 20, 2.0 ** 40, 2.0 ** 110])
+@pytest.mark.parametrize("ctas", [1, 5])
+def test_equal_logits_of_any_size_weigh_the_same(fmt, D, scale, ctas):
+    """One key for all tokens: whatever the logits' size, each token weighs the same, so the output is
+    the values' mean, in tiles of any values.  Bounds: the output's rounding, a value's 4 h of its group's
+    largest M, P's h, and what fp16 drops of small operands and probabilities (2^-38 and 2^-24 of the
+    largest of a tile, each)."""
+    U, h = 2.0 ** -8, 2.0 ** -11
+
+    def f(k, v):
+        return k[:1, :1].expand_as(k).contiguous(), by_tile((0, 12, -9, 30, 3))(k, v)[1]
+    n_q = 5
+    case = Case(fmt, D, 2, [n_q + 630], seed=3, shape_kv=f)
+    case.pool.decode_set_ctas(ctas)
+    q = torch.randn(1, n_q, 4, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    out = case.pool.paged_tree_attention(0, q, torch.full((n_q, 1), 31, dtype=torch.int32, device="cuda"), case.table, case.ctx,
+                                         scale)[0].double()
+    _, v, _, vm = case.kv(0)
+    L = v.shape[0]
+    for hq in range(4):
+        x, m = v[:, hq // 2], vm[:, hq // 2]
+        top = m.max()
+        tol = U * x.mean(0).abs() + 4 * h * m.mean(0) + h * x.abs().mean(0) + 2 * 2.0 ** -38 * top + 2.0 ** -24 * top
+        err = (out[:, hq] - x.mean(0)).abs()
+        assert (err <= tol).all(), (err / tol).max().item()
