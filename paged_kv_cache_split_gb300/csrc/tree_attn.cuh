@@ -518,12 +518,14 @@ __device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // Codes of a piece as operand pieces in fp16: s c + o, s and o rounded to fp16, one rounding
-// for the rest.  A code under a fitting exponent is 1024 + c (or 64 + c, four bits up), exactly.
+// for the rest.  `s` comes as 2^BITS s, about the group's range, which stays a normal fp16 as long as that does
+// (s itself is 2^BITS smaller: it would lose bits that much earlier), and c as c / 2^BITS: a code under a
+// fitting exponent is 4 + c / 256, 64 + c / 16 or, four bits up, 4 + c / 16, exactly.
 template <int BITS>
 __device__ __forceinline__ void expand(const uint4& code, float s, float o, uint8_t* slot, int token, int value) {
   const uint32_t w[4] = {code.x, code.y, code.z, code.w};
   const __half2 ss = __float2half2_rn(s), oo = __float2half2_rn(o);
-  const __half2 k1024 = half2_of(0x64006400u), k64 = half2_of(0x54005400u);
+  const __half2 k64 = half2_of(0x54005400u), k4 = half2_of(0x44004400u);
   constexpr int N = BITS == 4 ? 4 : 2;  // operand pieces of eight values
 #pragma unroll
   for (int q = 0; q < N; ++q) {
@@ -531,15 +533,15 @@ __device__ __forceinline__ void expand(const uint4& code, float s, float o, uint
     if constexpr (BITS == 4) {
       // pairs (0, 4), (1, 5), (2, 6), (3, 7)
       const uint32_t lo = w[q], hi = w[q] >> 8;
-      out[0] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x000f000fu) | 0x64006400u), k1024), ss, oo));
-      out[1] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x00f000f0u) | 0x54005400u), k64), ss, oo));
-      out[2] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x000f000fu) | 0x64006400u), k1024), ss, oo));
-      out[3] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x00f000f0u) | 0x54005400u), k64), ss, oo));
+      out[0] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x000f000fu) | 0x54005400u), k64), ss, oo));
+      out[1] = bits_of(__hfma2(__hsub2(half2_of((lo & 0x00f000f0u) | 0x44004400u), k4), ss, oo));
+      out[2] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x000f000fu) | 0x54005400u), k64), ss, oo));
+      out[3] = bits_of(__hfma2(__hsub2(half2_of((hi & 0x00f000f0u) | 0x44004400u), k4), ss, oo));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         out[i] = bits_of(__hfma2(
-            __hsub2(half2_of(__byte_perm(w[2 * q + (i >> 1)], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), k1024), ss, oo));
+            __hsub2(half2_of(__byte_perm(w[2 * q + (i >> 1)], 0x44444444u, i & 1 ? 0x4342 : 0x4140)), k4), ss, oo));
     }
     *reinterpret_cast<uint4*>(slot + swizzled(token, value / 8 + q, kTile * 128)) = make_uint4(out[0], out[1], out[2], out[3]);
   }
@@ -1099,13 +1101,13 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
 #pragma unroll
       for (int i = 0; i < W; ++i) kmax = fmaxf(kmax, all[i].x), vmax = fmaxf(vmax, all[i].y);
       const int kx = power_of(kmax), vx = power_of(vmax);
-      const float kf = pow2(-kx), vf = pow2(-vx);
+      const float kf = pow2(-kx), vf = pow2(-vx), ks2 = pow2(KB - kx), vs2 = pow2(VB - vx);
       if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_float2(P.a.scale_log2 * pow2(kx), (float)vx);
 #pragma unroll
       for (int j = 0; j < KN; ++j) {
         const int g = kw + W * j;
         if (KP::kUnits % W && g >= KP::kUnits) continue;
-        expand<KB>(kc[j], km[j].x * kf, km[j].y * kf, ks + kslot * L::kSlot, g * KP::kTokens + kp.token, kp.value);
+        expand<KB>(kc[j], km[j].x * ks2, km[j].y * kf, ks + kslot * L::kSlot, g * KP::kTokens + kp.token, kp.value);
       }
       // (the warps that issue the products order these writes before the products' reads)
       mbar_arrive(&sm.k_full[kslot]);
@@ -1114,7 +1116,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       for (int j = 0; j < VN; ++j) {
         const int g = vw + W * j;
         if (VP::kUnits % W && g >= VP::kUnits) continue;
-        expand<VB>(vc[j], vm[j].x * vf, vm[j].y * vf, vs + vslot * L::kSlot, g * VP::kTokens + vp.token, vp.value);
+        expand<VB>(vc[j], vm[j].x * vs2, vm[j].y * vf, vs + vslot * L::kSlot, g * VP::kTokens + vp.token, vp.value);
       }
       mbar_arrive(&sm.v_full[vslot]);
     }

@@ -4,7 +4,7 @@ import math
 
 import pytest
 
-from tests.test_gpu_drafts import Case, run_tree
+from tests.test_gpu_drafts import Case, basis, run_tree
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -92,4 +92,43 @@ def test_equal_logits_of_any_size_weigh_the_same(fmt, D, scale, ctas):
         top = m.max()
         tol = U * x.mean(0).abs() + 4 * h * m.mean(0) + h * x.abs().mean(0) + 2 * 2.0 ** -38 * top + 2.0 ** -24 * top
         err = (out[:, hq] - x.mean(0)).abs()
+        assert (err <= tol).all(), (err / tol).max().item()
+
+
+@pytest.mark.parametrize("fmt,D,group", [("k4v4", 64, 32), ("k4v4", 128, 32), ("k4v4", 128, 64), ("k8v4", 128, 32),
+                                         ("k8v8", 64, 32), ("k8v8", 128, 32), ("k8v8", 256, 32)])
+@pytest.mark.parametrize("apart", [18, 22, 24, 26])
+@pytest.mark.parametrize("L", [2, 9])
+def test_small_tokens_beside_a_huge_one(fmt, D, group, apart, L):
+    """A drafted token 2^apart larger lies in the tile of the others, seen by one query alone: the other
+    queries keep the accuracy of what they see.  A value s c + o, all three rounded to fp16, is off by
+    4 h of its group's largest M, h = 2^-11, and where they fall below fp16's normal range by 2^-25 each, which is
+    2^-38 of the tile's largest T, of 2^13 at least; the queries by h, the logits' fp32 sums by D 2^-23,
+    P by h and the output by u = 2^-8.  Errors d of the logits count 2 d, as p moves with its sum; a token
+    that is alone has p = 1 whatever its logit."""
+    U, h = 2.0 ** -8, 2.0 ** -11
+    n_q, Hq = 2, 4
+
+    def f(k, v):
+        huge = (torch.arange(k.shape[0] * 32, device="cuda").view(-1, 32, 1, 1) == L - n_q) * (2.0 ** apart - 1) + 1
+        return k * huge, v * huge
+    case = Case(fmt, D, 2, [L], seed=apart, group=group, shape_kv=f)
+    q = torch.randn(1, n_q, Hq, D, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    mask = torch.tensor([[1], [2]], dtype=torch.int32, device="cuda")
+    scale = D ** -0.5
+    out = case.pool.paged_tree_attention(0, q, mask, case.table, case.ctx, scale)[0, 1].double()
+    k, v, km, vm = case.kv(0)
+    see = [t for t in range(L) if t != L - n_q]
+    for hq in range(Hq):
+        kv = hq // 2
+        Tk, Tv = km[:, kv].max(), vm[:, kv].max()
+        K, V, KM, VM = (y[see, kv] for y in (k, v, km, vm))
+        qd = q[0, 1, hq].double() @ basis(D)
+        p = torch.softmax(K @ qd * scale, 0)
+        size = K.abs() @ qd.abs()
+        d = (D * 2.0 ** -23 + h) * size + 4 * h * (KM @ qd.abs()) + 3 * 2.0 ** -38 * Tk * qd.abs().sum()
+        d = d.max() * scale if L > n_q else 0.0
+        ref = p @ V
+        tol = U * ref.abs() + (h + 2 * d) * (p @ V.abs()) + 4 * h * (p @ VM) + 3 * 2.0 ** -38 * Tv
+        err = (out[hq] - ref).abs()
         assert (err <= tol).all(), (err / tol).max().item()
