@@ -686,7 +686,7 @@ class Pool:
 
     def paged_tree_attention(self, layer: int, q, tree_mask, block_table, ctx_lens, scale: float, max_ctx: int = 0,
                              out=None, workspace=None, stream=None):
-        """Attention of each sequence's last n_q tokens, drafted as a tree: q [B, n_q, Hq, D];
+        """Attention of each sequence's last n_q tokens, drafted as a tree: q [B, n_q, Hq, D], contiguous;
         tree_mask int32 [B, n_q, ceil(n_q / 32)], or [n_q, ceil(n_q / 32)] for one tree in all
         sequences (tree_masks makes them from parents).  Query i sees every token before the
         drafted ones and drafted token j where bit j of its mask row is set.  Returns out, shaped

@@ -16,10 +16,12 @@
 // rest.  That carries 40 bits relative to the largest value at twice the FP32 additions;
 // FP64 (2 lanes a cycle and SM) would take thirty times as long.
 //
-// Measured on one GB300: 16384 tokens of 8 kv and 32 query heads of 128, half of each turned, norms, bf16
-// 71 us, 5.7 TB/s (HBM); 5001 tokens, heads of 64, 11.1 us, 5.7 TB/s; 8 tokens 3.1 us (latency); 1512 tokens into a
-// K4/V4 pool 11.0 us, 16384 107 us: 3 and 3.1 times the bytes' time, the butterflies' and quantiser's
-// instructions (issue 64% active).
+// Measured on one GB300, over six sets of buffers in turn (more than L2 holds): 16384 tokens of 8 kv and 32 query
+// heads of 128, half of each turned, norms, bf16 71.5 us, 5.7 TB/s (HBM); 5001 tokens, heads of 64, 15.5 us,
+// 4.1 TB/s (11.2 replayed on one set, whose 63 MB stay in L2); 8 tokens 2.9 us (latency); 1512 tokens into a K4/V4
+// pool 12.3 us (11.0 on one set), 16384 108 us (K8/V4 108, K8/V8 110): 3.8 and 3.1 times the bytes' time.  Issue is 63%
+// active there, with the butterflies and the quantiser; the rest was not taken apart (the stages of shuffles
+// follow one another).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -17,7 +17,7 @@
 //   kTurns  up to 128 rows: the same rows, key tiles in turns, an O each, added at the end
 //   kSolo   head_dim 256 (whose O fills half of tensor memory): one of them takes all
 // S is double-buffered per warpgroup, so that the next product runs under the softmax.  The
-// reference m moves only when a logit passes it by more than 2^8: O is then rescaled.
+// reference m moves only when a logit (in log2 units) passes it by more than 8: O is then rescaled.
 //
 // bf16 keys and values go from the pool to swizzled operand tiles by 16-byte asynchronous
 // copies, which fill tokens that nobody sees (past the length, unused drafts) with zeros: a
@@ -25,7 +25,7 @@
 // tile's keys and its values each under the power of two that puts the largest near 2^13.  The
 // keys' power goes back into the logits.  The values' e goes into the probabilities' exponent,
 //   P[t] = exp2(x[t] - m + c),   c = max(e - u, -64),
-// so that O needs nothing: u, an integer, is O's power of two beside 2^m and follows x + e - m as m follows
+// so that O needs nothing: u (`up`), an integer, is O's power of two beside 2^m and follows x + e - m as m follows
 // x.  The sum is of the x alone: it takes a tile's P times 2^-c.  (A P that the 64 raises is below
 // 2^-56 all the same and 0 in fp16, while its share of the sum stays what it is.)  A reference from 2^22 on comes
 // off first, which is exact where x is near it; below, c - m is.  Any magnitudes fit; within a tile,
@@ -39,12 +39,18 @@
 // column for all heads, 204 MB, what is stored, with one each).  A unit inside one CTA's share is
 // written directly; a split one leaves FP32 records that a second kernel merges in order.
 //
+// P has 16 bits (as its product wants both operands of one type, bf16 or fp16), the sums it is divided by 32: with
+// the output's own rounding the results are off by 0.0023 (bf16) and 0.0019 to 0.0021 (packed) of their size, where
+// the rounding of the output alone is 0.0017.
+//
 // Measured on one GB300, with the merge, in a stream of calls: 16 trees of 64 drafts behind 16384 tokens
-// (bf16, 16 of 8 heads of 128) 183 to 187 us, 5.8 to 5.9 TB/s: HBM.  16 trees of 13, 32 of 8 heads of 64, behind 2048,
-// 4096, 8192 tokens: 25.5, 38.2, 62.0 us: 5.6 TB/s from length to length, and 14 us for what does not hang on it: the
+// (bf16, 16 of 8 heads of 128) 183 to 189 us, 5.7 to 5.9 TB/s: HBM.  16 trees of 13, 32 of 8 heads of 64, behind 2048,
+// 4096, 8192 tokens: 25.0, 37.6, 61.5 us: 5.6 TB/s from length to length, and 14 us for what does not hang on it: the
 // start (walk, block rows, queries), the last tiles, the records and their merge.  8 trees of 24 behind 2048, 8192, 16384
-// in K4/V4: 29.8, 65.1, 107.9 us, 0.8 us a tile and CTA: the feeders' loads and expansion (16384: 85 us
-// without either of them, 75 without both).  1 tree of 8 behind 1000: 11.8 us, latency.
+// in K4/V4: 30.2, 65.1, 108.6 us, 0.8 us a tile and CTA: the hand-over of tiles and the feeders' loads and expansion
+// (16384: 85 us without either of the latter, 75 without both).  1 tree of 8 behind 1000: 11.7 us, latency.
+// More than 128 rows: 4 trees behind 16384, 100 drafts of 2 heads 69 us, 64 drafts of 4 heads 71, of 8 heads (two
+// units) 125, where the bytes take 40 and the operations 28, 35 and 71.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -248,7 +254,7 @@ struct Small {
   Walk walk;
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
-  float m[2][kRows], u[2][kRows], l[2][kRows];  // the warpgroups' references, O's powers and sums of shared rows
+  float m[2][kRows], up[2][kRows], l[2][kRows];  // the warpgroups' references, O's powers and sums of shared rows
   // Packed: the power of two that a row's query was divided by, for every other segment: a
   // warpgroup may load the next segment's queries before the other has read this one's powers.
   float q_pow[2][2 * kRows];
@@ -780,7 +786,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       if (shared_rows) {
         sm.m[t][tr] = m;
         sm.l[t][tr] = sum;
-        if constexpr (PACKED) sm.u[t][tr] = up;
+        if constexpr (PACKED) sm.up[t][tr] = up;
         __syncwarp();
         named_barrier_sync(1, kSoftmaxThreads);
         const float m0 = sm.m[0][tr], m1 = sm.m[1][tr];
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
         f[0] = ex2(m0 - m), f[1] = ex2(m1 - m);
         sum = f[0] * sm.l[0][tr] + f[1] * sm.l[1][tr];
         if constexpr (PACKED) {
-          const float u0 = sm.u[0][tr] + (m0 - m), u1 = sm.u[1][tr] + (m1 - m);
+          const float u0 = sm.up[0][tr] + (m0 - m), u1 = sm.up[1][tr] + (m1 - m);
           up = fmaxf(u0, u1);
           f[0] = ex2(u0 - up), f[1] = ex2(u1 - up);
         }

@@ -132,3 +132,11 @@ def test_small_tokens_beside_a_huge_one(fmt, D, group, apart, L):
         tol = U * ref.abs() + (h + 2 * d) * (p @ V.abs()) + 4 * h * (p @ VM) + 3 * 2.0 ** -38 * Tv
         err = (out[hq] - ref).abs()
         assert (err <= tol).all(), (err / tol).max().item()
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 128), ("k4v4", 64), ("k8v8", 256)])
+@pytest.mark.parametrize("Hk,Hq,n_q", [(1, 128, 5), (1, 1024, 1), (2, 1024, 3)])
+def test_many_query_heads_a_kv_head(fmt, D, Hk, Hq, n_q):
+    case = Case(fmt, D, Hk, [n_q + 100, 0, n_q + 65], seed=Hq)
+    run_tree(case, n_q, Hq, seed=Hq)
+    assert case.pool.check_errors() == 0
