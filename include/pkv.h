@@ -603,8 +603,8 @@ pkv_status pkv_tree_workspace_bytes(const pkv_pool* pool, int B, int n_q, int Hq
  * fp32 (bf16 pools: 2^8 times the sum of a sequence's values' magnitudes has to fit).  A packed pool's keys,
  * values and rotated queries are expanded to fp16 (c s + o with s and o rounded to fp16), keys and
  * values under a power of two for each 64 tokens (positions 64 j to 64 j + 63), so that any magnitude
- * fits, in every 64 another one, but what is below 2^-27 of the largest of its 64 loses bits; the logits
- * times log2(e) are expected to be finite in fp32.  A chain of few drafts in a packed pool goes faster
+ * fits, in every 64 another one, but what is below 2^-27 of the largest of its 64, or below 2^-114, loses
+ * bits; the logits times log2(e) are expected to be finite in fp32.  A chain of few drafts in a packed pool goes faster
  * through pkv_paged_prefill_attention (8 drafts of 16 / 8 heads behind 16 x 16384 tokens in K4/V4: 144 us
  * there, 195 here).  Deterministic.  Limits: B <= 4096, n_q <= 1024, Hq <= 1024 and a multiple of
  * n_kv_heads, B * n_q * Hq <= 2^24, max_blocks <= 2^20, |scale| log2(e) finite in fp32, pointers

@@ -29,7 +29,7 @@
 // x.  The sum is of the x alone: it takes a tile's P times 2^-c.  (A P that the 64 raises is below
 // 2^-56 all the same and 0 in fp16, while its share of the sum stays what it is.)  A reference from 2^22 on comes
 // off first, which is exact where x is near it; below, c - m is.  Any magnitudes fit; within a tile,
-// what is 2^-27 of the largest and less loses bits.  (Powers by token took 48 loads a row and tile in the softmax:
+// what is 2^-27 of the largest and less (or 2^-114) loses bits.  (Powers by token took 48 loads a row and tile in the softmax:
 // three times its time.)
 //
 // Every kv head has a column of CTAs, one CTA a SM.  The key tiles of a head's units (sequence, 128 or
@@ -255,12 +255,11 @@ struct Small {
   uint32_t tmem;
   int dead;                    // a wait gave up: every role runs on without waiting or issuing
   float m[2][kRows], up[2][kRows], l[2][kRows];  // the warpgroups' references, O's powers and sums of shared rows
-  // Packed: the power of two that a row's query was divided by, for every other segment: a
+  // Packed: log2 of the power of two that a row's query was divided by, for every other segment: a
   // warpgroup may load the next segment's queries before the other has read this one's powers.
-  float q_pow[2][2 * kRows];
-  // Packed, by tile: scale times the power of two that its keys were divided by, and log2 of the
-  // one its values were divided by.
-  alignas(8) float2 pow[kPowRing];
+  int q_pow[2][2 * kRows];
+  // Packed, by tile: log2 of the powers of two that its keys and its values were divided by.
+  alignas(8) int2 pow[kPowRing];
   Place at[kAtRing];           // packed
   float2 widest[6][2][12];      // by team, parity of its tile and warp: largest key and value
 };
@@ -401,7 +400,7 @@ __host__ __device__ constexpr int octet_column(int c) { return (c & ~7) | (c & 3
 // Queries of a unit's rows into shared memory, a row a warp at a time; packed: into the keys'
 // basis, under a power of two in fp16.
 template <int D, int KB>
-__device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, float* q_pow, int row0, int nrow) {
+__device__ __forceinline__ void load_queries(const Params& P, const Segment& s, uint8_t* qs, int* q_pow, int row0, int nrow) {
   constexpr int E = D / 32;
   constexpr bool PACKED = KB < 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -465,7 +464,7 @@ __device__ __forceinline__ void load_queries(const Params& P, const Segment& s, 
         const float f = pow2(-ex);
 #pragma unroll
         for (int e = 0; e < E; e += 2) w[u][e / 2] = fp16x2(x[e] * f, x[e + 1] * f);
-        if (lane == 0) q_pow[r] = pow2(ex);
+        if (lane == 0) q_pow[r] = ex;
         if constexpr (KB == 4) octets<E>(w[u]);
       }
       const int byte = lane * E * 2, tile = r / kRows, rr = r % kRows;
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const int row0 = seg.x % P.n_rt * L::kTileRows, nrow = min(L::kTileRows, P.rows - row0);
       const int kvh = seg.x / P.n_rt;
       if (n_seg > 0) wait_or_die(&sm.q_empty, (n_seg - 1) & 1, dead, err);
-      float* q_pow = sm.q_pow[n_seg & 1];  // (read for the last time before the barrier of the segment in between)
+      int* q_pow = sm.q_pow[n_seg & 1];  // (read for the last time before the barrier of the segment in between)
       load_queries<D, KB>(P, seg, qs, q_pow, row0, nrow);
       fence_async_shared();
       mbar_arrive(&sm.q_full);
@@ -630,7 +629,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       const bool mine = rr < nrow;
       const bool idle = (MODE == kPair ? t * kRows : 0) + (warp & 3) * 32 >= nrow;  // a warp without rows
       const int r = row0 + (mine ? rr : 0);
-      const float qp = PACKED && mine ? q_pow[rr] : 1.f;
+      const int qp = PACKED && mine ? q_pow[rr] : 0;
       float m = kNoMax, up = 0.f;  // O is in units of 2^(m + up)
       float slack = kSlack;  // (packed: none for a reference from kExact on)
       uint64_t l = 0;  // two partial sums, in units of 2^m
@@ -645,8 +644,10 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
           // Logits are in units of scale (times the row's and the tile's powers).
           float sc = P.a.scale_log2, lift = 0.f;
           if constexpr (PACKED) {
-            const float2 f = sm.pow[it % kPowRing];
-            sc = f.x * qp, lift = f.y;
+            // (by halves: no product of two of the three leaves fp32's range unless all three do)
+            const int2 f = sm.pow[it % kPowRing];
+            const int e = f.x + qp, half = e >> 1;
+            sc = sc * pow2(half) * pow2(e - half), lift = (float)f.y;
           }
           const uint64_t sc2 = pair2(sc, sc);
           // 32 tokens at a time: 64 logits would not fit the registers beside the rest.
@@ -1108,7 +1109,7 @@ __global__ void __launch_bounds__(Plan<D, MODE, KB, VB>::kThreads, 1) tree_attn_
       for (int i = 0; i < W; ++i) kmax = fmaxf(kmax, all[i].x), vmax = fmaxf(vmax, all[i].y);
       const int kx = power_of(kmax), vx = power_of(vmax);
       const float kf = pow2(-kx), vf = pow2(-vx), ks2 = pow2(KB - kx), vs2 = pow2(VB - vx);
-      if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_float2(P.a.scale_log2 * pow2(kx), (float)vx);
+      if (kw == 0 && lane == 0) sm.pow[it % kPowRing] = make_int2(kx, vx);
 #pragma unroll
       for (int j = 0; j < KN; ++j) {
         const int g = kw + W * j;

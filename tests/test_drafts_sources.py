@@ -53,7 +53,7 @@ def test_the_powers_of_two_segments_queries_lie_apart():
     other does: it may load the next segment's queries before the other has read the powers of this
     one.  Two copies in turns are enough: a barrier lies in every segment."""
     text = sources()["tree_attn.cuh"]
-    assert re.search(r"float q_pow\[2\]\[2 \* kRows\];", text)
+    assert re.search(r"\w+ q_pow\[2\]\[2 \* kRows\];", text)
     uses = re.findall(r"sm\.q_pow\b[^;,]*", text)
     assert uses and all(u.startswith("sm.q_pow[n_seg & 1]") for u in uses), uses
     body = text[text.index("load_queries<D, KB>(P"):]

@@ -140,3 +140,21 @@ def test_many_query_heads_a_kv_head(fmt, D, Hk, Hq, n_q):
     case = Case(fmt, D, Hk, [n_q + 100, 0, n_q + 65], seed=Hq)
     run_tree(case, n_q, Hq, seed=Hq)
     assert case.pool.check_errors() == 0
+
+
+@pytest.mark.parametrize("fmt,D", PACKED)
+@pytest.mark.parametrize("mk,mq,scale", [(114, -100, 2.0 ** 30), (-80, 120, 2.0 ** 40), (-80, 100, -2.0 ** -60), (100, -60, 2.0 ** -100)])
+def test_logits_of_extreme_factors(fmt, D, mk, mq, scale):
+    """Keys, queries and scales whose products two by two leave fp32's range, all three not.  One key for
+    all tokens: the output is the values' mean (bounds as above)."""
+    U, h = 2.0 ** -8, 2.0 ** -11
+    case = Case(fmt, D, 2, [205], seed=3, shape_kv=lambda k, v: ((k[:1, :1] * 2.0 ** mk).expand_as(k).contiguous(), v))
+    q = torch.randn(1, 5, 4, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 2.0 ** mq
+    out = case.pool.paged_tree_attention(0, q.bfloat16(), torch.full((5, 1), 31, dtype=torch.int32, device="cuda"), case.table,
+                                         case.ctx, scale)[0].double()
+    _, v, _, vm = case.kv(0)
+    for hq in range(4):
+        x, m = v[:, hq // 2], vm[:, hq // 2]
+        tol = U * x.mean(0).abs() + 4 * h * m.mean(0) + h * x.abs().mean(0) + 3 * 2.0 ** -38 * m.max() + 2.0 ** -24 * m.max()
+        err = (out[:, hq] - x.mean(0)).abs()
+        assert (err <= tol).all(), (err / tol).max().item()
